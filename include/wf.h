@@ -8,6 +8,13 @@
  *   wf_paged_decode       one query per sequence over its whole cached context
  *   wf_paged_prefill      causal attention of new tokens over prefix + themselves
  *
+ * A step that verifies drafted tokens (speculative decoding with a draft tree) has
+ * three of its own over the same pool:
+ *
+ *   wf_qk_norm_rope_and_cache  per-head norms and rotation of q and k, and the scatter
+ *   wf_paged_tree_decode       attention of every draft over the context and its ancestors
+ *   wf_keep_accepted           the accepted path's rows moved to the front of the drafts
+ *
  * Sources (page title, section):
  *   weft, "Shapes and symbols": B, H_q, H_kv (H_q / H_kv = GQA group), D, N, P, T_total.
  *   weft, "Cache layouts": per-layer paged view [N, P, H_kv, D]; write = scatter
@@ -73,6 +80,10 @@ typedef enum wf_dtype {
 #define WF_DEV_TIMEOUT     0x8u  /* a wait gave up: an internal pipeline wait (should never
                                     happen), or a decode worker idle past its limit          */
 #define WF_DEV_BAD_TASK    0x10u /* decode worker: a task record out of range (skipped)     */
+#define WF_DEV_BAD_POSITION 0x20u /* norm + rotation: a position outside the table: token
+                                    skipped                                                 */
+#define WF_DEV_BAD_NODE    0x40u /* accepted path out of range or not increasing: request
+                                    skipped                                                 */
 
 /* One layer's pool geometry.  k_pool and v_pool are each [N, P, H_kv, D]. */
 typedef struct wf_pool_desc {
@@ -118,6 +129,46 @@ typedef struct wf_pool_desc {
 wf_status wf_reshape_and_cache(const void* k, const void* v, void* k_pool, void* v_pool,
                                const int64_t* slot_mapping, int32_t num_tokens,
                                wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * wf_qk_norm_rope_and_cache -- what stands between a layer's q, k, v projections and
+ * its attention, in one pass: the norms of queries and keys per head, their rotation
+ * by position, and the write of the new rows into the block pool.
+ * (tiny-vllm-py, "KV Cache": the cache holds RoPE-rotated K and plain V; weft, "Cache
+ *  layouts": write = scatter via slot_mapping)
+ *
+ *   q_out        [T, H_q, D] dense: the normed and rotated queries (must not overlap q)
+ *   q            [T, H_q, D], k and v [T, H_kv, D]: heads and elements of a token are
+ *                dense; *_stride is the distance between tokens in elements (at least
+ *                the token's own size when T > 1, a multiple of 16 bytes), so the three
+ *                may be cut from one fused projection.
+ *   q_weight     [D] weights of the RMS norm of each query head, in q's dtype:
+ *                y = x / sqrt(mean(x^2) + eps) * w.  NULL: queries are not normed.
+ *   k_weight     the same for keys
+ *   eps          finite, >= 0
+ *   cos_sin      [max_position, rotary_dim] float32: row p holds cos of the
+ *                rotary_dim / 2 angles of position p, then their sin
+ *   positions    [T] int32: the token's position, 0 <= positions[t] < max_position
+ *   rotary_dim   even, 0 .. D: the leading elements of each head that are rotated,
+ *                (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i), i < rotary_dim / 2.
+ *                0: no rotation; cos_sin and positions are not read and may be NULL.
+ *   interleaved  0: a, b are elements i and i + rotary_dim / 2; else 2i and 2i + 1
+ *   k_pool, v_pool, slot_mapping, num_tokens: as for wf_reshape_and_cache
+ * q, k, v and q_out have the pool's dtype (bfloat16 for fp8 pools).  Norm and rotation
+ * are float32 and each result is rounded once, K straight to the pool's type: an fp8
+ * code is e4m3(y * (1.0f / scale_h)) of the float32 y, which is not always the code
+ * that wf_reshape_and_cache stores for a y rounded to bfloat16 first.
+ * A token with a negative slot is padding: nothing is written for it, its q_out row
+ * included, and its position is not looked at.  A token with a slot >= N*P (WF_DEV_BAD_SLOT) or a position out
+ * of range (WF_DEV_BAD_POSITION) is skipped and flagged the same way.
+ * Any rotary_dim is taken; multiples of 16 read the table in 16-byte chunks.
+ */
+wf_status wf_qk_norm_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, const void* q_weight, const void* k_weight,
+                                    float eps, const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                                    int32_t interleaved, const int32_t* positions, void* k_pool, void* v_pool,
+                                    const int64_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                    wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream);
 
 /*
  * wf_copy_blocks -- copy-on-write block copy for prefix sharing.
@@ -239,6 +290,79 @@ wf_status wf_paged_prefill_decode(void* pf_out, const void* pf_q, const int32_t*
 int wf_paged_prefill_decode_fused(wf_pool_desc pool, int32_t num_q_heads);
 
 /*
+ * Bytes of caller-allocated device workspace wf_paged_tree_decode needs for at most B
+ * requests of at most max_q_len drafts and max_seq_len tokens.  Depends only on its
+ * arguments; 0 if they are invalid.
+ */
+size_t wf_paged_tree_decode_workspace_size(int32_t B, int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len,
+                                           wf_pool_desc pool);
+
+/*
+ * wf_paged_tree_decode -- attention of trees of drafted tokens over the pool: every
+ * draft sees its request's cached context and those drafts of its own request that its
+ * mask row names (itself and its ancestors in the tree, as a rule).
+ * (the decode of wf_paged_decode and the packed rows of wf_paged_prefill; the pages
+ *  have no drafts)
+ *
+ *   out, q     [T_total, H_q, D]: request b owns rows cu_q_lens[b] .. cu_q_lens[b+1]-1,
+ *              its n_b drafts.  Rows past cu_q_lens[B] are neither read nor written.
+ *   cu_q_lens  [B+1] int32, cu_q_lens[0] = 0, non-decreasing, cu_q_lens[B] <= T_total
+ *   seq_lens   [B] int32: tokens of request b in the pool INCLUDING its n_b drafts,
+ *              already written: with c_b = seq_lens[b] - n_b, draft j lies at cache
+ *              position c_b + j whatever its depth in the tree.
+ *   tree_mask  [T_total, mask_words] uint32: row i of request b attends to positions
+ *              0 .. c_b - 1 and to every c_b + j, j < n_b, whose bit j % 32 of word
+ *              j / 32 is set.  Bits of j >= n_b are ignored; a row's own bit is not
+ *              implied.  mask_words >= ceil(max_q_len / 32).
+ *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b]
+ *   workspace  device scratch of >= wf_paged_tree_decode_workspace_size(B, H_q,
+ *              max_q_len, max_seq_len, pool) bytes, 16-byte aligned; needs no
+ *              initialisation.  Calls that overlap in time must not share one.
+ * A row that sees nothing (no context and no bit set) gives zeros.  A draft that a row
+ * does not see has no effect on it, whatever its K and V rows hold (NaN and infinities
+ * included); the same holds for pool rows past a request's length.  Requests
+ * with n_b = 0 are no-ops.  A request whose n_b or length is out of range
+ * (WF_DEV_BAD_SEQLEN) is skipped and its rows are left unwritten; positions of a block
+ * id out of range (WF_DEV_BAD_BLOCK) are left out of the softmax.
+ * float32, bfloat16 and fp8 e4m3 pools (q and out bfloat16 for fp8), H_q / H_kv <= 8.
+ * Context tiles are dealt to the CTAs in equal shares, so where a request's softmax is
+ * cut and joined (in float32) depends on the whole batch: the outputs of two calls with
+ * the same inputs are the same bytes, those of one request in two different batches
+ * need not be.
+ */
+wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, const void* v_pool,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                               const int32_t* cu_q_lens, const uint32_t* tree_mask, int32_t mask_words, int32_t B,
+                               int32_t total_q, int32_t max_q_len, int32_t max_seq_len, int32_t num_q_heads,
+                               float scale, wf_pool_desc pool, void* workspace, size_t workspace_bytes,
+                               uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * wf_keep_accepted -- after a tree of drafts is verified: the K and V rows of each
+ * request's accepted path move to the front of its drafts, where the next step expects
+ * them, in both pools.
+ *
+ *   block_tables, seq_lens, cu_q_lens: as for wf_paged_tree_decode (seq_lens still
+ *              counts the drafts)
+ *   accepted   [B, max_accepted] int32: the accepted drafts of request b, strictly
+ *              increasing node numbers below n_b; entries past num_accepted[b] are not read
+ *   num_accepted [B] int32, 0 <= num_accepted[b] <= min(max_accepted, n_b)
+ *   new_seq_lens [B] int32, may be NULL: receives c_b + num_accepted[b] (must not overlap
+ *              another argument)
+ * Row c_b + accepted[b][j] is copied to c_b + j, byte for byte, as if all rows were read
+ * before any is written; rows behind the kept ones are left as they are.  K rows carry
+ * the rotation of their position in the text (context + depth), which is the position
+ * they move to.  The drafts' blocks must belong to one request each.
+ * A request whose lengths are out of range (WF_DEV_BAD_SEQLEN) or whose path is
+ * (WF_DEV_BAD_NODE) is skipped whole, its new_seq_lens entry left unwritten; a row whose
+ * source or target block id is out of range (WF_DEV_BAD_BLOCK) is not moved.
+ */
+wf_status wf_keep_accepted(void* k_pool, void* v_pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* accepted,
+                           int32_t max_accepted, const int32_t* num_accepted, int32_t* new_seq_lens, int32_t B,
+                           wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream);
+
+/*
  * Size of the fixed device array wf_paged_decode_static_scratch uses as its
  * workspace (32 MiB).  A device holds it from the first
  * wf_paged_decode_static_scratch call on that device until the process exits.
@@ -345,19 +469,21 @@ wf_status wf_decode_worker(void* out, const void* q, int32_t num_rows, const voi
                            uint64_t idle_timeout_ns, uint32_t* dev_status, cudaStream_t stream);
 
 /*
- * Which kernel wf_paged_decode / wf_paged_prefill runs for a pool geometry and
- * query-head count (host-only, no CUDA call; for tests and tooling).  Returns a
+ * Which kernel wf_paged_decode / wf_paged_prefill / wf_paged_tree_decode runs for a
+ * pool geometry and query-head count (host-only, no CUDA call; for tests and tooling).  Returns a
  * wf_kernel value; WF_KERNEL_NONE when the geometry is invalid or unsupported.
  */
 typedef enum wf_kernel {
     WF_KERNEL_NONE = 0,
-    WF_KERNEL_CUDA_CORES = 1,            /* decode: split-K kernel on the CUDA cores          */
+    WF_KERNEL_CUDA_CORES = 1,            /* decode, tree decode: kernel on the CUDA cores      */
     WF_KERNEL_TENSOR_CORES = 2,          /* decode: split-K tcgen05 kernel (bf16, or fp8 codes);
-                                            prefill: warp-specialised pipelined tcgen05 kernel */
+                                            prefill, tree decode: warp-specialised pipelined
+                                            tcgen05 kernel                                     */
     WF_KERNEL_TENSOR_CORES_SIMPLE = 3    /* prefill: single-stage tcgen05 kernel (any P)       */
 } wf_kernel;
 int wf_paged_decode_kernel(wf_pool_desc pool, int32_t num_q_heads);
 int wf_paged_prefill_kernel(wf_pool_desc pool, int32_t num_q_heads);
+int wf_paged_tree_decode_kernel(wf_pool_desc pool, int32_t num_q_heads);
 /*
  * 1 when wf_paged_prefill runs a batch of B requests of at most max_q_len new tokens
  * as the persistent grid (WF_KERNEL_TENSOR_CORES geometries within the work list's

@@ -17,21 +17,27 @@ LIB_PATH = os.path.join(PKG, "libwf.so")
 WF_OK, WF_ERR_INVALID_ARG, WF_ERR_UNSUPPORTED, WF_ERR_WORKSPACE, WF_ERR_CUDA, WF_ERR_NO_BLOCKS = range(6)
 WF_DTYPE_F32, WF_DTYPE_BF16, WF_DTYPE_FP8_E4M3 = 0, 1, 2
 WF_DEV_BAD_SLOT, WF_DEV_BAD_BLOCK, WF_DEV_BAD_SEQLEN, WF_DEV_TIMEOUT, WF_DEV_BAD_TASK = 0x1, 0x2, 0x4, 0x8, 0x10
+WF_DEV_BAD_POSITION, WF_DEV_BAD_NODE = 0x20, 0x40
 WF_KERNEL_NONE, WF_KERNEL_CUDA_CORES, WF_KERNEL_TENSOR_CORES, WF_KERNEL_TENSOR_CORES_SIMPLE = range(4)
 
 # every entry point include/*.h declares
 EXPORTS = (
     "wf_reshape_and_cache",
+    "wf_qk_norm_rope_and_cache",
     "wf_copy_blocks",
     "wf_paged_decode_workspace_size",
     "wf_paged_decode",
     "wf_paged_prefill",
     "wf_paged_prefill_decode",
     "wf_paged_prefill_decode_fused",
+    "wf_paged_tree_decode_workspace_size",
+    "wf_paged_tree_decode",
+    "wf_keep_accepted",
     "wf_paged_decode_static_scratch",
     "wf_decode_worker",
     "wf_paged_decode_kernel",
     "wf_paged_prefill_kernel",
+    "wf_paged_tree_decode_kernel",
     "wf_paged_prefill_persistent",
     "wf_device_status_fetch",
     "wf_status_string",
@@ -92,6 +98,18 @@ def load(path: str = LIB_PATH):
         lib.wf_paged_prefill_decode.restype = ctypes.c_int
         lib.wf_paged_prefill_decode_fused.argtypes = [wf_pool_desc, i32]
         lib.wf_paged_prefill_decode_fused.restype = ctypes.c_int
+        lib.wf_qk_norm_rope_and_cache.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, vp, f32, vp, i32, i32, i32, vp, vp,
+                                                  vp, vp, i32, i32, wf_pool_desc, vp, vp]
+        lib.wf_qk_norm_rope_and_cache.restype = ctypes.c_int
+        lib.wf_paged_tree_decode_workspace_size.argtypes = [i32, i32, i32, i32, wf_pool_desc]
+        lib.wf_paged_tree_decode_workspace_size.restype = sz
+        lib.wf_paged_tree_decode.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32,
+                                             wf_pool_desc, vp, sz, vp, vp]
+        lib.wf_paged_tree_decode.restype = ctypes.c_int
+        lib.wf_paged_tree_decode_kernel.argtypes = [wf_pool_desc, i32]
+        lib.wf_paged_tree_decode_kernel.restype = ctypes.c_int
+        lib.wf_keep_accepted.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, i32, wf_pool_desc, vp, vp]
+        lib.wf_keep_accepted.restype = ctypes.c_int
         lib.wf_paged_decode_static_scratch.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, f32,
                                                        wf_pool_desc, vp, vp]
         lib.wf_paged_decode_static_scratch.restype = ctypes.c_int
@@ -215,6 +233,47 @@ def wf_reshape_and_cache(k, v, k_pool, v_pool, slot_mapping, dev_status=None, st
     _check("wf_reshape_and_cache", rc)
 
 
+def _token_stride(name, t, dt, n):
+    """Elements between the tokens of t [n, heads, D], whose heads and elements are dense."""
+    if t.dim() != 3 or t.shape[0] != n or t.dtype != dt:
+        raise ValueError(f"{name} must be [{n}, heads, D] of {dt}")
+    token, head, elt = t.stride()
+    if elt != 1 or (head != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name}: heads and elements of a token must be dense")
+    return token if n > 1 else t.shape[1] * t.shape[2]
+
+
+def wf_qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps: float, cos_sin, positions, k_pool, v_pool,
+                              slot_mapping, interleaved: bool = False, dev_status=None, stream=None, k_scale=1.0,
+                              v_scale=1.0):
+    """Norm (q_weight, k_weight [D] or None) and rotate q [T, H_q, D] and k [T, H_kv, D] (cos_sin [positions, rotary_dim]
+    float32 or None, positions [T] int32), write q_out [T, H_q, D] and scatter the new k and v rows into the pools.
+    q, k and v may be strided over tokens (views of one fused projection)."""
+    import torch
+    _contig(q_out, q_weight, k_weight, cos_sin, positions, k_pool, v_pool, slot_mapping)
+    T, H_q, D = q.shape
+    N, P, H_kv, pool_D = k_pool.shape
+    dt = torch.bfloat16 if k_pool.dtype == torch.uint8 else k_pool.dtype
+    strides = [_token_stride(n, t, dt, T) for n, t in (("q", q), ("k", k), ("v", v))]
+    if q_out.shape != q.shape or q_out.dtype != dt or slot_mapping.shape[0] != T or D != pool_D or             k.shape[1:] != (H_kv, D) or v.shape[1:] != (H_kv, D) or slot_mapping.dtype != torch.int64:
+        raise ValueError("q_out is like q, k and v are [T, H_kv, D] of the pool, slot_mapping is [T] int64")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != dt or w.numel() != D):
+            raise ValueError(f"norm weights must be [{D}] of {dt}")
+    rotary, rows = 0, 0
+    if cos_sin is not None:
+        rows, rotary = cos_sin.shape
+        if cos_sin.dtype != torch.float32 or positions.dtype != torch.int32 or positions.shape[0] != T:
+            raise ValueError("cos_sin must be [max_position, rotary_dim] float32 and positions [T] int32")
+    lib = load()
+    rc = lib.wf_qk_norm_rope_and_cache(_ptr(q_out), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
+                                       _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin), rows, rotary,
+                                       int(interleaved), _ptr(positions) if rotary else None, _ptr(k_pool),
+                                       _ptr(v_pool), _ptr(slot_mapping), T, H_q, pool_desc(k_pool, k_scale, v_scale),
+                                       _ptr(dev_status), _stream(stream))
+    _check("wf_qk_norm_rope_and_cache", rc)
+
+
 def wf_copy_blocks(k_pool, v_pool, block_pairs, dev_status=None, stream=None, k_scale=1.0,
                    v_scale=1.0):
     """Copy block src to block dst of both pools for every (src, dst) row of block_pairs [n, 2] int32."""
@@ -280,6 +339,48 @@ def wf_paged_prefill_decode(pf_out, pf_q, pf_block_tables, pf_seq_lens, cu_q_len
     _check("wf_paged_prefill_decode", rc)
 
 
+def wf_paged_tree_decode_workspace_size(B: int, num_q_heads: int, max_q_len: int, max_seq_len: int,
+                                        desc: wf_pool_desc) -> int:
+    return int(load().wf_paged_tree_decode_workspace_size(B, num_q_heads, max_q_len, max_seq_len, desc))
+
+
+def wf_paged_tree_decode(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, tree_mask, max_q_len: int,
+                         max_seq_len: int, scale: float, workspace, dev_status=None, stream=None, k_scale=1.0,
+                         v_scale=1.0):
+    """out, q [T_total, H_q, D] packed drafts; cu_q_lens [B+1] int32; seq_lens [B] int32 count the drafts; tree_mask
+    [T_total, words] int32 (bit j of a row: draft j of its request is seen); workspace uint8 tensor."""
+    _contig(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, tree_mask)
+    lib = load()
+    T, H_q, D = q.shape
+    B, M = block_tables.shape
+    if out.shape != q.shape or out.dtype != q.dtype or D != k_pool.shape[3] or tree_mask.shape[0] != T or \
+            tree_mask.element_size() != 4 or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or \
+            q.element_size() != max(2, k_pool.element_size()):
+        raise ValueError("out is like q [T, H_q, D] of the pool's dtype (bf16 for fp8 pools), tree_mask [T, words] of "
+                         "32-bit words, block_tables [B, M], seq_lens [B], cu_q_lens [B + 1]")
+    rc = lib.wf_paged_tree_decode(_ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), M,
+                                  _ptr(seq_lens), _ptr(cu_q_lens), _ptr(tree_mask), tree_mask.shape[1], B, T,
+                                  max_q_len, max_seq_len, H_q, scale, pool_desc(k_pool, k_scale, v_scale),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                                  _stream(stream))
+    _check("wf_paged_tree_decode", rc)
+
+
+def wf_keep_accepted(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted, num_accepted, new_seq_lens=None,
+                     dev_status=None, stream=None, k_scale=1.0, v_scale=1.0):
+    """Move the rows of each request's accepted drafts (accepted [B, depth] int32, num_accepted [B] int32) to the front
+    of its drafts in both pools; new_seq_lens [B] int32 receives the kept lengths."""
+    _contig(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted, num_accepted, new_seq_lens)
+    B, M = block_tables.shape
+    if accepted.shape[0] != B or num_accepted.shape[0] != B or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 \
+            or (new_seq_lens is not None and new_seq_lens.shape[0] != B):
+        raise ValueError("accepted [B, depth], num_accepted, seq_lens and new_seq_lens [B], cu_q_lens [B + 1]")
+    rc = load().wf_keep_accepted(_ptr(k_pool), _ptr(v_pool), _ptr(block_tables), M, _ptr(seq_lens), _ptr(cu_q_lens),
+                                 _ptr(accepted), accepted.shape[1], _ptr(num_accepted), _ptr(new_seq_lens), B,
+                                 pool_desc(k_pool, k_scale, v_scale), _ptr(dev_status), _stream(stream))
+    _check("wf_keep_accepted", rc)
+
+
 WF_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -325,6 +426,11 @@ def wf_paged_decode_kernel(desc: wf_pool_desc, num_q_heads: int) -> int:
 def wf_paged_prefill_kernel(desc: wf_pool_desc, num_q_heads: int) -> int:
     """The WF_KERNEL_* value of the kernel wf_paged_prefill runs for this geometry."""
     return int(load().wf_paged_prefill_kernel(desc, int(num_q_heads)))
+
+
+def wf_paged_tree_decode_kernel(desc: wf_pool_desc, num_q_heads: int) -> int:
+    """The WF_KERNEL_* value of the kernel wf_paged_tree_decode runs for this geometry."""
+    return int(load().wf_paged_tree_decode_kernel(desc, int(num_q_heads)))
 
 
 def wf_paged_prefill_persistent(desc: wf_pool_desc, num_q_heads: int, B: int, max_q_len: int) -> bool:

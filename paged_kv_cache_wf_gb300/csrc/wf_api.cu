@@ -145,6 +145,71 @@ wf_status wf_reshape_and_cache(const void* k, const void* v, void* k_pool, void*
                                                   pool, dev_status, stream));
 }
 
+wf_status wf_qk_norm_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, const void* q_weight, const void* k_weight,
+                                    float eps, const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                                    int32_t interleaved, const int32_t* positions, void* k_pool, void* v_pool,
+                                    const int64_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                    wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream) {
+    wf_status s = check_pool(pool);
+    if (s != WF_OK) return s;
+    if (num_tokens < 0 || num_q_heads < 1 || num_q_heads % pool.num_kv_heads != 0) return WF_ERR_INVALID_ARG;
+    if (rotary_dim < 0 || rotary_dim > pool.head_dim || rotary_dim % 2 != 0) return WF_ERR_INVALID_ARG;
+    if (rotary_dim > 0 && max_position < 1) return WF_ERR_INVALID_ARG;
+    if (!std::isfinite(eps) || eps < 0.f) return WF_ERR_INVALID_ARG;
+    if (num_tokens == 0) return WF_OK;
+    if (!q_out || !q || !k || !v || !k_pool || !v_pool || !slot_mapping) return WF_ERR_INVALID_ARG;
+    if (rotary_dim > 0 && (!cos_sin || !positions || !aligned16(cos_sin) ||
+                           (reinterpret_cast<uintptr_t>(positions) & 3u)))
+        return WF_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_pool) ||
+        !aligned16(v_pool) || (q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return WF_ERR_INVALID_ARG;
+    const int64_t act = pool.dtype == WF_DTYPE_F32 ? 4 : 2;
+    const int64_t qrow = (int64_t)num_q_heads * pool.head_dim, krow = (int64_t)pool.num_kv_heads * pool.head_dim;
+    if (num_tokens > 1) {
+        if (q_stride < qrow || k_stride < krow || v_stride < krow) return WF_ERR_INVALID_ARG;
+        if (q_stride * act % 16 != 0 || k_stride * act % 16 != 0 || v_stride * act % 16 != 0)
+            return WF_ERR_INVALID_ARG;
+        // beyond any device's memory: keeps every byte offset within 63 bits
+        const int64_t cap = (int64_t)1 << 40;
+        if (q_stride > cap || k_stride > cap || v_stride > cap) return WF_ERR_INVALID_ARG;
+    } else {
+        q_stride = qrow;
+        k_stride = v_stride = krow;
+    }
+    // every q row is read by several threads while others write q_out
+    const uintptr_t o0 = reinterpret_cast<uintptr_t>(q_out), o1 = o0 + (uintptr_t)(num_tokens * qrow * act);
+    const uintptr_t i0 = reinterpret_cast<uintptr_t>(q),
+                    i1 = i0 + (uintptr_t)(((int64_t)(num_tokens - 1) * q_stride + qrow) * act);
+    if (o0 < i1 && i0 < o1) return WF_ERR_INVALID_ARG;
+    const wf::RopeArgs a{q_out, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos_sin, max_position,
+                         rotary_dim, interleaved, positions, k_pool, v_pool, slot_mapping, num_tokens, num_q_heads};
+    return from_cuda(wf::launch_qk_norm_rope(a, pool, dev_status, stream));
+}
+
+wf_status wf_keep_accepted(void* k_pool, void* v_pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* accepted,
+                           int32_t max_accepted, const int32_t* num_accepted, int32_t* new_seq_lens, int32_t B,
+                           wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream) {
+    wf_status s = check_pool(pool);
+    if (s != WF_OK) return s;
+    if (B < 0 || max_accepted < 0 || max_blocks_per_seq < 1) return WF_ERR_INVALID_ARG;
+    if (B == 0) return WF_OK;
+    if (!k_pool || !v_pool || !block_tables || !seq_lens || !cu_q_lens || !num_accepted ||
+        (max_accepted > 0 && !accepted))
+        return WF_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool)) return WF_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)block_tables, (const void*)seq_lens, (const void*)cu_q_lens,
+                          (const void*)accepted, (const void*)num_accepted, (const void*)new_seq_lens})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return WF_ERR_INVALID_ARG;
+    if (new_seq_lens == seq_lens || new_seq_lens == num_accepted) return WF_ERR_INVALID_ARG;
+    return from_cuda(wf::launch_keep_accepted(k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
+                                              accepted, max_accepted, num_accepted, new_seq_lens, B, pool, dev_status,
+                                              stream));
+}
+
 wf_status wf_copy_blocks(void* k_pool, void* v_pool, const int32_t* block_pairs, int32_t num_pairs,
                          wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream) {
     wf_status s = check_pool(pool);
@@ -281,6 +346,43 @@ wf_status wf_paged_prefill_decode(void* pf_out, const void* pf_q, const int32_t*
         dec_max_seq_len, k_pool, v_pool, num_q_heads, scale, pool, workspace, dev_status, stream));
 }
 
+size_t wf_paged_tree_decode_workspace_size(int32_t B, int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len,
+                                           wf_pool_desc pool) {
+    if (check_pool(pool) != WF_OK || num_q_heads < 1) return 0;
+    return wf::tree_workspace_bytes(B, num_q_heads, max_q_len, max_seq_len, pool);
+}
+
+wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, const void* v_pool,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                               const int32_t* cu_q_lens, const uint32_t* tree_mask, int32_t mask_words, int32_t B,
+                               int32_t total_q, int32_t max_q_len, int32_t max_seq_len, int32_t num_q_heads,
+                               float scale, wf_pool_desc pool, void* workspace, size_t workspace_bytes,
+                               uint32_t* dev_status, cudaStream_t stream) {
+    wf_status s = check_pool(pool);
+    if (s != WF_OK) return s;
+    if (B < 0 || total_q < 0 || max_q_len < 0 || max_seq_len < 0 || num_q_heads < 1 || max_blocks_per_seq < 1)
+        return WF_ERR_INVALID_ARG;
+    if (num_q_heads % pool.num_kv_heads != 0) return WF_ERR_INVALID_ARG;
+    if (num_q_heads / pool.num_kv_heads > 8) return WF_ERR_UNSUPPORTED;
+    if ((int64_t)max_seq_len > (int64_t)max_blocks_per_seq * pool.block_size || max_q_len > max_seq_len)
+        return WF_ERR_INVALID_ARG;
+    if (mask_words < 0 || (int64_t)mask_words * 32 < max_q_len) return WF_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return WF_ERR_INVALID_ARG;
+    if (B == 0 || total_q == 0 || max_q_len == 0) return WF_OK;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !cu_q_lens || !tree_mask)
+        return WF_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool)) return WF_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)block_tables, (const void*)seq_lens, (const void*)cu_q_lens,
+                          (const void*)tree_mask})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return WF_ERR_INVALID_ARG;
+    const size_t need = wf::tree_workspace_bytes(B, num_q_heads, max_q_len, max_seq_len, pool);
+    if (need == 0) return WF_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return WF_ERR_WORKSPACE;
+    const wf::TreeArgs a{out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, tree_mask,
+                         mask_words, B, total_q, max_q_len, max_seq_len, num_q_heads, scale, workspace};
+    return from_cuda(wf::launch_paged_tree(a, pool, dev_status, stream));
+}
+
 wf_status wf_decode_worker(void* out, const void* q, int32_t num_rows, const void* k_pool, const void* v_pool,
                            const int32_t* block_tables, int32_t num_table_rows, int32_t max_blocks_per_seq,
                            int32_t num_q_heads, float scale, wf_pool_desc pool, const wf_decode_task* tasks,
@@ -319,6 +421,11 @@ int wf_paged_decode_kernel(wf_pool_desc pool, int32_t num_q_heads) {
 int wf_paged_prefill_kernel(wf_pool_desc pool, int32_t num_q_heads) {
     if (check_pool(pool) != WF_OK || num_q_heads < 1) return WF_KERNEL_NONE;
     return wf::prefill_kernel_kind(pool, num_q_heads);
+}
+
+int wf_paged_tree_decode_kernel(wf_pool_desc pool, int32_t num_q_heads) {
+    if (check_pool(pool) != WF_OK || num_q_heads < 1) return WF_KERNEL_NONE;
+    return wf::tree_kernel_kind(pool, num_q_heads);
 }
 
 int wf_paged_prefill_persistent(wf_pool_desc pool, int32_t num_q_heads, int32_t B, int32_t max_q_len) {

@@ -143,6 +143,45 @@ cudaError_t launch_paged_prefill_decode(void* pf_out, const void* pf_q, const in
                                        const wf_pool_desc& pool, void* workspace, uint32_t* dev_status,
                                        cudaStream_t stream);
 
+// ---- drafts ---------------------------------------------------------------------
+// Norm + rotation + scatter (qk_norm_rope.cu) and the accepted rows' move (keep_accepted.cu).
+struct RopeArgs {
+    void* q_out;
+    const void *q, *k, *v;                       // token strides in elements
+    int64_t q_stride, k_stride, v_stride;
+    const void *q_weight, *k_weight;
+    float eps;
+    const float* cos_sin;
+    int32_t max_position, rotary_dim, interleaved;
+    const int32_t* positions;
+    void *k_pool, *v_pool;
+    const int64_t* slot_mapping;
+    int32_t num_tokens, num_q_heads;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, const wf_pool_desc& pool, uint32_t* dev_status,
+                                cudaStream_t stream);
+cudaError_t launch_keep_accepted(void* k_pool, void* v_pool, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* accepted,
+                                 int32_t max_accepted, const int32_t* num_accepted, int32_t* new_seq_lens, int32_t B,
+                                 const wf_pool_desc& pool, uint32_t* dev_status, cudaStream_t stream);
+
+// Tree attention (paged_tree.cu: CUDA cores, the joining kernel and the dispatch).
+struct TreeArgs {
+    void* out;
+    const void *q, *k_pool, *v_pool;
+    const int32_t* block_tables;
+    int32_t max_blocks_per_seq;
+    const int32_t *seq_lens, *cu_q_lens;
+    const uint32_t* tree_mask;
+    int32_t mask_words, B, total_q, max_q_len, max_seq_len, num_q_heads;
+    float scale;
+    void* workspace;
+};
+size_t tree_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len,
+                            const wf_pool_desc& pool);
+int tree_kernel_kind(const wf_pool_desc& pool, int32_t num_q_heads);
+cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint32_t* dev_status, cudaStream_t stream);
+
 // ---- prefill ------------------------------------------------------------------
 // Pipelined tcgen05 prefill (bf16, P % 16 == 0, G in {1, 2, 4, 8}, D in {64, 128}).
 bool prefill_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads);
