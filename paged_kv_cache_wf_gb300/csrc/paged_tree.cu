@@ -6,6 +6,7 @@
 // 0 .. c_b - 1 (ember, "The core idea": position p lives in block table[p / P] at
 // p % P) and the drafts c_b + j that its mask names; o = softmax(scale q K^T) V over
 // them, with the running maximum and sum of an online softmax in fp32 (exp2 domain).
+#include <cfloat>
 #include <cmath>
 
 #include "paged_tree.cuh"
@@ -336,15 +337,15 @@ __global__ void __launch_bounds__(256) paged_tree_join_kernel(const TreeParams p
         float mn = M;
 #pragma unroll
         for (int u = 0; u < kChunk; ++u) mn = fmaxf(mn, ml[u].x);
-        if (mn == -INFINITY) continue;   // the row sees nothing so far
-        const float a = M == -INFINITY ? 0.f : exp2f(M - mn);
+        // a piece (or all before it) without a maximum has a sum of 0, or of NaN, which has to stay
+        const float a = M == -INFINITY ? 1.f : exp2f(M - mn);
         den *= a;
 #pragma unroll
         for (int e = 0; e < VPL; ++e) o[e] *= a;
 #pragma unroll
         for (int u = 0; u < kChunk; ++u) {
-            if (u0 + u >= cnt || ml[u].x == -INFINITY) continue;
-            const float w = exp2f(ml[u].x - mn);
+            if (u0 + u >= cnt || ml[u].y == 0.f) continue;
+            const float w = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - mn);
             den += w * ml[u].y;
             o[0] += w * x[u].x;
             o[1] += w * x[u].y;
@@ -390,35 +391,38 @@ cudaError_t launch_cc(const TreeParams& p, const HeadScales& sc, int ctas, cudaS
 
 }  // namespace
 
-static bool tree_shape(const wf_pool_desc& pool, int32_t num_q_heads, TreeShape* s) {
+static bool tree_shape(const wf_pool_desc& pool, int32_t num_q_heads, int32_t max_q_len, TreeShape* s) {
     if (num_q_heads % pool.num_kv_heads != 0) return false;
     const int G = num_q_heads / pool.num_kv_heads;
     if (G < 1 || G > 8) return false;
-    *s = TreeShape{kCcRows, kCcRows / G, kCcTile, 2};
+    *s = tree_tc_supported(pool, num_q_heads) ? tree_tc_shape(G, max_q_len)
+                                              : TreeShape{kCcRows, kCcRows / G, kCcTile, 2};
     return true;
 }
 
 // CTAs the launch may use: no more than there can be tiles.
 static int64_t tree_ctas(const TreeShape& s, int32_t B, int32_t H_kv, int32_t max_q_len, int32_t max_seq_len) {
+    const int64_t cap = (int64_t)s.ctas_per_sm * kTreeMaxSms;
     int64_t all = 1;
     for (const int64_t f : {(int64_t)B, (int64_t)H_kv, ((int64_t)max_q_len + s.tokb - 1) / s.tokb,
                             ((int64_t)max_seq_len + s.tile - 1) / s.tile}) {
         if (f == 0) return 1;
-        all = f >= kTreeMaxCtas ? kTreeMaxCtas : all * f;
-        if (all >= kTreeMaxCtas) all = kTreeMaxCtas;
+        all = f >= cap ? cap : all * f;
+        if (all > cap) all = cap;
     }
     return all;
 }
 
 int tree_kernel_kind(const wf_pool_desc& pool, int32_t num_q_heads) {
     TreeShape s;
-    return tree_shape(pool, num_q_heads, &s) ? WF_KERNEL_CUDA_CORES : WF_KERNEL_NONE;
+    if (!tree_shape(pool, num_q_heads, 1, &s)) return WF_KERNEL_NONE;
+    return tree_tc_supported(pool, num_q_heads) ? WF_KERNEL_TENSOR_CORES : WF_KERNEL_CUDA_CORES;
 }
 
 size_t tree_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, int32_t max_seq_len,
                             const wf_pool_desc& pool) {
     TreeShape s;
-    if (B < 0 || max_q_len < 0 || max_seq_len < 0 || !tree_shape(pool, num_q_heads, &s)) return 0;
+    if (B < 0 || max_q_len < 0 || max_seq_len < 0 || !tree_shape(pool, num_q_heads, max_q_len, &s)) return 0;
     const int64_t ctas = tree_ctas(s, B, pool.num_kv_heads, max_q_len, max_seq_len);
     const int64_t rows = 2 * ctas * s.rows;
     return (size_t)(256 + ctas * (int64_t)sizeof(int4) + rows * 8 + rows * pool.head_dim * 4);
@@ -427,7 +431,7 @@ size_t tree_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, i
 cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint32_t* dev_status,
                               cudaStream_t stream) {
     TreeShape s;
-    if (!tree_shape(pool, a.num_q_heads, &s)) return cudaErrorNotSupported;
+    if (!tree_shape(pool, a.num_q_heads, a.max_q_len, &s)) return cudaErrorNotSupported;
     const int64_t cap = tree_ctas(s, a.B, pool.num_kv_heads, a.max_q_len, a.max_seq_len);
     const int64_t fit = (int64_t)s.ctas_per_sm * num_sms();
     const int ctas = (int)(cap < fit ? cap : fit);
@@ -459,8 +463,16 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint3
     p.rows = s.rows;
     p.tokb = s.tokb;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    const HeadScales sc = head_scales(pool);
+    // a masked score is -inf before it is scaled: a scale of 0 (equal weights) stands as the
+    // smallest normal number, which leaves every finite score a weight of 2^0
+    if (fabsf(p.scale_log2) < FLT_MIN) p.scale_log2 = copysignf(FLT_MIN, p.scale_log2);
     const bool d128 = pool.head_dim == 128;
+    if (tree_tc_supported(pool, a.num_q_heads)) {
+        const cudaError_t e = launch_tree_tc(p, pool.head_dim, ctas, stream);
+        if (e != cudaSuccess || ctas == 1) return e;
+        return d128 ? launch_join<BF16, 128>(p, ctas, stream) : launch_join<BF16, 64>(p, ctas, stream);
+    }
+    const HeadScales sc = head_scales(pool);
     switch (pool.dtype) {
         case WF_DTYPE_F32:
             return d128 ? launch_cc<F32, F32, 128>(p, sc, ctas, stream) : launch_cc<F32, F32, 64>(p, sc, ctas, stream);

@@ -19,11 +19,6 @@
 
 namespace wf {
 
-namespace {
-
-constexpr int kTreeMaxCtas = 320;   // CTAs a launch may use (the workspace holds their pieces)
-constexpr int kTreeUnitCost = 2;    // a unit's start and end, in tiles
-
 struct TreeParams {
     void* out;
     const void* q;
@@ -42,6 +37,21 @@ struct TreeParams {
     int32_t tokb;    // drafts of a row block
     float scale_log2;
 };
+
+// Rows of a row block, drafts in it, tile and CTAs an SM of the kernel that runs a call.
+struct TreeShape {
+    int rows, tokb, tile, ctas_per_sm;
+};
+
+// The tensor-core kernel (paged_tree_tc.cu).
+bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads);
+TreeShape tree_tc_shape(int G, int max_q_len);
+cudaError_t launch_tree_tc(const TreeParams& p, int D, int ctas, cudaStream_t stream);
+
+namespace {
+
+constexpr int kTreeMaxSms = 160;    // SMs a launch may use (the workspace holds their CTAs' pieces)
+constexpr int kTreeUnitCost = 2;    // a unit's start and end, in tiles
 
 // A request's drafts and length, n = 0 for one that fails the checks.
 struct TreeReq {
@@ -211,13 +221,5 @@ __device__ __forceinline__ bool tree_bit(const TreeParams& p, int row, int j) {
 }
 
 }  // namespace
-
-// Rows of a row block, drafts in it and tile of the kernel that runs a geometry.
-struct TreeShape {
-    int rows, tokb, tile, ctas_per_sm;
-};
-
-// The tensor-core kernel (paged_tree_tc.cu).
-bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads);
 
 }  // namespace wf

@@ -1,0 +1,687 @@
+// paged_tree_tc.cu -- tree attention on the tensor cores (tcgen05, TMA, TMEM) for bf16
+// pools whose block size is a multiple of 16.
+//
+// What is computed is paged_tree.cu's: row (draft, query head) sees its request's cached
+// positions and the drafts of its mask; o = softmax(scale q K^T) V.
+//
+// GB300 design.  A work unit (paged_tree.cuh) is one row block of a request under one
+// KV head.  Its K and V tiles (128 positions, gathered 16-position box by box through
+// the block table, 128-byte swizzle) run through a K ring and a V ring without a break
+// from piece to piece, and two softmax warpgroups (one thread a row, one TMEM lane a
+// thread) keep the tensor core on S = Q K^T of one stream while the other's softmax
+// runs.  What the two streams are is the template's choice:
+//   QT = 1  (all units of the batch have at most 128 rows): both streams are the same
+//           128 rows, on alternate tiles, each with its own running maximum, sum and O
+//           accumulator; at a piece's end the two are joined from TMEM, each warpgroup
+//           half of the columns.
+//   QT = 2  (up to 256 rows a unit): one 128-row query tile each, on the same tiles, so
+//           a loaded tile serves 256 rows.
+// 12 warps: 0-7 softmax (stream t = warp / 4), 8 K loads, 9 V loads, 10 query tiles and
+// the V tiles' finish, 11 MMA issue.
+// The finish of a V tile: a weight of 0 hides a position only from finite values (0 *
+// NaN is NaN in P V).  Rows past the request's end or of a bad block are zeroed; an
+// element of a draft's row that is not finite is zeroed too, and the epilogue adds it
+// to the rows that see the draft.  Only tiles that reach the drafts are looked at.
+#include <cuda.h>
+
+#include "paged_tree.cuh"
+
+namespace wf {
+
+namespace {
+
+constexpr int TM = 128;           // rows of a query tile (TMEM lanes)
+constexpr int TN = 128;           // positions of a tile
+constexpr float kLazyMax = 8.f;   // rescale O only when a row's maximum grows by more than 2^8
+constexpr int kSoftW = 8, kKW = 8, kVW = 9, kAuxW = 10, kMmaW = 11;
+constexpr int kTcThreads = 12 * 32;
+
+template <int D, int QT>
+struct TtLayout {
+    static constexpr int NC = D / 64;                    // 64-wide column blocks of D
+    static constexpr int QTILE = TM * D * 2;
+    static constexpr int SLOT = TN * D * 2;              // one K or V tile
+    static constexpr int ATOM = NC == 2 ? 2048 : 1024;   // stride between 8-position atoms
+    static constexpr int HALF_OFF = 1024;                // offset of the second 64-wide half
+    static constexpr int BOX = NC * 2048;                // one 16-position box
+    static constexpr int KS = QT == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 5);
+    static constexpr int VS = KS;
+    static constexpr int NSLOT = KS + VS;
+    static constexpr int q = 0;
+    static constexpr int kv = QT * QTILE;
+    static constexpr int ml = kv + NSLOT * SLOT;         // QT = 1: (m, l) of both streams' rows
+    static constexpr int bars = ml + (QT == 1 ? 2 * TM * 8 : 0);
+    // q_full[QT], q_empty[QT], slot_full[NSLOT], slot_empty[NSLOT], v_ready[VS], per
+    // stream s_full, p_full, pv_done, then x_ready, x_done
+    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 6 + 2;
+    static constexpr int start = bars + nbars * 8;
+    static constexpr int scratch = start + (int)sizeof(TreeStart);
+    static constexpr int misc = scratch + 12 * 8;        // [0] TMEM address, [1] abort, [8..15] wild drafts of a piece
+    static constexpr int total = misc + 64;
+    static constexpr int SCOL = 128, OCOL = 256, TMEM_COLS = 512;
+    static_assert(total <= 232448, "tree CTA exceeds shared memory");
+};
+
+// 32 drafts' bits of a mask row from draft `first` on (which may lie before 0 or past the
+// row): bit x is draft first + x, set for positions before the drafts, clear past n.
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int words, int first, int n) {
+    if (first + 31 < 0) return 0xffffffffu;
+    if (first >= n) return 0u;
+    const int w = first >> 5;
+    const uint32_t lo = w >= 0 && w < words ? __ldg(row + w) : 0u;
+    const uint32_t hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+    uint32_t r = __funnelshift_r(lo, hi, first & 31);
+    if (first < 0) r |= (1u << -first) - 1u;
+    if (n - first < 32) r &= (1u << (n - first)) - 1u;
+    return r;
+}
+
+// Zeroes the halves of w that are infinite or NaN; true when there were any.
+__device__ __forceinline__ bool tame(uint32_t& w) {
+    const uint32_t e = w & 0x7f807f80u;
+    uint32_t m = 0;
+    if ((e & 0xffffu) == 0x7f80u) m |= 0xffffu;
+    if ((e & 0xffff0000u) == 0x7f800000u) m |= 0xffff0000u;
+    w &= ~m;
+    return m != 0;
+}
+
+template <int D, int QT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const TreeParams p, const int box_tok) {
+    using L = TtLayout<D, QT>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+    uint64_t* q_full = bars;
+    uint64_t* q_empty = q_full + QT;
+    uint64_t* slot_full = q_empty + QT;
+    uint64_t* slot_empty = slot_full + L::NSLOT;
+    uint64_t* v_ready = slot_empty + L::NSLOT;
+    uint64_t* tb = v_ready + L::VS;
+    auto s_full = [&](int t) { return tb + t * 3; };
+    auto p_full = [&](int t) { return tb + t * 3 + 1; };
+    auto pv_done = [&](int t) { return tb + t * 3 + 2; };
+    uint64_t* x_ready = tb + 6;
+    uint64_t* x_done = x_ready + 1;
+    TreeStart* st = reinterpret_cast<TreeStart*>(smem + L::start);
+    volatile int* misc = reinterpret_cast<volatile int*>(smem + L::misc);
+    auto fail = [&]() {
+        report(p.dev_status, WF_DEV_TIMEOUT);
+        misc[1] = 1;
+    };
+    auto kslot = [&](int g) { return g % L::KS; };
+    auto vslot = [&](int g) { return L::KS + g % L::VS; };
+    auto slot_ptr = [&](int s) { return smem + L::kv + s * L::SLOT; };
+
+    if (warp == kMmaW) {
+        tc::alloc(reinterpret_cast<uint32_t*>(smem + L::misc), L::TMEM_COLS);
+        tc::relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < QT; ++t) {
+            mbar_init(&q_full[t], 1);
+            mbar_init(&q_empty[t], 1);
+        }
+        for (int i = 0; i < L::NSLOT; ++i) {
+            mbar_init(&slot_full[i], 1);
+            mbar_init(&slot_empty[i], 1);
+        }
+        for (int i = 0; i < L::VS; ++i) mbar_init(&v_ready[i], 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), 4);
+            mbar_init(pv_done(t), 1);
+        }
+        mbar_init(x_ready, kSoftW);
+        mbar_init(x_done, kSoftW);
+        fence_mbar_init();
+        misc[1] = 0;
+    }
+    tc::fence_before_sync();
+    tree_begin(p, TN, cta, gridDim.x, st, reinterpret_cast<int64_t*>(smem + L::scratch));
+    tc::fence_after_sync();
+    const uint32_t tmem = (uint32_t)misc[0];
+    const int tok_tile = TM / p.G;                       // drafts of a query tile
+    // steps of stream t over a piece of nt tiles (QT = 2: t's query tile may be empty),
+    // and the tile of its step u
+    auto steps = [&](const TreePiece& it, int t) {
+        const int nt = it.j1 - it.j0;
+        if constexpr (QT == 1) return (nt + 1 - t) >> 1;
+        return t == 0 || it.rows_tok > tok_tile ? nt : 0;
+    };
+    auto tile_at = [&](int t, int u) { return QT == 1 ? 2 * u + t : u; };
+    TreeWalk walk(*st);
+    TreePiece it;
+
+    if (warp == kKW || warp == kVW) {
+        // ============================= K and V loads =================================
+        // one 16-position box a lane; block ids are read one tile ahead
+        const bool isv = warp == kVW;
+        const CUtensorMap* tm = isv ? &tm_v : &tm_k;
+        int g = 0;
+        while (!misc[1] && walk.next(p, TN, it)) {
+            const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
+            int blk_next = 0;
+            if (lane < 8 && it.j0 * TN + lane * 16 < it.kend) blk_next = __ldg(trow + (it.j0 * TN + lane * 16) / p.P);
+            for (int j = it.j0; j < it.j1; ++j, ++g) {
+                const int s = isv ? vslot(g) : kslot(g);
+                const int round = isv ? g / L::VS : g / L::KS;
+                const int k0 = j * TN;
+                const int blk = blk_next;
+                const bool in = lane < 8 && k0 + lane * 16 < it.kend;
+                if (j + 1 < it.j1 && lane < 8 && k0 + TN + lane * 16 < it.kend)
+                    blk_next = __ldg(trow + (k0 + TN + lane * 16) / p.P);
+                if (round > 0 && !mbar_wait(&slot_empty[s], (round - 1) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                const bool okb = in && (unsigned)blk < (unsigned)p.N;
+                if (in && !okb && !isv) report(p.dev_status, WF_DEV_BAD_BLOCK);
+                const unsigned okm = __ballot_sync(0xffffffffu, okb);
+                if (lane == 0) mbar_arrive_expect_tx(&slot_full[s], (uint32_t)__popc(okm) * (uint32_t)L::BOX);
+                __syncwarp();
+                if (okb) {
+                    const int slot = blk * p.P + (k0 + lane * 16) % p.P;   // a multiple of 16
+                    unsigned char* dst = slot_ptr(s) + lane * L::BOX;
+                    if constexpr (L::NC == 2)
+                        tma_load_5d(dst, tm, 0, 0, 0, slot >> 3, it.h, &slot_full[s]);
+                    else
+                        tma_load_3d_nohint(dst, tm, 0, slot, it.h, &slot_full[s]);
+                }
+            }
+        }
+    } else if (warp == kAuxW) {
+        // ============================= query tiles, V finish =========================
+        int i = 0, nb = 0, g = 0;   // pieces, those with a second query tile, tiles so far
+        while (!misc[1] && walk.next(p, TN, it)) {
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                if (t == 1 && it.rows_tok <= tok_tile) continue;
+                const int prev = t == 0 ? i : nb;
+                if (prev > 0 && !mbar_wait(&q_empty[t], (prev - 1) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[t], (uint32_t)(L::NC * box_tok * p.G * 128));
+#pragma unroll
+                    for (int cb = 0; cb < L::NC; ++cb)
+                        tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64, it.h * p.G,
+                                           it.q_begin + it.qb * p.tokb + t * tok_tile, &q_full[t]);
+                }
+                __syncwarp();
+            }
+            const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
+            bool wild = false;
+            for (int j = it.j0; j < it.j1; ++j, ++g) {
+                const int k0 = j * TN;
+                const int x = g % L::VS;
+                const bool in = lane < 8 && k0 + lane * 16 < it.kend;
+                const int blk = in ? __ldg(trow + (k0 + lane * 16) / p.P) : -1;
+                const unsigned okm = __ballot_sync(0xffffffffu, (unsigned)blk < (unsigned)p.N);
+                if (!mbar_wait(&slot_full[L::KS + x], (g / L::VS) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                if (okm != 0xffu || k0 + TN > it.c) {
+                    unsigned char* base = slot_ptr(L::KS + x);
+                    // 16-byte chunk cc of row r (its place within the swizzle does not matter)
+                    const int r0 = min(TN, max(0, it.c - k0)), r1 = min(TN, it.kend - k0);
+                    // with every block id in range, the rows before the first draft stay as they are
+                    const int from = okm == (1u << ((r1 + 15) >> 4)) - 1u ? r0 : 0;
+                    for (int y = from * L::NC * 8 + lane; y < TN * L::NC * 8; y += 32) {
+                        const int r = y / (L::NC * 8), cb = (y >> 3) % L::NC, cc = y & 7;
+                        uint4* at = reinterpret_cast<uint4*>(base + (r >> 3) * L::ATOM + cb * L::HALF_OFF +
+                                                             (r & 7) * 128 + cc * 16);
+                        if (r >= r1 || !((okm >> (r >> 4)) & 1u)) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (r >= r0) {
+                            uint4 v = *at;
+                            bool w = tame(v.x);
+                            w |= tame(v.y);
+                            w |= tame(v.z);
+                            w |= tame(v.w);
+                            if (w) *at = v;
+                            wild |= w;
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                }
+                wild = __any_sync(0xffffffffu, wild);
+                if (lane == 0) {
+                    if (j + 1 == it.j1) misc[8 + (i & 7)] = wild ? 1 : 0;
+                    mbar_arrive(&v_ready[x]);
+                }
+            }
+            if (it.rows_tok > tok_tile) ++nb;
+            ++i;
+        }
+    } else if (warp == kMmaW) {
+        // ============================= MMA issue =====================================
+        // Per stream the products run in order S(0), P(0) V, S(1), P(1) V, ...: S(u + 1)
+        // overwrites the columns P(u) lives in, and the tensor core executes one thread's
+        // products in issue order.  Lane 0's observations decide, broadcast by shuffle, so
+        // control flow stays uniform.
+        constexpr uint32_t idS = tc::idesc_bf16_f32(TM, TN, 0, 0);
+        constexpr uint32_t idO = tc::idesc_bf16_f32(TM, D, 0, 1);
+        const uint64_t qdesc = tc::sdesc_sw128(smem_u32(smem + L::q), 16, 1024);
+        const uint64_t kdesc = tc::sdesc_sw128(smem_u32(smem + L::kv), 16, L::ATOM);
+        const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::kv), L::HALF_OFF, L::ATOM);
+        int g = 0, i = 0, nb = 0;
+        int gs[2] = {0, 0};
+        bool ok = true;
+        while (ok && walk.next(p, TN, it)) {
+            const int nt[2] = {steps(it, 0), steps(it, 1)};
+            int sq[2] = {0, 0}, sp[2] = {0, 0};
+            uint32_t idle = 0;
+            while (ok && (sp[0] < nt[0] || sp[1] < nt[1])) {
+                bool did = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int o = t ^ 1;
+                    const int u = sp[t];
+                    if (u < sq[t]) {
+                        const int gv = g + tile_at(t, u);
+                        const int x = gv % L::VS;
+                        const bool rdy = mbar_test(p_full(t), (gs[t] + u) & 1) &&
+                                         mbar_test(&v_ready[x], (gv / L::VS) & 1);
+                        if (__shfl_sync(0xffffffffu, (int)rdy, 0)) {
+                            tc::fence_after_sync();
+                            const uint32_t dO = tmem + L::OCOL + t * D;
+                            const uint32_t pcol = tmem + t * L::SCOL;
+                            const uint64_t vd = vdesc + (uint64_t)(((L::KS + x) * L::SLOT) >> 4);
+                            if (lane == 0) {
+#pragma unroll
+                                for (int kk = 0; kk < TN / 16; ++kk)
+                                    tc::mma_f16_tmem_a(dO, pcol + kk * 8 + (kk >= 4 ? 32 : 0),
+                                                       vd + (uint64_t)((kk * 2 * L::ATOM) >> 4), idO,
+                                                       (u > 0 || kk > 0) ? 1u : 0u);
+                                tc::commit(pv_done(t));
+                                if (QT == 1 || sp[o] > u || u >= nt[o]) tc::commit(&slot_empty[L::KS + x]);
+                            }
+                            __syncwarp();
+                            sp[t] = u + 1;
+                            did = true;
+                        }
+                    }
+                    const int j = sq[t];
+                    if (j < nt[t] && j == sp[t]) {
+                        const int gk = g + tile_at(t, j);
+                        const int ks = kslot(gk);
+                        const int tq = QT == 1 ? 0 : t;
+                        const bool rdy = mbar_test(&slot_full[ks], (gk / L::KS) & 1) &&
+                                         (j > 0 || mbar_test(&q_full[tq], (uint32_t)(tq == 0 ? i : nb) & 1u));
+                        if (__shfl_sync(0xffffffffu, (int)rdy, 0)) {
+                            tc::fence_after_sync();
+                            const uint32_t dS = tmem + t * L::SCOL;
+                            const uint64_t qd = qdesc + (uint64_t)((tq * L::QTILE) >> 4);
+                            const uint64_t kd = kdesc + (uint64_t)((ks * L::SLOT) >> 4);
+                            if (lane == 0) {
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
+                                    const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
+                                    tc::mma_f16(dS, qd + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS,
+                                                kk > 0 ? 1u : 0u);
+                                }
+                                tc::commit(s_full(t));
+                                if (QT == 1 || sq[o] > j || j >= nt[o]) tc::commit(&slot_empty[ks]);
+                                if (QT == 1 ? j + 1 + sq[o] == nt[0] + nt[1] : j + 1 == nt[t]) tc::commit(&q_empty[tq]);
+                            }
+                            __syncwarp();
+                            sq[t] = j + 1;
+                            did = true;
+                        }
+                    }
+                }
+                if (did) {
+                    idle = 0;
+                } else {
+                    if (misc[1] || ++idle > (1u << 24)) {
+                        if (lane == 0) fail();
+                        ok = false;
+                        break;
+                    }
+                    if (idle > 8) __nanosleep(32);
+                }
+            }
+            g += it.j1 - it.j0;
+            gs[0] += nt[0];
+            gs[1] += nt[1];
+            if (it.rows_tok > tok_tile) ++nb;
+            ++i;
+        }
+    } else {
+        // ============================= softmax =======================================
+        const int t = warp >> 2;
+        const int quad = warp & 3;
+        const int r = quad * 32 + lane;                  // TMEM lane
+        const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+        const uint32_t sbase = tmem + lane_addr + t * L::SCOL;
+        const uint32_t obase = tmem + lane_addr + L::OCOL + t * D;
+        const int tok = (QT == 2 ? t * tok_tile : 0) + r / p.G;
+        const bool row_fits = r < tok_tile * p.G;
+        const float scale = fabsf(p.scale_log2);
+        const bool negate = p.scale_log2 < 0.f;
+        int4 rec = make_int4(0, 0, 0, 0);
+        int gs = 0, i = 0;
+        bool ok = true;
+        while (ok && !misc[1] && walk.next(p, TN, it)) {
+            const int nt = steps(it, t);
+            const int tk = it.qb * p.tokb + tok;         // this row's draft
+            const bool row_valid = row_fits && tok < it.rows_tok;
+            const bool warp_live = __any_sync(0xffffffffu, row_valid);
+            const uint32_t* mrow = p.mask + (int64_t)(it.q_begin + (row_valid ? tk : 0)) * p.W;
+            const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
+            float m_ref = -INFINITY, l_run = 0.f;
+            for (int u = 0; u < nt; ++u) {
+                const int k0 = (it.j0 + tile_at(t, u)) * TN;
+                // positions of this tile that the row sees, when it is not all of them
+                const bool in = lane < 8 && k0 + lane * 16 < it.kend;
+                const int blk = warp_live && in ? __ldg(trow + (k0 + lane * 16) / p.P) : 0;
+                const unsigned okm = __ballot_sync(0xffffffffu, (unsigned)blk < (unsigned)p.N);
+                const bool masked = k0 + TN > it.c || okm != 0xffffffffu;
+                uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                if (warp_live && masked) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        vis[w] = row_valid ? mask_bits(mrow, p.W, k0 + 32 * w - it.c, it.n) : 0u;
+                        if (!((okm >> (2 * w)) & 1u)) vis[w] &= 0xffff0000u;
+                        if (!((okm >> (2 * w + 1)) & 1u)) vis[w] &= 0x0000ffffu;
+                    }
+                }
+                if (!mbar_wait(s_full(t), (gs + u) & 1)) {
+                    if (lane == 0) fail();
+                    ok = false;
+                    break;
+                }
+                if (warp_live) {
+                    tc::fence_after_sync();
+                    float m8[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
+                    auto load_half = [&](int hh, float (&s)[2][32]) {
+                        tc::ld_32cols(sbase + hh * 64, s[0]);
+                        tc::ld_32cols(sbase + hh * 64 + 32, s[1]);
+                        tc::wait_ld();
+                        if (negate) {
+#pragma unroll
+                            for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) s[c2][e] = -s[c2][e];
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    s[c2][e] = (vis[2 * hh + c2] >> e) & 1u ? s[c2][e] : -INFINITY;
+                        }
+                    };
+                    float s[2][32];
+                    load_half(0, s);
+#pragma unroll
+                    for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) m8[e & 7] = fmax3(m8[e & 7], s[c2][e], s[c2][e + 16]);
+                    load_half(1, s);
+#pragma unroll
+                    for (int c2 = 0; c2 < 2; ++c2)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) m8[e & 7] = fmax3(m8[e & 7], s[c2][e], s[c2][e + 16]);
+                    const float mraw = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                             fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+                    const float mt = mraw == -INFINITY ? -INFINITY : mraw * scale;
+                    float alpha = 1.f;
+                    if (m_ref == -INFINITY) {
+                        m_ref = mt;
+                    } else if (row_valid && mt > m_ref + kLazyMax) {
+                        alpha = ex2(m_ref - mt);
+                        m_ref = mt;
+                    }
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                        if (!mbar_wait(pv_done(t), (gs + u - 1) & 1)) fail();
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int c4 = 0; c4 < D / 32; ++c4) {
+                            float o[32];
+                            tc::ld_32cols(obase + c4 * 32, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tc::st_32cols(obase + c4 * 32, o);
+                        }
+                        tc::wait_st();
+                    }
+                    l_run *= alpha;
+                    const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+                    const float2 sc2 = make_float2(scale, scale);
+                    const float2 nm2 = make_float2(-m_use, -m_use);
+                    float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                    make_float2(0.f, 0.f)};
+                    auto weights = [&](int hh) {
+                        uint32_t pw[32];
+#pragma unroll
+                        for (int c2 = 0; c2 < 2; ++c2) {
+#pragma unroll
+                            for (int v = 0; v < 16; ++v) {
+                                const float2 x = __ffma2_rn(make_float2(s[c2][2 * v], s[c2][2 * v + 1]), sc2, nm2);
+                                const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
+                                ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
+                                pw[c2 * 16 + v] = pack_bf16x2(e2.x, e2.y);
+                            }
+                        }
+                        tc::st_32words(sbase + hh * 64, pw);
+                    };
+                    weights(1);
+                    load_half(0, s);
+                    weights(0);
+                    tc::wait_st();
+                    const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
+                    const float2 pst = __fadd2_rn(ps01, ps23);
+                    l_run += pst.x + pst.y;
+                    tc::fence_before_sync();
+                }
+                __syncwarp();
+                // the first P of a piece lets P V overwrite O, which the last piece's join reads
+                if (QT == 1 && u == 0 && i > 0 && !mbar_wait(x_done, (i - 1) & 1)) {
+                    if (lane == 0) fail();
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive(p_full(t));
+            }
+            if (!ok) break;
+            // ---- epilogue: the rows, or this piece of them ------------------------------
+            if (nt > 0 && !mbar_wait(pv_done(t), (gs + nt - 1) & 1)) {
+                if (lane == 0) fail();
+                break;
+            }
+            gs += nt;
+            const bool whole = it.j0 == 0 && it.j1 == it.nt;
+            float w0 = 1.f, w1 = 0.f;                     // weights of the streams' O (QT = 1)
+            const float2* ml = reinterpret_cast<const float2*>(smem + L::ml);
+            if constexpr (QT == 1) {
+                if (nt == 0 && i > 0 && !mbar_wait(x_done, (i - 1) & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                reinterpret_cast<float2*>(smem + L::ml)[t * TM + r] = make_float2(m_ref, l_run);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_ready);
+                if (!mbar_wait(x_ready, i & 1)) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                const float2 a = ml[r], b = ml[TM + r];
+                const float mm = fmaxf(a.x, b.x);
+                // a stream without a maximum has a sum and an O of 0, or of NaN, which has to stay
+                w0 = a.x == -INFINITY ? 1.f : ex2(a.x - mm);
+                w1 = b.x == -INFINITY ? 1.f : ex2(b.x - mm);
+                m_ref = mm;
+                l_run = w0 * a.y + w1 * b.y;
+            }
+            tc::fence_after_sync();
+            const bool both = QT == 1 && it.j1 - it.j0 > 1;    // stream 1 has an O
+            const bool wild = misc[8 + (i & 7)] != 0;
+            const int piece = tree_piece_slot(cta, it.j0);
+            const int64_t wrow = (int64_t)piece * p.rows + tok * p.G + r % p.G;
+            if (!whole) {
+                if (it.j0 == 0 && threadIdx.x == 0) rec = tree_record(p, *st, it, cta);
+                if (row_valid && (QT == 2 || t == 0)) p.ws_ml[wrow] = make_float2(m_ref, l_run);
+            }
+            const float f = !whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;
+            const int64_t orow = (int64_t)(it.q_begin + tk) * p.H_q + it.h * p.G + r % p.G;
+            if (nt > 0 || QT == 1) {
+                constexpr int kHalf = QT == 1 ? D / 64 : D / 32;   // 32-column groups of this warp
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c) {
+                    const int col = (QT == 1 ? t * (D / 2) : 0) + c * 32;
+                    float o[32];
+                    if (warp_live) {
+                        if constexpr (QT == 1) {
+                            float o1[32];
+                            tc::ld_32cols(tmem + lane_addr + L::OCOL + col, o);
+                            if (both) tc::ld_32cols(tmem + lane_addr + L::OCOL + D + col, o1);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                o[e] *= w0;
+                                if (both) o[e] += w1 * o1[e];
+                            }
+                        } else {
+                            tc::ld_32cols(obase + col, o);
+                            tc::wait_ld();
+                        }
+                    }
+                    if (!row_valid) continue;
+                    if (wild) {
+                        // drafts whose V row is not finite: what was zeroed for P V, added to the
+                        // rows that see them
+                        const int d0 = max(0, it.j0 * TN - it.c), d1 = min(it.n, it.j1 * TN - it.c);
+                        for (int d = d0; d < d1; ++d) {
+                            const int pos = it.c + d;
+                            const int blk = __ldg(trow + pos / p.P);
+                            if ((unsigned)blk >= (unsigned)p.N || !tree_bit(p, it.q_begin + tk, d)) continue;
+                            const int64_t slot = (int64_t)blk * p.P + pos % p.P;
+                            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_pool) +
+                                                     (slot * p.H_kv + it.h) * D + col;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float x = __bfloat162float(v[e]);
+                                if (!(fabsf(x) < INFINITY)) o[e] += x;
+                            }
+                        }
+                    }
+                    if (l_run == 0.f) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                    if (whole) {
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + orow * D + col;
+#pragma unroll
+                        for (int e8 = 0; e8 < 4; ++e8)
+                            *reinterpret_cast<uint4*>(dst + e8 * 8) =
+                                make_uint4(pack_bf16x2(o[e8 * 8 + 0] * f, o[e8 * 8 + 1] * f),
+                                           pack_bf16x2(o[e8 * 8 + 2] * f, o[e8 * 8 + 3] * f),
+                                           pack_bf16x2(o[e8 * 8 + 4] * f, o[e8 * 8 + 5] * f),
+                                           pack_bf16x2(o[e8 * 8 + 6] * f, o[e8 * 8 + 7] * f));
+                    } else {
+                        float* dst = p.ws_o + wrow * D + col;
+#pragma unroll
+                        for (int e4 = 0; e4 < 8; ++e4)
+                            *reinterpret_cast<float4*>(dst + e4 * 4) =
+                                make_float4(o[e4 * 4], o[e4 * 4 + 1], o[e4 * 4 + 2], o[e4 * 4 + 3]);
+                    }
+                }
+            }
+            // O (and the streams' sums) are read: the next piece may overwrite them
+            tc::fence_before_sync();
+            if constexpr (QT == 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_done);
+            }
+            ++i;
+        }
+        if (threadIdx.x == 0) p.ws_rec[cta] = rec;
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaW) {
+        __syncwarp();
+        tc::fence_after_sync();
+        tc::dealloc(tmem, L::TMEM_COLS);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <int D, int QT>
+cudaError_t launch_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                      int box_tok, int ctas, cudaStream_t stream) {
+    auto kern = paged_tree_tc_kernel<D, QT>;
+    const int smem = TtLayout<D, QT>::total;
+    cudaError_t err = allow_dynamic_smem((const void*)kern, smem);
+    if (err != cudaSuccess) return err;
+    kern<<<ctas, kTcThreads, smem, stream>>>(tq, tk, tv, p, box_tok);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads) {
+    if (pool.dtype != WF_DTYPE_BF16 || pool.block_size % 16 != 0) return false;
+    // slots are TMA coordinates
+    return (int64_t)pool.num_blocks * pool.block_size <= INT32_MAX && num_q_heads / pool.num_kv_heads <= 8;
+}
+
+// Units of at most 128 rows: two streams over the same rows; else two query tiles.
+TreeShape tree_tc_shape(int G, int max_q_len) {
+    const int tok = TM / G;
+    const int qt = max_q_len <= tok ? 1 : 2;
+    return TreeShape{qt * TM, qt * tok, TN, 1};
+}
+
+cudaError_t launch_tree_tc(const TreeParams& p, int D, int ctas, cudaStream_t stream) {
+    const int tok = TM / p.G;
+    const int box_tok = p.max_q_len < tok ? p.max_q_len : tok;   // drafts of a query tile's box
+    CUtensorMap tq, tk, tv;
+    cudaError_t e;
+    {
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.H_q, (uint64_t)p.total_q};
+        const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)p.H_q * D * 2};
+        const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)box_tok};
+        e = encode_tiled_bf16(&tq, const_cast<void*>(p.q), 3, dims, strides, box);
+        if (e != cudaSuccess) return e;
+    }
+    const uint64_t slots = (uint64_t)p.N * p.P;
+    const uint64_t row = (uint64_t)p.H_kv * D * 2;   // bytes of one pool slot
+    if (D == 128) {
+        // (d 0-63, slot % 8, d half, slot / 8, head): a 16-slot box of one head holds both
+        // halves of D as [slot/8 % 2][half][slot % 8][64]
+        const uint64_t dims[5] = {64, 8, 2, slots / 8, (uint64_t)p.H_kv};
+        const uint64_t strides[4] = {row, 128, 8 * row, (uint64_t)D * 2};
+        const uint32_t box[5] = {64, 8, 2, 2, 1};
+        e = encode_tiled_bf16(&tk, const_cast<void*>(p.k_pool), 5, dims, strides, box);
+        if (e == cudaSuccess) e = encode_tiled_bf16(&tv, const_cast<void*>(p.v_pool), 5, dims, strides, box);
+    } else {
+        const uint64_t dims[3] = {(uint64_t)D, slots, (uint64_t)p.H_kv};
+        const uint64_t strides[2] = {row, (uint64_t)D * 2};
+        const uint32_t box[3] = {64, 16, 1};
+        e = encode_tiled_bf16(&tk, const_cast<void*>(p.k_pool), 3, dims, strides, box);
+        if (e == cudaSuccess) e = encode_tiled_bf16(&tv, const_cast<void*>(p.v_pool), 3, dims, strides, box);
+    }
+    if (e != cudaSuccess) return e;
+    const bool one = p.rows == TM;
+    if (D == 128)
+        return one ? launch_tc<128, 1>(tq, tk, tv, p, box_tok, ctas, stream)
+                   : launch_tc<128, 2>(tq, tk, tv, p, box_tok, ctas, stream);
+    return one ? launch_tc<64, 1>(tq, tk, tv, p, box_tok, ctas, stream)
+               : launch_tc<64, 2>(tq, tk, tv, p, box_tok, ctas, stream);
+}
+
+}  // namespace wf
