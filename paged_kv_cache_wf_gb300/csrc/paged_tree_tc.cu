@@ -16,8 +16,10 @@
 //           half of the columns.
 //   QT = 2  (up to 256 rows a unit): one 128-row query tile each, on the same tiles, so
 //           a loaded tile serves 256 rows.
-// 12 warps: 0-7 softmax (stream t = warp / 4), 8 K loads, 9 V loads, 10 query tiles and
-// the V tiles' finish, 11 MMA issue.
+// 16 warps: 0-7 softmax (stream t = warp / 4), 8 K loads, 9 V loads, 10 the walk over the
+// CTA's pieces (a ring of records that the other warps read) and the query tiles, 11 and
+// 12 MMA issue (a stream each), 13-15 the V tiles' finish.  The softmax warps take
+// registers from the others.
 // The finish of a V tile: a weight of 0 hides a position only from finite values (0 *
 // NaN is NaN in P V).  Rows past the request's end or of a bad block are zeroed; an
 // element of a draft's row that is not finite is zeroed too, and the epilogue adds it
@@ -33,8 +35,28 @@ namespace {
 constexpr int TM = 128;           // rows of a query tile (TMEM lanes)
 constexpr int TN = 128;           // positions of a tile
 constexpr float kLazyMax = 8.f;   // rescale O only when a row's maximum grows by more than 2^8
-constexpr int kSoftW = 8, kKW = 8, kVW = 9, kAuxW = 10, kMmaW = 11;
-constexpr int kTcThreads = 12 * 32;
+constexpr int kSoftW = 8, kKW = 8, kVW = 9, kWalkW = 10, kMmaW = 11, kFinW = 13, kFin = 3;
+constexpr int kTcThreads = (kFinW + kFin) * 32;
+constexpr int kSoftRegs = 184, kOtherRegs = 72;
+static_assert(kTcThreads / 2 * (kSoftRegs + kOtherRegs) <= 65536, "register split exceeds the block's registers");
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A piece as the warps read it; nt = 0 ends the list.
+constexpr int kRing = 8;
+struct PieceRec {
+    int b, h, q_row, n;      // request, KV head, first row of q of the row block, drafts of the request
+    int tok0, rows_tok;      // first draft of the row block, drafts in it
+    int c, kend;             // cached positions, all positions
+    int j0, j1, nt, last;    // tiles [j0, j1) of nt; last CTA with a piece of the unit
+};
 
 template <int D, int QT>
 struct TtLayout {
@@ -44,20 +66,25 @@ struct TtLayout {
     static constexpr int ATOM = NC == 2 ? 2048 : 1024;   // stride between 8-position atoms
     static constexpr int HALF_OFF = 1024;                // offset of the second 64-wide half
     static constexpr int BOX = NC * 2048;                // one 16-position box
-    static constexpr int KS = QT == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 5);
-    static constexpr int VS = KS;
+    static constexpr int KS = D == 128 ? (QT == 1 ? 3 : 2) : 5;
+    static constexpr int VS = D == 128 ? 2 : 5;
     static constexpr int NSLOT = KS + VS;
     static constexpr int q = 0;
     static constexpr int kv = QT * QTILE;
-    static constexpr int ml = kv + NSLOT * SLOT;         // QT = 1: (m, l) of both streams' rows
+    static constexpr int stage = kv + NSLOT * SLOT;      // a 32 x 32 fp32 block a softmax warp, for whole-line stores
+    static constexpr int ml = stage + kSoftW * 4096;     // QT = 1: (m, l) of both streams' rows
     static constexpr int bars = ml + (QT == 1 ? 2 * TM * 8 : 0);
     // q_full[QT], q_empty[QT], slot_full[NSLOT], slot_empty[NSLOT], v_ready[VS], per
     // stream s_full, p_full, pv_done, then x_ready, x_done
-    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 6 + 2;
-    static constexpr int start = bars + nbars * 8;
+    // and piece_full[kRing], piece_empty[kRing]
+    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 6 + 2 + 2 * kRing;
+    static constexpr int ring = bars + nbars * 8;        // [kRing] records of pieces
+    static constexpr int start = ring + kRing * (int)sizeof(PieceRec);
     static constexpr int scratch = start + (int)sizeof(TreeStart);
-    static constexpr int misc = scratch + 12 * 8;        // [0] TMEM address, [1] abort, [8..15] wild drafts of a piece
-    static constexpr int total = misc + 64;
+    static constexpr int misc = scratch + 16 * 8;        // [0] TMEM address, [1] abort
+    static constexpr int wild = misc + 16;               // [kRing]: a byte a finishing warp
+    static constexpr int okm = wild + kRing * 4;         // [16 tiles]: boxes with a good block id
+    static constexpr int total = okm + 16;
     static constexpr int SCOL = 128, OCOL = 256, TMEM_COLS = 512;
     static_assert(total <= 232448, "tree CTA exceeds shared memory");
 };
@@ -106,14 +133,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto pv_done = [&](int t) { return tb + t * 3 + 2; };
     uint64_t* x_ready = tb + 6;
     uint64_t* x_done = x_ready + 1;
+    uint64_t* piece_full = x_done + 1;
+    uint64_t* piece_empty = piece_full + kRing;
+    PieceRec* ring = reinterpret_cast<PieceRec*>(smem + L::ring);
     TreeStart* st = reinterpret_cast<TreeStart*>(smem + L::start);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::misc);
     auto fail = [&]() {
         report(p.dev_status, WF_DEV_TIMEOUT);
         misc[1] = 1;
     };
-    auto kslot = [&](int g) { return g % L::KS; };
-    auto vslot = [&](int g) { return L::KS + g % L::VS; };
     auto slot_ptr = [&](int s) { return smem + L::kv + s * L::SLOT; };
 
     if (warp == kMmaW) {
@@ -123,13 +151,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         for (int t = 0; t < QT; ++t) {
             mbar_init(&q_full[t], 1);
-            mbar_init(&q_empty[t], 1);
+            mbar_init(&q_empty[t], QT == 1 ? 2 : 1);
         }
         for (int i = 0; i < L::NSLOT; ++i) {
             mbar_init(&slot_full[i], 1);
-            mbar_init(&slot_empty[i], 1);
+            mbar_init(&slot_empty[i], QT);   // QT = 1: a tile belongs to one stream
         }
-        for (int i = 0; i < L::VS; ++i) mbar_init(&v_ready[i], 1);
+        for (int i = 0; i < L::VS; ++i) mbar_init(&v_ready[i], kFin);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
             mbar_init(p_full(t), 4);
@@ -137,8 +165,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         mbar_init(x_ready, kSoftW);
         mbar_init(x_done, kSoftW);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&piece_full[i], 1);
+            mbar_init(&piece_empty[i], kTcThreads / 32 - 1);
+        }
         fence_mbar_init();
         misc[1] = 0;
+        for (int i = 0; i < kRing * 4; ++i) smem[L::wild + i] = 0;
     }
     tc::fence_before_sync();
     tree_begin(p, TN, cta, gridDim.x, st, reinterpret_cast<int64_t*>(smem + L::scratch));
@@ -147,93 +180,183 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int tok_tile = TM / p.G;                       // drafts of a query tile
     // steps of stream t over a piece of nt tiles (QT = 2: t's query tile may be empty),
     // and the tile of its step u
-    auto steps = [&](const TreePiece& it, int t) {
+    auto steps = [&](const PieceRec& it, int t) {
         const int nt = it.j1 - it.j0;
         if constexpr (QT == 1) return (nt + 1 - t) >> 1;
         return t == 0 || it.rows_tok > tok_tile ? nt : 0;
     };
     auto tile_at = [&](int t, int u) { return QT == 1 ? 2 * u + t : u; };
-    TreeWalk walk(*st);
-    TreePiece it;
-
+    volatile unsigned char* wild_of = smem + L::wild;
+    volatile unsigned char* okm_of = smem + L::okm;
+    // the record of piece i, when it is there: false ends a warp's loop
+    auto piece = [&](int i) -> bool {
+        if (misc[1]) return false;
+        if (!mbar_wait(&piece_full[i % kRing], (i / kRing) & 1)) {
+            if (lane == 0) fail();
+            return false;
+        }
+        return ring[i % kRing].nt != 0;
+    };
+    auto piece_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_empty[i % kRing]);
+    };
+    if (warp >= kSoftW) {
+    regs_down<kOtherRegs>();
     if (warp == kKW || warp == kVW) {
         // ============================= K and V loads =================================
         // one 16-position box a lane; block ids are read one tile ahead
         const bool isv = warp == kVW;
         const CUtensorMap* tm = isv ? &tm_v : &tm_k;
-        int g = 0;
-        while (!misc[1] && walk.next(p, TN, it)) {
+        const int nslots = isv ? L::VS : L::KS;
+        unsigned char* slots = slot_ptr(isv ? L::KS : 0);
+        uint64_t* full = slot_full + (isv ? L::KS : 0);
+        uint64_t* empty = slot_empty + (isv ? L::KS : 0);
+        int x = 0, g = 0;       // slot and number of the next tile
+        uint32_t par = 1;       // parity of the slot's last release: 1 passes before the first
+        bool ok = true;
+        for (int i = 0; ok && piece(i); ++i) {
+            const PieceRec& it = ring[i % kRing];
             const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
-            int blk_next = 0;
-            if (lane < 8 && it.j0 * TN + lane * 16 < it.kend) blk_next = __ldg(trow + (it.j0 * TN + lane * 16) / p.P);
-            for (int j = it.j0; j < it.j1; ++j, ++g) {
-                const int s = isv ? vslot(g) : kslot(g);
-                const int round = isv ? g / L::VS : g / L::KS;
-                const int k0 = j * TN;
+            const int h = it.h, kend = it.kend;
+            int pos = it.j0 * TN + lane * 16;
+            int left = it.j1 - it.j0;
+            int blk_next = lane < 8 && pos < kend ? __ldg(trow + pos / p.P) : 0;
+#pragma unroll 1
+            for (; left > 0; --left, pos += TN, ++g) {
                 const int blk = blk_next;
-                const bool in = lane < 8 && k0 + lane * 16 < it.kend;
-                if (j + 1 < it.j1 && lane < 8 && k0 + TN + lane * 16 < it.kend)
-                    blk_next = __ldg(trow + (k0 + TN + lane * 16) / p.P);
-                if (round > 0 && !mbar_wait(&slot_empty[s], (round - 1) & 1)) {
+                const bool in = lane < 8 && pos < kend;
+                if (left > 1 && lane < 8 && pos + TN < kend) blk_next = __ldg(trow + (pos + TN) / p.P);
+                if (!mbar_wait(&empty[x], par)) {
                     if (lane == 0) fail();
+                    ok = false;
                     break;
                 }
                 const bool okb = in && (unsigned)blk < (unsigned)p.N;
                 if (in && !okb && !isv) report(p.dev_status, WF_DEV_BAD_BLOCK);
                 const unsigned okm = __ballot_sync(0xffffffffu, okb);
-                if (lane == 0) mbar_arrive_expect_tx(&slot_full[s], (uint32_t)__popc(okm) * (uint32_t)L::BOX);
+                if (lane == 0) {
+                    // 16 tiles on, the tensor core and the softmax are past this one
+                    if (!isv) okm_of[g & 15] = (unsigned char)okm;
+                    mbar_arrive_expect_tx(&full[x], (uint32_t)__popc(okm) * (uint32_t)L::BOX);
+                }
                 __syncwarp();
                 if (okb) {
-                    const int slot = blk * p.P + (k0 + lane * 16) % p.P;   // a multiple of 16
-                    unsigned char* dst = slot_ptr(s) + lane * L::BOX;
+                    const int slot = blk * p.P + pos % p.P;   // a multiple of 16
+                    unsigned char* dst = slots + x * L::SLOT + lane * L::BOX;
                     if constexpr (L::NC == 2)
-                        tma_load_5d(dst, tm, 0, 0, 0, slot >> 3, it.h, &slot_full[s]);
+                        tma_load_5d(dst, tm, 0, 0, 0, slot >> 3, h, &full[x]);
                     else
-                        tma_load_3d_nohint(dst, tm, 0, slot, it.h, &slot_full[s]);
+                        tma_load_3d_nohint(dst, tm, 0, slot, h, &full[x]);
+                }
+                if (++x == nslots) {
+                    x = 0;
+                    par ^= 1;
                 }
             }
+            piece_done(i);
         }
-    } else if (warp == kAuxW) {
-        // ============================= query tiles, V finish =========================
-        int i = 0, nb = 0, g = 0;   // pieces, those with a second query tile, tiles so far
-        while (!misc[1] && walk.next(p, TN, it)) {
+    } else if (warp == kWalkW) {
+        // ============================= walk, query tiles =============================
+        // publishes records as far ahead as the ring allows and loads each piece's query
+        // tiles once the products that read the tiles before are done
+        TreeWalk walk(*st);
+        TreePiece it;
+        bool more = true;
+        int made = 0, asked = 0, second = 0;   // records, pieces whose tiles are asked for, second tiles
+        int t = 0;
+        uint32_t idle = 0;
+        while (!misc[1] && (more || asked < made)) {
+            bool did = false;
+            if (more && (made < kRing || __shfl_sync(0xffffffffu, (int)mbar_test(&piece_empty[made % kRing],
+                                                                                  (made / kRing - 1) & 1), 0))) {
+                more = walk.next(p, TN, it);
+                if (lane == 0) {
+                    PieceRec& e = ring[made % kRing];
+                    e.nt = more ? it.nt : 0;
+                    if (more) {
+                        e.b = it.b;
+                        e.h = it.h;
+                        e.tok0 = it.qb * p.tokb;
+                        e.q_row = it.q_begin + e.tok0;
+                        e.n = it.n;
+                        e.rows_tok = it.rows_tok;
+                        e.c = it.c;
+                        e.kend = it.kend;
+                        e.j0 = it.j0;
+                        e.j1 = it.j1;
+                        e.last = it.j0 == 0 && it.j1 < it.nt ? tree_record(p, *st, it, cta).z : 0;
+                    }
+                    mbar_arrive(&piece_full[made % kRing]);
+                }
+                __syncwarp();
+                if (more) ++made;
+                did = true;
+            }
+            if (asked < made) {
+                const PieceRec& e = ring[asked % kRing];
+                const int prev = t == 0 ? asked : second;
+                if (prev == 0 || __shfl_sync(0xffffffffu, (int)mbar_test(&q_empty[t], (prev - 1) & 1), 0)) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&q_full[t], (uint32_t)(L::NC * box_tok * p.G * 128));
 #pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                if (t == 1 && it.rows_tok <= tok_tile) continue;
-                const int prev = t == 0 ? i : nb;
-                if (prev > 0 && !mbar_wait(&q_empty[t], (prev - 1) & 1)) {
+                        for (int cb = 0; cb < L::NC; ++cb)
+                            tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64, e.h * p.G,
+                                               e.q_row + t * tok_tile, &q_full[t]);
+                    }
+                    __syncwarp();
+                    if (QT == 2 && t == 0 && e.rows_tok > tok_tile) {
+                        t = 1;
+                    } else {
+                        second += t;
+                        t = 0;
+                        ++asked;
+                    }
+                    did = true;
+                }
+            }
+            if (did) {
+                idle = 0;
+            } else {
+                if (++idle > (1u << 24)) {
                     if (lane == 0) fail();
                     break;
                 }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[t], (uint32_t)(L::NC * box_tok * p.G * 128));
-#pragma unroll
-                    for (int cb = 0; cb < L::NC; ++cb)
-                        tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64, it.h * p.G,
-                                           it.q_begin + it.qb * p.tokb + t * tok_tile, &q_full[t]);
-                }
-                __syncwarp();
+                __nanosleep(64);
             }
+        }
+    } else if (warp >= kFinW) {
+        // ============================= V finish ======================================
+        // a third of a tile's rows each, dealt in turn
+        const int fw = warp - kFinW;
+        int x = 0;           // slot
+        uint32_t par = 0;
+        bool ok = true;
+        for (int i = 0; ok && piece(i); ++i) {
+            const PieceRec& it = ring[i % kRing];
             const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
             bool wild = false;
-            for (int j = it.j0; j < it.j1; ++j, ++g) {
+#pragma unroll 1
+            for (int j = it.j0; j < it.j1; ++j) {
                 const int k0 = j * TN;
-                const int x = g % L::VS;
                 const bool in = lane < 8 && k0 + lane * 16 < it.kend;
                 const int blk = in ? __ldg(trow + (k0 + lane * 16) / p.P) : -1;
                 const unsigned okm = __ballot_sync(0xffffffffu, (unsigned)blk < (unsigned)p.N);
-                if (!mbar_wait(&slot_full[L::KS + x], (g / L::VS) & 1)) {
+                if (!mbar_wait(&slot_full[L::KS + x], par)) {
                     if (lane == 0) fail();
+                    ok = false;
                     break;
                 }
                 if (okm != 0xffu || k0 + TN > it.c) {
                     unsigned char* base = slot_ptr(L::KS + x);
-                    // 16-byte chunk cc of row r (its place within the swizzle does not matter)
+                    // 16-byte chunk cc of row r (its place within the swizzle does not matter);
+                    // with every block id in range, the rows before the first draft stay
                     const int r0 = min(TN, max(0, it.c - k0)), r1 = min(TN, it.kend - k0);
-                    // with every block id in range, the rows before the first draft stay as they are
-                    const int from = okm == (1u << ((r1 + 15) >> 4)) - 1u ? r0 : 0;
-                    for (int y = from * L::NC * 8 + lane; y < TN * L::NC * 8; y += 32) {
-                        const int r = y / (L::NC * 8), cb = (y >> 3) % L::NC, cc = y & 7;
+                    const int first = okm == (1u << ((r1 + 15) >> 4)) - 1u ? r0 : 0;
+                    constexpr int kRowChunks = L::NC * 8;
+                    constexpr int kStep = 32 / kRowChunks;   // rows a warp covers at once
+                    const int rr = lane / kRowChunks, cb = (lane >> 3) % L::NC, cc = lane & 7;
+                    for (int r = first + fw * kStep + rr; r < TN; r += kFin * kStep) {
                         uint4* at = reinterpret_cast<uint4*>(base + (r >> 3) * L::ATOM + cb * L::HALF_OFF +
                                                              (r & 7) * 128 + cc * 16);
                         if (r >= r1 || !((okm >> (r >> 4)) & 1u)) {
@@ -252,146 +375,142 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 wild = __any_sync(0xffffffffu, wild);
                 if (lane == 0) {
-                    if (j + 1 == it.j1) misc[8 + (i & 7)] = wild ? 1 : 0;
+                    if (j + 1 == it.j1) wild_of[(i % kRing) * 4 + fw] = wild ? 1 : 0;
                     mbar_arrive(&v_ready[x]);
                 }
-            }
-            if (it.rows_tok > tok_tile) ++nb;
-            ++i;
-        }
-    } else if (warp == kMmaW) {
-        // ============================= MMA issue =====================================
-        // Per stream the products run in order S(0), P(0) V, S(1), P(1) V, ...: S(u + 1)
-        // overwrites the columns P(u) lives in, and the tensor core executes one thread's
-        // products in issue order.  Lane 0's observations decide, broadcast by shuffle, so
-        // control flow stays uniform.
-        constexpr uint32_t idS = tc::idesc_bf16_f32(TM, TN, 0, 0);
-        constexpr uint32_t idO = tc::idesc_bf16_f32(TM, D, 0, 1);
-        const uint64_t qdesc = tc::sdesc_sw128(smem_u32(smem + L::q), 16, 1024);
-        const uint64_t kdesc = tc::sdesc_sw128(smem_u32(smem + L::kv), 16, L::ATOM);
-        const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::kv), L::HALF_OFF, L::ATOM);
-        int g = 0, i = 0, nb = 0;
-        int gs[2] = {0, 0};
-        bool ok = true;
-        while (ok && walk.next(p, TN, it)) {
-            const int nt[2] = {steps(it, 0), steps(it, 1)};
-            int sq[2] = {0, 0}, sp[2] = {0, 0};
-            uint32_t idle = 0;
-            while (ok && (sp[0] < nt[0] || sp[1] < nt[1])) {
-                bool did = false;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int o = t ^ 1;
-                    const int u = sp[t];
-                    if (u < sq[t]) {
-                        const int gv = g + tile_at(t, u);
-                        const int x = gv % L::VS;
-                        const bool rdy = mbar_test(p_full(t), (gs[t] + u) & 1) &&
-                                         mbar_test(&v_ready[x], (gv / L::VS) & 1);
-                        if (__shfl_sync(0xffffffffu, (int)rdy, 0)) {
-                            tc::fence_after_sync();
-                            const uint32_t dO = tmem + L::OCOL + t * D;
-                            const uint32_t pcol = tmem + t * L::SCOL;
-                            const uint64_t vd = vdesc + (uint64_t)(((L::KS + x) * L::SLOT) >> 4);
-                            if (lane == 0) {
-#pragma unroll
-                                for (int kk = 0; kk < TN / 16; ++kk)
-                                    tc::mma_f16_tmem_a(dO, pcol + kk * 8 + (kk >= 4 ? 32 : 0),
-                                                       vd + (uint64_t)((kk * 2 * L::ATOM) >> 4), idO,
-                                                       (u > 0 || kk > 0) ? 1u : 0u);
-                                tc::commit(pv_done(t));
-                                if (QT == 1 || sp[o] > u || u >= nt[o]) tc::commit(&slot_empty[L::KS + x]);
-                            }
-                            __syncwarp();
-                            sp[t] = u + 1;
-                            did = true;
-                        }
-                    }
-                    const int j = sq[t];
-                    if (j < nt[t] && j == sp[t]) {
-                        const int gk = g + tile_at(t, j);
-                        const int ks = kslot(gk);
-                        const int tq = QT == 1 ? 0 : t;
-                        const bool rdy = mbar_test(&slot_full[ks], (gk / L::KS) & 1) &&
-                                         (j > 0 || mbar_test(&q_full[tq], (uint32_t)(tq == 0 ? i : nb) & 1u));
-                        if (__shfl_sync(0xffffffffu, (int)rdy, 0)) {
-                            tc::fence_after_sync();
-                            const uint32_t dS = tmem + t * L::SCOL;
-                            const uint64_t qd = qdesc + (uint64_t)((tq * L::QTILE) >> 4);
-                            const uint64_t kd = kdesc + (uint64_t)((ks * L::SLOT) >> 4);
-                            if (lane == 0) {
-#pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk) {
-                                    const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
-                                    const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
-                                    tc::mma_f16(dS, qd + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS,
-                                                kk > 0 ? 1u : 0u);
-                                }
-                                tc::commit(s_full(t));
-                                if (QT == 1 || sq[o] > j || j >= nt[o]) tc::commit(&slot_empty[ks]);
-                                if (QT == 1 ? j + 1 + sq[o] == nt[0] + nt[1] : j + 1 == nt[t]) tc::commit(&q_empty[tq]);
-                            }
-                            __syncwarp();
-                            sq[t] = j + 1;
-                            did = true;
-                        }
-                    }
-                }
-                if (did) {
-                    idle = 0;
-                } else {
-                    if (misc[1] || ++idle > (1u << 24)) {
-                        if (lane == 0) fail();
-                        ok = false;
-                        break;
-                    }
-                    if (idle > 8) __nanosleep(32);
+                if (++x == L::VS) {
+                    x = 0;
+                    par ^= 1;
                 }
             }
-            g += it.j1 - it.j0;
-            gs[0] += nt[0];
-            gs[1] += nt[1];
-            if (it.rows_tok > tok_tile) ++nb;
-            ++i;
+            piece_done(i);
         }
     } else {
+        // ============================= MMA issue =====================================
+        // One warp a stream: its products run in order S(0), P(0) V, S(1), P(1) V, ...: S(u + 1)
+        // overwrites the columns P(u) lives in, and the tensor core executes one thread's
+        // products in issue order.  One issuer for both streams was the bound at 16 products a
+        // tile and stream.
+        constexpr uint32_t idS = tc::idesc_bf16_f32(TM, TN, 0, 0);
+        constexpr uint32_t idO = tc::idesc_bf16_f32(TM, D, 0, 1);
+        const int t = warp - kMmaW;
+        const int tq = QT == 1 ? 0 : t;
+        const uint64_t qdesc = tc::sdesc_sw128(smem_u32(smem + L::q + tq * L::QTILE), 16, 1024);
+        const uint64_t kdesc = tc::sdesc_sw128(smem_u32(smem + L::kv), 16, L::ATOM);
+        const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::kv + L::KS * L::SLOT), L::HALF_OFF, L::ATOM);
+        const uint32_t dS = tmem + t * L::SCOL, dO = tmem + L::OCOL + t * D;
+        int kx = 0, vx = 0;                 // slots of the next tile
+        uint32_t kpar = 0, vpar = 0;        // and their parities
+        uint32_t qpar = 0, ppar = 0;
+        bool ok = true;
+        auto need = [&](uint64_t* bar, uint32_t par) {
+            if (ok && !mbar_wait(bar, par)) {
+                if (lane == 0) fail();
+                ok = false;
+            }
+            return ok;
+        };
+        auto step = [&](int& x, uint32_t& par, int n) {
+            if (++x == n) {
+                x = 0;
+                par ^= 1;
+            }
+        };
+        for (int i = 0; ok && piece(i); ++i) {
+            const PieceRec& it = ring[i % kRing];
+            const int nt = steps(it, t), all = it.j1 - it.j0;
+            if (QT == 2 && nt == 0) {       // no rows: hand the tiles on as they land
+                for (int u = 0; u < all && ok; ++u) {
+                    if (need(&slot_full[kx], kpar) && lane == 0) mbar_arrive(&slot_empty[kx]);
+                    if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&slot_empty[L::KS + vx]);
+                    step(kx, kpar, L::KS);
+                    step(vx, vpar, L::VS);
+                }
+                piece_done(i);
+                continue;
+            }
+            if (!need(&q_full[tq], qpar)) break;
+            qpar ^= 1;
+            if (nt == 0 && lane == 0) mbar_arrive(&q_empty[tq]);
+            if (QT == 1 && t == 1) {        // the first tile is stream 0's
+                step(kx, kpar, L::KS);
+                step(vx, vpar, L::VS);
+            }
+#pragma unroll 1
+            for (int u = 0; u < nt && ok; ++u) {
+                if (!need(&slot_full[kx], kpar)) break;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint64_t kd = kdesc + (uint64_t)((kx * L::SLOT) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
+                        const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
+                        tc::mma_f16(dS, qdesc + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS, kk > 0 ? 1u : 0u);
+                    }
+                    tc::commit(s_full(t));
+                    tc::commit(&slot_empty[kx]);
+                    if (u + 1 == nt) tc::commit(&q_empty[tq]);
+                }
+                __syncwarp();
+                if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
+                ppar ^= 1;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint64_t vd = vdesc + (uint64_t)((vx * L::SLOT) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < TN / 16; ++kk)
+                        tc::mma_f16_tmem_a(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), vd + (uint64_t)((kk * 2 * L::ATOM) >> 4),
+                                           idO, (u > 0 || kk > 0) ? 1u : 0u);
+                    tc::commit(pv_done(t));
+                    tc::commit(&slot_empty[L::KS + vx]);
+                }
+                __syncwarp();
+                step(kx, kpar, L::KS);
+                step(vx, vpar, L::VS);
+                if (QT == 1 && 2 * u + t + 1 < all) {   // the other stream's tile
+                    step(kx, kpar, L::KS);
+                    step(vx, vpar, L::VS);
+                }
+            }
+            piece_done(i);
+        }
+    }
+    } else {
         // ============================= softmax =======================================
+        regs_up<kSoftRegs>();
         const int t = warp >> 2;
         const int quad = warp & 3;
         const int r = quad * 32 + lane;                  // TMEM lane
         const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
         const uint32_t sbase = tmem + lane_addr + t * L::SCOL;
         const uint32_t obase = tmem + lane_addr + L::OCOL + t * D;
+        unsigned char* stage = smem + L::stage + warp * 4096;
         const int tok = (QT == 2 ? t * tok_tile : 0) + r / p.G;
         const bool row_fits = r < tok_tile * p.G;
         const float scale = fabsf(p.scale_log2);
         const bool negate = p.scale_log2 < 0.f;
         int4 rec = make_int4(0, 0, 0, 0);
-        int gs = 0, i = 0;
+        int gs = 0, g = 0;   // steps of the stream and tiles before this piece
         bool ok = true;
-        while (ok && !misc[1] && walk.next(p, TN, it)) {
+        for (int i = 0; ok && piece(i); ++i) {
+            const PieceRec& it = ring[i % kRing];
             const int nt = steps(it, t);
-            const int tk = it.qb * p.tokb + tok;         // this row's draft
             const bool row_valid = row_fits && tok < it.rows_tok;
             const bool warp_live = __any_sync(0xffffffffu, row_valid);
-            const uint32_t* mrow = p.mask + (int64_t)(it.q_begin + (row_valid ? tk : 0)) * p.W;
+            const int c = it.c, n = it.n, j0 = it.j0;
+            const int q_row = it.q_row + (row_valid ? tok : 0);   // this row's draft
+            const uint32_t* mrow = p.mask + (int64_t)q_row * p.W;
             const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
             float m_ref = -INFINITY, l_run = 0.f;
             for (int u = 0; u < nt; ++u) {
-                const int k0 = (it.j0 + tile_at(t, u)) * TN;
+                const int k0 = (j0 + tile_at(t, u)) * TN;
                 // positions of this tile that the row sees, when it is not all of them
-                const bool in = lane < 8 && k0 + lane * 16 < it.kend;
-                const int blk = warp_live && in ? __ldg(trow + (k0 + lane * 16) / p.P) : 0;
-                const unsigned okm = __ballot_sync(0xffffffffu, (unsigned)blk < (unsigned)p.N);
-                const bool masked = k0 + TN > it.c || okm != 0xffffffffu;
+                bool masked = k0 + TN > c;
                 uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                 if (warp_live && masked) {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        vis[w] = row_valid ? mask_bits(mrow, p.W, k0 + 32 * w - it.c, it.n) : 0u;
-                        if (!((okm >> (2 * w)) & 1u)) vis[w] &= 0xffff0000u;
-                        if (!((okm >> (2 * w + 1)) & 1u)) vis[w] &= 0x0000ffffu;
-                    }
+                    for (int w = 0; w < 4; ++w) vis[w] = row_valid ? mask_bits(mrow, p.W, k0 + 32 * w - c, n) : 0u;
                 }
                 if (!mbar_wait(s_full(t), (gs + u) & 1)) {
                     if (lane == 0) fail();
@@ -400,6 +519,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (warp_live) {
                     tc::fence_after_sync();
+                    const uint32_t okm = okm_of[(g + tile_at(t, u)) & 15];
+                    if (!masked && okm != 0xffu) masked = true;
+                    if (masked) {   // boxes past the request's end are not in okm either
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            vis[w] &= ((okm >> (2 * w)) & 1u ? 0xffffu : 0u) |
+                                      ((okm >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
+                    }
                     float m8[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
@@ -501,6 +628,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             }
             gs += nt;
+            g += it.j1 - it.j0;
             const bool whole = it.j0 == 0 && it.j1 == it.nt;
             float w0 = 1.f, w1 = 0.f;                     // weights of the streams' O (QT = 1)
             const float2* ml = reinterpret_cast<const float2*>(smem + L::ml);
@@ -527,20 +655,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             tc::fence_after_sync();
             const bool both = QT == 1 && it.j1 - it.j0 > 1;    // stream 1 has an O
-            const bool wild = misc[8 + (i & 7)] != 0;
-            const int piece = tree_piece_slot(cta, it.j0);
-            const int64_t wrow = (int64_t)piece * p.rows + tok * p.G + r % p.G;
+            const bool wild = reinterpret_cast<const volatile uint32_t*>(wild_of)[i % kRing] != 0;
+            const int slot_of_piece = tree_piece_slot(cta, j0);
+            // this query tile: its rows, first draft row of q, first row of the workspace
+            const int t0 = QT == 2 ? t * tok_tile : 0;
+            const int live_rows = min(tok_tile, it.rows_tok - t0) * p.G;
+            const int tile_row = it.q_row + t0;
+            const int64_t wbase = (int64_t)slot_of_piece * p.rows + t0 * p.G;
             if (!whole) {
-                if (it.j0 == 0 && threadIdx.x == 0) rec = tree_record(p, *st, it, cta);
-                if (row_valid && (QT == 2 || t == 0)) p.ws_ml[wrow] = make_float2(m_ref, l_run);
+                if (it.j0 == 0) rec = make_int4(it.b, it.tok0 / p.tokb * p.H_kv + it.h, it.last, 1);
+                if (row_valid && (QT == 2 || t == 0)) p.ws_ml[wbase + r] = make_float2(m_ref, l_run);
             }
             const float f = !whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;
-            const int64_t orow = (int64_t)(it.q_begin + tk) * p.H_q + it.h * p.G + r % p.G;
             if (nt > 0 || QT == 1) {
                 constexpr int kHalf = QT == 1 ? D / 64 : D / 32;   // 32-column groups of this warp
-#pragma unroll
-                for (int c = 0; c < kHalf; ++c) {
-                    const int col = (QT == 1 ? t * (D / 2) : 0) + c * 32;
+#pragma unroll 1
+                for (int part = 0; part < kHalf; ++part) {
+                    const int col = (QT == 1 ? t * (D / 2) : 0) + part * 32;
                     float o[32];
                     if (warp_live) {
                         if constexpr (QT == 1) {
@@ -558,15 +689,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc::wait_ld();
                         }
                     }
-                    if (!row_valid) continue;
-                    if (wild) {
+                    if (!warp_live) continue;
+                    if (wild && row_valid) {
                         // drafts whose V row is not finite: what was zeroed for P V, added to the
                         // rows that see them
-                        const int d0 = max(0, it.j0 * TN - it.c), d1 = min(it.n, it.j1 * TN - it.c);
+                        const int d0 = max(0, j0 * TN - c), d1 = min(n, it.j1 * TN - c);
                         for (int d = d0; d < d1; ++d) {
-                            const int pos = it.c + d;
+                            const int pos = c + d;
                             const int blk = __ldg(trow + pos / p.P);
-                            if ((unsigned)blk >= (unsigned)p.N || !tree_bit(p, it.q_begin + tk, d)) continue;
+                            if ((unsigned)blk >= (unsigned)p.N || !tree_bit(p, q_row, d)) continue;
                             const int64_t slot = (int64_t)blk * p.P + pos % p.P;
                             const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_pool) +
                                                      (slot * p.H_kv + it.h) * D + col;
@@ -577,26 +708,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     }
-                    if (l_run == 0.f) {
+                    // through shared memory, so that a store writes whole lines: a thread has one
+                    // row, and 32 rows a store would be 32 lines of 16 bytes
+                    const bool none = l_run == 0.f;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    for (int e4 = 0; e4 < 8; ++e4) {
+                        float4 y = make_float4(o[e4 * 4] * f, o[e4 * 4 + 1] * f, o[e4 * 4 + 2] * f, o[e4 * 4 + 3] * f);
+                        if (none) y = make_float4(0.f, 0.f, 0.f, 0.f);
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e4 ^ (lane & 7)) << 4)) = y;
                     }
+                    __syncwarp();
                     if (whole) {
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + orow * D + col;
 #pragma unroll
-                        for (int e8 = 0; e8 < 4; ++e8)
-                            *reinterpret_cast<uint4*>(dst + e8 * 8) =
-                                make_uint4(pack_bf16x2(o[e8 * 8 + 0] * f, o[e8 * 8 + 1] * f),
-                                           pack_bf16x2(o[e8 * 8 + 2] * f, o[e8 * 8 + 3] * f),
-                                           pack_bf16x2(o[e8 * 8 + 4] * f, o[e8 * 8 + 5] * f),
-                                           pack_bf16x2(o[e8 * 8 + 6] * f, o[e8 * 8 + 7] * f));
+                        for (int k = 0; k < 4; ++k) {           // 8 rows of 64 bytes a store
+                            const int rr = k * 8 + (lane >> 2), cc = (lane & 3) * 2;
+                            const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
+                            const float4 b = ld_shared_f4(stage + rr * 128 + (((cc + 1) ^ (rr & 7)) << 4));
+                            const int row = quad * 32 + rr;      // of the query tile
+                            if (row < live_rows) {
+                                const int64_t at = (int64_t)(tile_row + row / p.G) * p.H_q + it.h * p.G + row % p.G;
+                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at * D + col + cc * 4) =
+                                    make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                                               pack_bf16x2(b.z, b.w));
+                            }
+                        }
                     } else {
-                        float* dst = p.ws_o + wrow * D + col;
 #pragma unroll
-                        for (int e4 = 0; e4 < 8; ++e4)
-                            *reinterpret_cast<float4*>(dst + e4 * 4) =
-                                make_float4(o[e4 * 4], o[e4 * 4 + 1], o[e4 * 4 + 2], o[e4 * 4 + 3]);
+                        for (int k = 0; k < 8; ++k) {           // 4 rows of 128 bytes a store
+                            const int rr = k * 4 + (lane >> 3), cc = lane & 7;
+                            const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
+                            const int row = quad * 32 + rr;
+                            if (row < live_rows)
+                                *reinterpret_cast<float4*>(p.ws_o + (wbase + row) * D + col + cc * 4) = a;
+                        }
                     }
+                    __syncwarp();
                 }
             }
             // O (and the streams' sums) are read: the next piece may overwrite them
@@ -605,7 +751,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(x_done);
             }
-            ++i;
+            piece_done(i);
         }
         if (threadIdx.x == 0) p.ws_rec[cta] = rec;
     }
