@@ -541,24 +541,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 for (int e = 0; e < 32; ++e) s[c2][e] = -s[c2][e];
                         }
                         if (masked) {
+                            const uint32_t v0 = hh ? vis[2] : vis[0], v1 = hh ? vis[3] : vis[1];
 #pragma unroll
-                            for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    s[c2][e] = (vis[2 * hh + c2] >> e) & 1u ? s[c2][e] : -INFINITY;
+                            for (int e = 0; e < 32; ++e) {
+                                s[0][e] = (v0 >> e) & 1u ? s[0][e] : -INFINITY;
+                                s[1][e] = (v1 >> e) & 1u ? s[1][e] : -INFINITY;
+                            }
                         }
                     };
-                    float s[2][32];
-                    load_half(0, s);
+                    // both passes go through the row 64 columns at a time in a rolled loop: the
+                    // unrolled form of 128 does not stay in the instruction cache next to the
+                    // other warps' code
+#pragma unroll 1
+                    for (int hh = 0; hh < 2; ++hh) {
+                        float s[2][32];
+                        load_half(hh, s);
 #pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2)
+                        for (int c2 = 0; c2 < 2; ++c2)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) m8[e & 7] = fmax3(m8[e & 7], s[c2][e], s[c2][e + 16]);
-                    load_half(1, s);
-#pragma unroll
-                    for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) m8[e & 7] = fmax3(m8[e & 7], s[c2][e], s[c2][e + 16]);
+                            for (int e = 0; e < 16; ++e) m8[e & 7] = fmax3(m8[e & 7], s[c2][e], s[c2][e + 16]);
+                    }
                     const float mraw = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                                              fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
                     const float mt = mraw == -INFINITY ? -INFINITY : mraw * scale;
@@ -589,7 +591,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float2 nm2 = make_float2(-m_use, -m_use);
                     float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
-                    auto weights = [&](int hh) {
+#pragma unroll 1
+                    for (int hh = 0; hh < 2; ++hh) {
+                        float s[2][32];
+                        load_half(hh, s);
                         uint32_t pw[32];
 #pragma unroll
                         for (int c2 = 0; c2 < 2; ++c2) {
@@ -602,10 +607,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                         tc::st_32words(sbase + hh * 64, pw);
-                    };
-                    weights(1);
-                    load_half(0, s);
-                    weights(0);
+                    }
                     tc::wait_st();
                     const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
                     const float2 pst = __fadd2_rn(ps01, ps23);
