@@ -5,10 +5,9 @@
 // group)) under one KV head: softmax over the request's cached positions and drafts,
 // read tile by tile (kTile positions of the kernel).  Its cost is its tiles plus a
 // constant for its start and end.  All units stand in a row, request by request
-// (row block, then KV head innermost), and CTA k of n takes the stretch
-// [W k / n, W (k + 1) / n) of their total cost W: every CTA gets the same share of
-// tiles whatever the lengths, and at most the first and the last unit of a stretch are
-// cut.  A cut unit's pieces leave their running maximum, sum and unnormalised outputs
+// (row block, then KV head innermost), and CTA k of n takes the stretch [s k, s (k + 1))
+// of their total cost W, s = ceil(W / n): every CTA gets the same share of tiles
+// whatever the lengths, and at most the first and the last unit of a stretch are cut.  A cut unit's pieces leave their running maximum, sum and unnormalised outputs
 // in the workspace, two pieces a CTA at most, so the workspace does not grow with the
 // context; the joining kernel adds them up in position order.
 // Fixed spans (as the decode's) would write a row's partial every few hundred
@@ -73,6 +72,11 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, bool
     return r;
 }
 
+// a / b, b > 0; in 32 bits where a fits (a 64-bit division is some hundred instructions).
+__device__ __forceinline__ int64_t tree_div(int64_t a, int b) {
+    return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 __device__ __forceinline__ int64_t tree_cost(const TreeParams& p, const TreeReq& r, int tile) {
     if (r.n == 0) return 0;
     return (int64_t)((r.n + p.tokb - 1) / p.tokb) * p.H_kv * ((r.len + tile - 1) / tile + kTreeUnitCost);
@@ -80,12 +84,11 @@ __device__ __forceinline__ int64_t tree_cost(const TreeParams& p, const TreeReq&
 
 // Where a CTA's stretch begins.  In shared memory, filled by tree_begin.
 struct TreeStart {
-    int64_t total;   // W
+    int64_t share;   // s
     int64_t left;    // cost of this CTA's stretch
     int64_t pos;     // its first cost position
     int64_t off;     // that position within request b
     int b;
-    int ctas;        // CTAs that have work: min(grid, W)
 };
 
 // All threads of the CTA; `scratch` holds blockDim.x / 32 values.  Ends with a barrier.
@@ -109,14 +112,13 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    const int n = (int)(total < ncta ? total : ncta);
-    const int64_t s = cta < n ? total * cta / n : total, e = cta < n ? total * (cta + 1) / n : total;
+    const int64_t share = tree_div(total + ncta - 1, ncta);
+    const int64_t s = min(share * cta, total), e = min(s + share, total);
     const int64_t first = before + incl - mine;   // cost position of request b0
     if (tid == 0) {
-        st->total = total;
+        st->share = share;
         st->left = e - s;
         st->pos = s;
-        st->ctas = n;
     }
     if (s < e && first <= s && s < first + mine) {
         int64_t at = first;
@@ -177,7 +179,7 @@ struct TreeWalk {
                 if (b >= p.B) return false;   // not reached: the stretches end at W
                 continue;
             }
-            const int unit = (int)(off / w), x0 = (int)(off - (int64_t)unit * w);
+            const int unit = (int)tree_div(off, w), x0 = (int)(off - (int64_t)unit * w);
             const int64_t room = (int64_t)x0 + left;
             const int x1 = (int)(room < w ? room : w);
             it.end = pos - x0 + w;
@@ -211,7 +213,7 @@ __device__ __forceinline__ int tree_piece_slot(int cta, int j0) { return 2 * cta
 // head, last CTA that holds a piece, 1}.
 __device__ __forceinline__ int4 tree_record(const TreeParams& p, const TreeStart& st, const TreePiece& it, int cta) {
     int last = cta;
-    while (last + 1 < st.ctas && st.total * (last + 1) / st.ctas < it.end) ++last;
+    for (int64_t next = st.share * (cta + 1); next < it.end; next += st.share) ++last;
     return make_int4(it.b, it.qb * p.H_kv + it.h, last, 1);
 }
 

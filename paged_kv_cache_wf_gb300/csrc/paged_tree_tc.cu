@@ -37,7 +37,7 @@ constexpr int TN = 128;           // positions of a tile
 constexpr float kLazyMax = 8.f;   // rescale O only when a row's maximum grows by more than 2^8
 constexpr int kSoftW = 8, kKW = 8, kVW = 9, kWalkW = 10, kMmaW = 11, kFinW = 13, kFin = 3;
 constexpr int kTcThreads = (kFinW + kFin) * 32;
-constexpr int kSoftRegs = 184, kOtherRegs = 72;
+constexpr int kSoftRegs = 192, kOtherRegs = 64;
 static_assert(kTcThreads / 2 * (kSoftRegs + kOtherRegs) <= 65536, "register split exceeds the block's registers");
 
 template <int N>
@@ -113,6 +113,15 @@ __device__ __forceinline__ bool tame(uint32_t& w) {
     return m != 0;
 }
 
+__device__ __forceinline__ void st_16words(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
 template <int D, int QT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -170,6 +179,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&piece_empty[i], kTcThreads / 32 - 1);
         }
         fence_mbar_init();
+        for (const CUtensorMap* m : {&tm_q, &tm_k, &tm_v})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
         misc[1] = 0;
         for (int i = 0; i < kRing * 4; ++i) smem[L::wild + i] = 0;
     }
@@ -488,6 +499,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         unsigned char* stage = smem + L::stage + warp * 4096;
         const int tok = (QT == 2 ? t * tok_tile : 0) + r / p.G;
         const bool row_fits = r < tok_tile * p.G;
+        const int g_inv = (65536 + p.G - 1) / p.G;       // row / G for rows below 128
         const float scale = fabsf(p.scale_log2);
         const bool negate = p.scale_log2 < 0.f;
         int4 rec = make_int4(0, 0, 0, 0);
@@ -527,42 +539,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             vis[w] &= ((okm >> (2 * w)) & 1u ? 0xffffu : 0u) |
                                       ((okm >> (2 * w + 1)) & 1u ? 0xffff0000u : 0u);
                     }
+                    // the whole row in registers: one TMEM round trip a tile
+                    float s[4][32];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) tc::ld_32cols(sbase + w * 32, s[w]);
+                    tc::wait_ld();
+                    if (negate) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[w][e] = -s[w][e];
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[w][e] = (vis[w] >> e) & 1u ? s[w][e] : -INFINITY;
+                    }
                     float m8[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
-                    auto load_half = [&](int hh, float (&s)[2][32]) {
-                        tc::ld_32cols(sbase + hh * 64, s[0]);
-                        tc::ld_32cols(sbase + hh * 64 + 32, s[1]);
-                        tc::wait_ld();
-                        if (negate) {
+                    for (int e = 0; e < 8; ++e) m8[e] = fmax3(s[0][e], s[0][e + 8], s[0][e + 16]);
 #pragma unroll
-                            for (int c2 = 0; c2 < 2; ++c2)
+                    for (int w = 1; w < 4; ++w)
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) s[c2][e] = -s[c2][e];
+                        for (int e = 0; e < 8; ++e) {
+                            m8[e] = fmax3(m8[e], s[w - 1][e + 24], s[w][e]);
+                            m8[e] = fmax3(m8[e], s[w][e + 8], s[w][e + 16]);
                         }
-                        if (masked) {
-                            const uint32_t v0 = hh ? vis[2] : vis[0], v1 = hh ? vis[3] : vis[1];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                s[0][e] = (v0 >> e) & 1u ? s[0][e] : -INFINITY;
-                                s[1][e] = (v1 >> e) & 1u ? s[1][e] : -INFINITY;
-                            }
-                        }
-                    };
-                    // both passes go through the row 64 columns at a time in a rolled loop: the
-                    // unrolled form of 128 does not stay in the instruction cache next to the
-                    // other warps' code
-#pragma unroll 1
-                    for (int hh = 0; hh < 2; ++hh) {
-                        float s[2][32];
-                        load_half(hh, s);
-#pragma unroll
-                        for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) m8[e & 7] = fmax3(m8[e & 7], s[c2][e], s[c2][e + 16]);
-                    }
-                    const float mraw = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                             fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+                    for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[3][e + 24]);
+                    const float mraw = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
                     const float mt = mraw == -INFINITY ? -INFINITY : mraw * scale;
                     float alpha = 1.f;
                     if (m_ref == -INFINITY) {
@@ -574,14 +580,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
                         if (!mbar_wait(pv_done(t), (gs + u - 1) & 1)) fail();
                         tc::fence_after_sync();
-#pragma unroll
-                        for (int c4 = 0; c4 < D / 32; ++c4) {
-                            float o[32];
-                            tc::ld_32cols(obase + c4 * 32, o);
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            uint32_t w[16];
+                            tc::ld_16cols(obase + c, o);
                             tc::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tc::st_32cols(obase + c4 * 32, o);
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                            st_16words(obase + c, w);
                         }
                         tc::wait_st();
                     }
@@ -591,22 +598,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float2 nm2 = make_float2(-m_use, -m_use);
                     float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
-#pragma unroll 1
-                    for (int hh = 0; hh < 2; ++hh) {
-                        float s[2][32];
-                        load_half(hh, s);
-                        uint32_t pw[32];
+                    // the weights of positions 0-63 take columns 0-31, those of 64-127 columns 64-95
 #pragma unroll
-                        for (int c2 = 0; c2 < 2; ++c2) {
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t pw[16];
 #pragma unroll
-                            for (int v = 0; v < 16; ++v) {
-                                const float2 x = __ffma2_rn(make_float2(s[c2][2 * v], s[c2][2 * v + 1]), sc2, nm2);
-                                const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
-                                ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
-                                pw[c2 * 16 + v] = pack_bf16x2(e2.x, e2.y);
-                            }
+                        for (int v = 0; v < 16; ++v) {
+                            const float2 x = __ffma2_rn(make_float2(s[w][2 * v], s[w][2 * v + 1]), sc2, nm2);
+                            const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
+                            ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
+                            pw[v] = pack_bf16x2(e2.x, e2.y);
                         }
-                        tc::st_32words(sbase + hh * 64, pw);
+                        st_16words(sbase + (w >> 1) * 64 + (w & 1) * 16, pw);
                     }
                     tc::wait_st();
                     const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
@@ -669,6 +672,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (row_valid && (QT == 2 || t == 0)) p.ws_ml[wbase + r] = make_float2(m_ref, l_run);
             }
             const float f = !whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;
+            w0 *= f;
+            w1 *= f;
             if (nt > 0 || QT == 1) {
                 constexpr int kHalf = QT == 1 ? D / 64 : D / 32;   // 32-column groups of this warp
 #pragma unroll 1
@@ -689,6 +694,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         } else {
                             tc::ld_32cols(obase + col, o);
                             tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= w0;
                         }
                     }
                     if (!warp_live) continue;
@@ -712,30 +719,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     // through shared memory, so that a store writes whole lines: a thread has one
                     // row, and 32 rows a store would be 32 lines of 16 bytes
-                    const bool none = l_run == 0.f;
 #pragma unroll
-                    for (int e4 = 0; e4 < 8; ++e4) {
-                        float4 y = make_float4(o[e4 * 4] * f, o[e4 * 4 + 1] * f, o[e4 * 4 + 2] * f, o[e4 * 4 + 3] * f);
-                        if (none) y = make_float4(0.f, 0.f, 0.f, 0.f);
-                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e4 ^ (lane & 7)) << 4)) = y;
-                    }
+                    for (int e4 = 0; e4 < 8; ++e4)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e4 ^ (lane & 7)) << 4)) =
+                            make_float4(o[e4 * 4], o[e4 * 4 + 1], o[e4 * 4 + 2], o[e4 * 4 + 3]);
                     __syncwarp();
                     if (whole) {
-#pragma unroll
+#pragma unroll 2
                         for (int k = 0; k < 4; ++k) {           // 8 rows of 64 bytes a store
                             const int rr = k * 8 + (lane >> 2), cc = (lane & 3) * 2;
                             const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
                             const float4 b = ld_shared_f4(stage + rr * 128 + (((cc + 1) ^ (rr & 7)) << 4));
                             const int row = quad * 32 + rr;      // of the query tile
                             if (row < live_rows) {
-                                const int64_t at = (int64_t)(tile_row + row / p.G) * p.H_q + it.h * p.G + row % p.G;
+                                const int dr = (row * g_inv) >> 16;
+                                const int64_t at = (int64_t)(tile_row + dr) * p.H_q + it.h * p.G + row - dr * p.G;
                                 *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at * D + col + cc * 4) =
                                     make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
                                                pack_bf16x2(b.z, b.w));
                             }
                         }
                     } else {
-#pragma unroll
+#pragma unroll 2
                         for (int k = 0; k < 8; ++k) {           // 4 rows of 128 bytes a store
                             const int rr = k * 4 + (lane >> 3), cc = lane & 7;
                             const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
