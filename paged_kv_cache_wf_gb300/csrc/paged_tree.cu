@@ -395,7 +395,7 @@ static bool tree_shape(const wf_pool_desc& pool, int32_t num_q_heads, int32_t ma
     if (num_q_heads % pool.num_kv_heads != 0) return false;
     const int G = num_q_heads / pool.num_kv_heads;
     if (G < 1 || G > 8) return false;
-    *s = tree_tc_supported(pool, num_q_heads) ? tree_tc_shape(G, max_q_len)
+    *s = tree_tc_supported(pool, num_q_heads) ? tree_tc_shape(G, max_q_len, pool.dtype == WF_DTYPE_FP8_E4M3)
                                               : TreeShape{kCcRows, kCcRows / G, kCcTile, 2};
     return true;
 }
@@ -425,7 +425,10 @@ size_t tree_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, i
     if (B < 0 || max_q_len < 0 || max_seq_len < 0 || !tree_shape(pool, num_q_heads, max_q_len, &s)) return 0;
     const int64_t ctas = tree_ctas(s, B, pool.num_kv_heads, max_q_len, max_seq_len);
     const int64_t rows = 2 * ctas * s.rows;
-    return (size_t)(256 + ctas * (int64_t)sizeof(int4) + rows * 8 + rows * pool.head_dim * 4);
+    const size_t bytes = (size_t)(256 + ctas * (int64_t)sizeof(int4) + rows * 8 + rows * pool.head_dim * 4);
+    if (pool.dtype != WF_DTYPE_FP8_E4M3 || !tree_tc_supported(pool, num_q_heads)) return bytes;
+    const size_t prep = tree_tc_prep_bytes(B, num_q_heads, max_q_len, pool);
+    return prep == SIZE_MAX ? 0 : bytes + prep;
 }
 
 cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint32_t* dev_status,
@@ -462,13 +465,15 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint3
     p.W = a.mask_words;
     p.rows = s.rows;
     p.tokb = s.tokb;
+    p.q_inv = nullptr;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     // a masked score is -inf before it is scaled: a scale of 0 (equal weights) stands as the
     // smallest normal number, which leaves every finite score a weight of 2^0
     if (fabsf(p.scale_log2) < FLT_MIN) p.scale_log2 = copysignf(FLT_MIN, p.scale_log2);
     const bool d128 = pool.head_dim == 128;
     if (tree_tc_supported(pool, a.num_q_heads)) {
-        const cudaError_t e = launch_tree_tc(p, pool.head_dim, ctas, stream);
+        void* prep = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(p.ws_rec + cap) + 127) & ~(uintptr_t)127);
+        const cudaError_t e = launch_tree_tc(p, pool, prep, ctas, stream);
         if (e != cudaSuccess || ctas == 1) return e;
         return d128 ? launch_join<BF16, 128>(p, ctas, stream) : launch_join<BF16, 64>(p, ctas, stream);
     }

@@ -35,6 +35,7 @@ struct TreeParams {
     int32_t rows;    // rows of a row block in the workspace
     int32_t tokb;    // drafts of a row block
     float scale_log2;
+    const float* q_inv;   // fp8 pools on the tensor cores: factors of the prepared q rows
 };
 
 // Rows of a row block, drafts in it, tile and CTAs an SM of the kernel that runs a call.
@@ -44,8 +45,9 @@ struct TreeShape {
 
 // The tensor-core kernel (paged_tree_tc.cu).
 bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads);
-TreeShape tree_tc_shape(int G, int max_q_len);
-cudaError_t launch_tree_tc(const TreeParams& p, int D, int ctas, cudaStream_t stream);
+TreeShape tree_tc_shape(int G, int max_q_len, bool codes);
+size_t tree_tc_prep_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, const wf_pool_desc& pool);
+cudaError_t launch_tree_tc(const TreeParams& p, const wf_pool_desc& pool, void* prep, int ctas, cudaStream_t stream);
 
 namespace {
 

@@ -1,5 +1,5 @@
 // paged_tree_tc.cu -- tree attention on the tensor cores (tcgen05, TMA, TMEM) for bf16
-// pools whose block size is a multiple of 16.
+// and fp8 pools whose block size is a multiple of 16.
 //
 // What is computed is paged_tree.cu's: row (draft, query head) sees its request's cached
 // positions and the drafts of its mask; o = softmax(scale q K^T) V.
@@ -24,7 +24,20 @@
 // NaN is NaN in P V).  Rows past the request's end or of a bad block are zeroed; an
 // element of a draft's row that is not finite is zeroed too, and the epilogue adds it
 // to the rows that see the draft.  Only tiles that reach the drafts are looked at.
+//
+// fp8 pools (CODES; always QT = 1).  S takes the K codes as they are (e4m3 x e4m3 ->
+// fp32): a small grid before this one splits every q row, scaled by a power of two so
+// that its largest magnitude lies in [128, 256), into hi = e4m3(q) and lo = e4m3(q - hi).
+// hi keeps four of a bf16 value's eight significant bits and lo the rest, so their sum is
+// the row up to 2^-10 (a 2^-17 part of its largest value).  The row's power of two and
+// the K scale go into the exponent's factor.  V codes are widened to bf16, which is
+// exact, by the finishing warps, into the ring that P V reads; the V scale multiplies
+// the outputs.  Widening K too would cost twice the finishing warps' work, and splitting
+// the weights into two e4m3 parts would cost the softmax warps more conversions than
+// they have time for.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "paged_tree.cuh"
 
@@ -58,26 +71,33 @@ struct PieceRec {
     int j0, j1, nt, last;    // tiles [j0, j1) of nt; last CTA with a piece of the unit
 };
 
-template <int D, int QT>
+template <int D, int QT, bool CODES>
 struct TtLayout {
+    static_assert(QT == 1 || !CODES, "fp8 pools have one query tile");
     static constexpr int NC = D / 64;                    // 64-wide column blocks of D
-    static constexpr int QTILE = TM * D * 2;
-    static constexpr int SLOT = TN * D * 2;              // one K or V tile
-    static constexpr int ATOM = NC == 2 ? 2048 : 1024;   // stride between 8-position atoms
-    static constexpr int HALF_OFF = 1024;                // offset of the second 64-wide half
-    static constexpr int BOX = NC * 2048;                // one 16-position box
-    static constexpr int KS = D == 128 ? (QT == 1 ? 3 : 2) : 5;
-    static constexpr int VS = D == 128 ? 2 : 5;
+    static constexpr int QTILE = TM * D * 2;             // bf16, or the two e4m3 parts
+    static constexpr int KTILE = TN * D * (CODES ? 1 : 2);
+    static constexpr int VTILE = TN * D * 2;
+    static constexpr int RAW = CODES ? TN * D : 0;       // V codes before they are widened
+    static constexpr int ATOM = NC == 2 ? 2048 : 1024;   // bf16: stride between 8-position atoms
+    static constexpr int HALF_OFF = 1024;                // bf16: offset of the second 64-wide half
+    static constexpr int BOX = 16 * D * (CODES ? 1 : 2); // one 16-position box
+    // slots of the K ring, the V ring and (CODES) the ring of V codes
+    static constexpr int KS = CODES ? (D == 128 ? 4 : 6) : D == 128 ? (QT == 1 ? 3 : 2) : 5;
+    static constexpr int VS = D == 128 ? 2 : CODES ? 3 : 5;
+    static constexpr int RS = CODES ? (D == 128 ? 2 : 4) : 0;
     static constexpr int NSLOT = KS + VS;
     static constexpr int q = 0;
-    static constexpr int kv = QT * QTILE;
-    static constexpr int stage = kv + NSLOT * SLOT;      // a 32 x 32 fp32 block a softmax warp, for whole-line stores
+    static constexpr int k = q + QT * QTILE;
+    static constexpr int v = k + KS * KTILE;
+    static constexpr int raw = v + VS * VTILE;
+    static constexpr int stage = raw + RS * RAW;         // a 32 x 32 fp32 block a softmax warp, for whole-line stores
     static constexpr int ml = stage + kSoftW * 4096;     // QT = 1: (m, l) of both streams' rows
     static constexpr int bars = ml + (QT == 1 ? 2 * TM * 8 : 0);
-    // q_full[QT], q_empty[QT], slot_full[NSLOT], slot_empty[NSLOT], v_ready[VS], per
-    // stream s_full, p_full, pv_done, then x_ready, x_done
-    // and piece_full[kRing], piece_empty[kRing]
-    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 6 + 2 + 2 * kRing;
+    // q_full[QT], q_empty[QT], k_full[KS], k_empty[KS], v_full[VS] (CODES: not used), v_empty[VS], v_ready[VS],
+    // raw_full[RS], raw_empty[RS], per stream s_full, p_full, pv_done, then x_ready, x_done and
+    // piece_full[kRing], piece_empty[kRing]
+    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing;
     static constexpr int ring = bars + nbars * 8;        // [kRing] records of pieces
     static constexpr int start = ring + kRing * (int)sizeof(PieceRec);
     static constexpr int scratch = start + (int)sizeof(TreeStart);
@@ -122,21 +142,52 @@ __device__ __forceinline__ void st_16words(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 
-template <int D, int QT>
+// 16 e4m3 codes -> 16 bf16 values (two 16-byte chunks), exactly: a code's exponent and
+// mantissa bits stand in a bf16 as a value 2^-120 times its own.  The NaN codes come out
+// as +-480.
+__device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
+    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+    uint32_t o[8];
+    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));   // 2^120
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t t = __byte_perm(in[i >> 1], 0u, (i & 1) ? 0x3424 : 0x1404);   // codes in the upper bytes
+        uint32_t u = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), up);
+        o[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Whether one of 16 codes is NaN (S.1111.111).
+__device__ __forceinline__ bool nan_code(const uint4& c) {
+    auto n = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+    return (n(c.x) | n(c.y) | n(c.z) | n(c.w)) != 0;
+}
+
+struct NoScales {};
+
+template <int D, int QT, bool CODES>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const TreeParams p, const int box_tok) {
-    using L = TtLayout<D, QT>;
+                         const __grid_constant__ CUtensorMap tm_v, const TreeParams p, const int box_tok,
+                         const typename std::conditional<CODES, HeadScales, NoScales>::type sc) {
+    using L = TtLayout<D, QT, CODES>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
     uint64_t* q_full = bars;
     uint64_t* q_empty = q_full + QT;
-    uint64_t* slot_full = q_empty + QT;
-    uint64_t* slot_empty = slot_full + L::NSLOT;
-    uint64_t* v_ready = slot_empty + L::NSLOT;
-    uint64_t* tb = v_ready + L::VS;
+    uint64_t* k_full = q_empty + QT;
+    uint64_t* k_empty = k_full + L::KS;
+    uint64_t* v_full = k_empty + L::KS;
+    uint64_t* v_empty = v_full + L::VS;
+    uint64_t* v_ready = v_empty + L::VS;
+    uint64_t* raw_full = v_ready + L::VS;
+    uint64_t* raw_empty = raw_full + L::RS;
+    uint64_t* tb = raw_empty + L::RS;
     auto s_full = [&](int t) { return tb + t * 3; };
     auto p_full = [&](int t) { return tb + t * 3 + 1; };
     auto pv_done = [&](int t) { return tb + t * 3 + 2; };
@@ -151,7 +202,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         report(p.dev_status, WF_DEV_TIMEOUT);
         misc[1] = 1;
     };
-    auto slot_ptr = [&](int s) { return smem + L::kv + s * L::SLOT; };
 
     if (warp == kMmaW) {
         tc::alloc(reinterpret_cast<uint32_t*>(smem + L::misc), L::TMEM_COLS);
@@ -162,11 +212,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&q_full[t], 1);
             mbar_init(&q_empty[t], QT == 1 ? 2 : 1);
         }
-        for (int i = 0; i < L::NSLOT; ++i) {
-            mbar_init(&slot_full[i], 1);
-            mbar_init(&slot_empty[i], QT);   // QT = 1: a tile belongs to one stream
+        for (int i = 0; i < L::KS; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], QT);   // QT = 1: a tile belongs to one stream
         }
-        for (int i = 0; i < L::VS; ++i) mbar_init(&v_ready[i], kFin);
+        for (int i = 0; i < L::VS; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], QT);
+            mbar_init(&v_ready[i], kFin);
+        }
+        for (int i = 0; i < L::RS; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], kFin);
+        }
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
             mbar_init(p_full(t), 4);
@@ -219,10 +277,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // one 16-position box a lane; block ids are read one tile ahead
         const bool isv = warp == kVW;
         const CUtensorMap* tm = isv ? &tm_v : &tm_k;
-        const int nslots = isv ? L::VS : L::KS;
-        unsigned char* slots = slot_ptr(isv ? L::KS : 0);
-        uint64_t* full = slot_full + (isv ? L::KS : 0);
-        uint64_t* empty = slot_empty + (isv ? L::KS : 0);
+        const int nslots = !isv ? L::KS : CODES ? L::RS : L::VS;
+        const int slot_bytes = !isv ? L::KTILE : CODES ? L::RAW : L::VTILE;
+        unsigned char* slots = smem + (!isv ? L::k : CODES ? L::raw : L::v);
+        uint64_t* full = !isv ? k_full : CODES ? raw_full : v_full;
+        uint64_t* empty = !isv ? k_empty : CODES ? raw_empty : v_empty;
         int x = 0, g = 0;       // slot and number of the next tile
         uint32_t par = 1;       // parity of the slot's last release: 1 passes before the first
         bool ok = true;
@@ -254,8 +313,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 if (okb) {
                     const int slot = blk * p.P + pos % p.P;   // a multiple of 16
-                    unsigned char* dst = slots + x * L::SLOT + lane * L::BOX;
-                    if constexpr (L::NC == 2)
+                    unsigned char* dst = slots + x * slot_bytes + lane * L::BOX;
+                    if constexpr (L::NC == 2 && !CODES)
                         tma_load_5d(dst, tm, 0, 0, 0, slot >> 3, h, &full[x]);
                     else
                         tma_load_3d_nohint(dst, tm, 0, slot, h, &full[x]);
@@ -306,14 +365,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (asked < made) {
                 const PieceRec& e = ring[asked % kRing];
+                if (CODES && asked == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the q parts
                 const int prev = t == 0 ? asked : second;
                 if (prev == 0 || __shfl_sync(0xffffffffu, (int)mbar_test(&q_empty[t], (prev - 1) & 1), 0)) {
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&q_full[t], (uint32_t)(L::NC * box_tok * p.G * 128));
+                        mbar_arrive_expect_tx(&q_full[t], (uint32_t)(2 * D * box_tok * p.G));
+                        if constexpr (CODES) {
 #pragma unroll
-                        for (int cb = 0; cb < L::NC; ++cb)
-                            tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64, e.h * p.G,
-                                               e.q_row + t * tok_tile, &q_full[t]);
+                            for (int part = 0; part < 2; ++part)   // hi rows, then lo rows
+                                tma_load_3d_nohint(smem + L::q + part * (TM * D), &tm_q, 0, e.h * p.G,
+                                                   (part * p.B + e.b) * p.max_q_len + e.tok0, &q_full[t]);
+                        } else {
+#pragma unroll
+                            for (int cb = 0; cb < L::NC; ++cb)
+                                tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64,
+                                                   e.h * p.G, e.q_row + t * tok_tile, &q_full[t]);
+                        }
                     }
                     __syncwarp();
                     if (QT == 2 && t == 0 && e.rows_tok > tok_tile) {
@@ -340,8 +407,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ============================= V finish ======================================
         // a third of a tile's rows each, dealt in turn
         const int fw = warp - kFinW;
-        int x = 0;           // slot
-        uint32_t par = 0;
+        int x = 0, rx = 0;              // slots of the V ring and of the ring of codes
+        uint32_t par = 0, rpar = 0;
         bool ok = true;
         for (int i = 0; ok && piece(i); ++i) {
             const PieceRec& it = ring[i % kRing];
@@ -353,19 +420,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool in = lane < 8 && k0 + lane * 16 < it.kend;
                 const int blk = in ? __ldg(trow + (k0 + lane * 16) / p.P) : -1;
                 const unsigned okm = __ballot_sync(0xffffffffu, (unsigned)blk < (unsigned)p.N);
-                if (!mbar_wait(&slot_full[L::KS + x], par)) {
+                if (CODES ? !mbar_wait(&raw_full[rx], rpar) || !mbar_wait(&v_empty[x], par ^ 1)
+                          : !mbar_wait(&v_full[x], par)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
                 }
-                if (okm != 0xffu || k0 + TN > it.c) {
-                    unsigned char* base = slot_ptr(L::KS + x);
+                unsigned char* base = smem + L::v + x * L::VTILE;
+                const int r0 = min(TN, max(0, it.c - k0)), r1 = min(TN, it.kend - k0);
+                if constexpr (CODES) {
+                    const unsigned char* raw = smem + L::raw + rx * L::RAW;
+                    constexpr int kRowChunks = D / 16;       // chunks of 16 codes
+                    constexpr int kStep = 32 / kRowChunks;   // rows a warp covers at once
+                    const int rr = lane / kRowChunks, ch = lane % kRowChunks;
+                    const int cb = ch >> 2, cc = (ch & 3) * 2;
+#pragma unroll 2
+                    for (int r = fw * kStep + rr; r < TN; r += kFin * kStep) {
+                        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+                        if (r < r1 && ((okm >> (r >> 4)) & 1u)) {
+                            const uint4 c = ld_shared_v4(raw + r * D + ch * 16);
+                            widen16(c, lo, hi);
+                            if (nan_code(c)) {               // +-480 so far: NaN, or a draft's to be set aside
+                                uint32_t* w[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        const uint32_t m = 0xffffu << (16 * half);
+                                        if (((*w[e] >> (16 * half)) & 0x7fffu) != 0x43f0u) continue;   // 480
+                                        *w[e] = r >= r0 ? *w[e] & ~m : *w[e] | m;
+                                    }
+                                wild |= r >= r0;
+                            }
+                        }
+                        unsigned char* at = base + (r >> 3) * L::ATOM + cb * L::HALF_OFF + (r & 7) * 128;
+                        *reinterpret_cast<uint4*>(at + ((cc ^ (r & 7)) << 4)) = lo;
+                        *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (r & 7)) << 4)) = hi;
+                    }
+                    tc::fence_proxy_async_smem();
+                } else if (okm != 0xffu || k0 + TN > it.c) {
                     // 16-byte chunk cc of row r (its place within the swizzle does not matter);
                     // with every block id in range, the rows before the first draft stay
-                    const int r0 = min(TN, max(0, it.c - k0)), r1 = min(TN, it.kend - k0);
                     const int first = okm == (1u << ((r1 + 15) >> 4)) - 1u ? r0 : 0;
                     constexpr int kRowChunks = L::NC * 8;
-                    constexpr int kStep = 32 / kRowChunks;   // rows a warp covers at once
+                    constexpr int kStep = 32 / kRowChunks;
                     const int rr = lane / kRowChunks, cb = (lane >> 3) % L::NC, cc = lane & 7;
                     for (int r = first + fw * kStep + rr; r < TN; r += kFin * kStep) {
                         uint4* at = reinterpret_cast<uint4*>(base + (r >> 3) * L::ATOM + cb * L::HALF_OFF +
@@ -388,10 +486,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0) {
                     if (j + 1 == it.j1) wild_of[(i % kRing) * 4 + fw] = wild ? 1 : 0;
                     mbar_arrive(&v_ready[x]);
+                    if constexpr (CODES) mbar_arrive(&raw_empty[rx]);
                 }
                 if (++x == L::VS) {
                     x = 0;
                     par ^= 1;
+                }
+                if (CODES && ++rx == L::RS) {
+                    rx = 0;
+                    rpar ^= 1;
                 }
             }
             piece_done(i);
@@ -403,12 +506,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // products in issue order.  One issuer for both streams was the bound at 16 products a
         // tile and stream.
         constexpr uint32_t idS = tc::idesc_bf16_f32(TM, TN, 0, 0);
+        constexpr uint32_t idS8 = tc::idesc_e4m3_f32(TM, TN, 0, 0);
         constexpr uint32_t idO = tc::idesc_bf16_f32(TM, D, 0, 1);
         const int t = warp - kMmaW;
         const int tq = QT == 1 ? 0 : t;
         const uint64_t qdesc = tc::sdesc_sw128(smem_u32(smem + L::q + tq * L::QTILE), 16, 1024);
-        const uint64_t kdesc = tc::sdesc_sw128(smem_u32(smem + L::kv), 16, L::ATOM);
-        const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::kv + L::KS * L::SLOT), L::HALF_OFF, L::ATOM);
+        const uint64_t kdesc = tc::sdesc_sw128(smem_u32(smem + L::k), 16, L::ATOM);
+        const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::v), L::HALF_OFF, L::ATOM);
         const uint32_t dS = tmem + t * L::SCOL, dO = tmem + L::OCOL + t * D;
         int kx = 0, vx = 0;                 // slots of the next tile
         uint32_t kpar = 0, vpar = 0;        // and their parities
@@ -432,8 +536,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int nt = steps(it, t), all = it.j1 - it.j0;
             if (QT == 2 && nt == 0) {       // no rows: hand the tiles on as they land
                 for (int u = 0; u < all && ok; ++u) {
-                    if (need(&slot_full[kx], kpar) && lane == 0) mbar_arrive(&slot_empty[kx]);
-                    if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&slot_empty[L::KS + vx]);
+                    if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
+                    if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&v_empty[vx]);
                     step(kx, kpar, L::KS);
                     step(vx, vpar, L::VS);
                 }
@@ -449,18 +553,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
 #pragma unroll 1
             for (int u = 0; u < nt && ok; ++u) {
-                if (!need(&slot_full[kx], kpar)) break;
+                if (!need(&k_full[kx], kpar)) break;
                 tc::fence_after_sync();
                 if (lane == 0) {
-                    const uint64_t kd = kdesc + (uint64_t)((kx * L::SLOT) >> 4);
+                    if constexpr (CODES) {   // rows of D one-byte values: swizzled over their own width
+                        auto desc = [](uint32_t at) {
+                            return D == 128 ? tc::sdesc_sw128(at, 16, 1024) : tc::sdesc_sw64(at, 16, 512);
+                        };
+                        const uint64_t kd = desc(smem_u32(smem + L::k + kx * L::KTILE));
+                        const uint64_t qd = desc(smem_u32(smem + L::q));
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
-                        const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
-                        tc::mma_f16(dS, qdesc + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS, kk > 0 ? 1u : 0u);
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk)
+                                tc::mma_f8f6f4(dS, qd + (uint64_t)((part * TM * D + kk * 32) >> 4),
+                                               kd + (uint64_t)((kk * 32) >> 4), idS8, (part | kk) ? 1u : 0u);
+                    } else {
+                        const uint64_t kd = kdesc + (uint64_t)((kx * L::KTILE) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
+                            const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
+                            tc::mma_f16(dS, qdesc + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS,
+                                        kk > 0 ? 1u : 0u);
+                        }
                     }
                     tc::commit(s_full(t));
-                    tc::commit(&slot_empty[kx]);
+                    tc::commit(&k_empty[kx]);
                     if (u + 1 == nt) tc::commit(&q_empty[tq]);
                 }
                 __syncwarp();
@@ -468,13 +587,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ppar ^= 1;
                 tc::fence_after_sync();
                 if (lane == 0) {
-                    const uint64_t vd = vdesc + (uint64_t)((vx * L::SLOT) >> 4);
+                    const uint64_t vd = vdesc + (uint64_t)((vx * L::VTILE) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < TN / 16; ++kk)
                         tc::mma_f16_tmem_a(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), vd + (uint64_t)((kk * 2 * L::ATOM) >> 4),
                                            idO, (u > 0 || kk > 0) ? 1u : 0u);
                     tc::commit(pv_done(t));
-                    tc::commit(&slot_empty[L::KS + vx]);
+                    tc::commit(&v_empty[vx]);
                 }
                 __syncwarp();
                 step(kx, kpar, L::KS);
@@ -500,7 +619,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tok = (QT == 2 ? t * tok_tile : 0) + r / p.G;
         const bool row_fits = r < tok_tile * p.G;
         const int g_inv = (65536 + p.G - 1) / p.G;       // row / G for rows below 128
-        const float scale = fabsf(p.scale_log2);
+        float scale = fabsf(p.scale_log2);
         const bool negate = p.scale_log2 < 0.f;
         int4 rec = make_int4(0, 0, 0, 0);
         int gs = 0, g = 0;   // steps of the stream and tiles before this piece
@@ -514,6 +633,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int q_row = it.q_row + (row_valid ? tok : 0);   // this row's draft
             const uint32_t* mrow = p.mask + (int64_t)q_row * p.W;
             const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
+            float v_scale = 1.f;
+            if constexpr (CODES) {
+                if (i == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the q rows' factors
+                const int hs = min(it.h, kMaxScaleHeads - 1);
+                const int64_t row = ((int64_t)it.b * p.max_q_len + it.tok0 + tok) * p.H_q + it.h * p.G + r % p.G;
+                scale = fabsf(p.scale_log2) * sc.k[hs] * (row_valid ? __ldcg(p.q_inv + row) : 1.f);
+                v_scale = sc.v[hs];
+            }
             float m_ref = -INFINITY, l_run = 0.f;
             for (int u = 0; u < nt; ++u) {
                 const int k0 = (j0 + tile_at(t, u)) * TN;
@@ -671,7 +798,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (it.j0 == 0) rec = make_int4(it.b, it.tok0 / p.tokb * p.H_kv + it.h, it.last, 1);
                 if (row_valid && (QT == 2 || t == 0)) p.ws_ml[wbase + r] = make_float2(m_ref, l_run);
             }
-            const float f = !whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;
+            const float f = v_scale * (!whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run);
             w0 *= f;
             w1 *= f;
             if (nt > 0 || QT == 1) {
@@ -708,11 +835,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const int blk = __ldg(trow + pos / p.P);
                             if ((unsigned)blk >= (unsigned)p.N || !tree_bit(p, q_row, d)) continue;
                             const int64_t slot = (int64_t)blk * p.P + pos % p.P;
-                            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_pool) +
-                                                     (slot * p.H_kv + it.h) * D + col;
+                            const int64_t at = (slot * p.H_kv + it.h) * D + col;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                const float x = __bfloat162float(v[e]);
+                                float x;
+                                if constexpr (CODES)
+                                    x = (static_cast<const unsigned char*>(p.v_pool)[at + e] & 0x7f) == 0x7f ? NAN : 0.f;
+                                else
+                                    x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pool)[at + e]);
                                 if (!(fabsf(x) < INFINITY)) o[e] += x;
                             }
                         }
@@ -773,36 +903,76 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// q [rows of all requests, D] bf16 -> the e4m3 parts of q 2^e_r, row r of a request b and
+// draft i at ((b max_q_len + i) H_q + head): hi, then (B max_q_len H_q rows on) lo; and
+// q_inv = 2^-e_r.  A warp a row, lane l holding elements VL l .. VL l + VL - 1.
+template <int D>
+__global__ void __launch_bounds__(256) tree_q_parts_kernel(const TreeParams p, unsigned char* __restrict__ parts,
+                                                           float* __restrict__ q_inv) {
+    constexpr int VL = D / 32;
+    // the attention grid may start its set-up now; it waits for this grid before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t di = w / p.H_q;                    // (request, draft)
+    const int b = (int)(di / p.max_q_len), i = (int)(di % p.max_q_len), hq = (int)(w % p.H_q);
+    if (b >= p.B) return;
+    const TreeReq req = tree_request(p, b, false);
+    if (i >= req.n) return;
+    const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(req.q_begin + i) * p.H_q + hq) * D;
+    float x[VL];
+    if constexpr (VL == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+        const float2 a = bf16x2_to_float2(v.x), c = bf16x2_to_float2(v.y);
+        x[0] = a.x; x[1] = a.y; x[2] = c.x; x[3] = c.y;
+    } else {
+        const float2 a = bf16x2_to_float2(__ldg(reinterpret_cast<const uint32_t*>(row) + lane));
+        x[0] = a.x; x[1] = a.y;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < VL; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    int ex = 0;
+    if (top > 0.f && top < INFINITY) {
+        // floor(log2 top) from the exponent bits; 2^ex and 2^-ex stay normal numbers
+        const int E = max(-126, (int)((__float_as_uint(top) >> 23) & 0xffu) - 127);
+        ex = min(126, max(-126, 7 - E));
+    }
+    const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int e = 0; e < VL; e += 2) {
+        float a = x[e] * up, c = x[e + 1] * up;
+        // the format has no infinities: they count as NaN here, as q K^T of one would be
+        if (!(fabsf(a) < INFINITY)) a = NAN;
+        if (!(fabsf(c) < INFINITY)) c = NAN;
+        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
+        const float2 back = e4m3x2_to_float2(h2);
+        const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, c - back.y), __NV_SATFINITE, __NV_E4M3) &
+                            0xffffu;
+        hi |= h2 << (8 * e);
+        lo |= l2 << (8 * e);
+    }
+    const int64_t rows = (int64_t)p.B * p.max_q_len * p.H_q;
+    if constexpr (VL == 4) {
+        *reinterpret_cast<uint32_t*>(parts + w * D + 4 * lane) = hi;
+        *reinterpret_cast<uint32_t*>(parts + (rows + w) * D + 4 * lane) = lo;
+    } else {
+        *reinterpret_cast<unsigned short*>(parts + w * D + 2 * lane) = (unsigned short)hi;
+        *reinterpret_cast<unsigned short*>(parts + (rows + w) * D + 2 * lane) = (unsigned short)lo;
+    }
+    if (lane == 0) q_inv[w] = __uint_as_float((uint32_t)(127 - ex) << 23);
+}
+
 template <int D, int QT>
-cudaError_t launch_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
-                      int box_tok, int ctas, cudaStream_t stream) {
-    auto kern = paged_tree_tc_kernel<D, QT>;
-    const int smem = TtLayout<D, QT>::total;
-    cudaError_t err = allow_dynamic_smem((const void*)kern, smem);
-    if (err != cudaSuccess) return err;
-    kern<<<ctas, kTcThreads, smem, stream>>>(tq, tk, tv, p, box_tok);
-    return cudaGetLastError();
-}
-
-}  // namespace
-
-bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads) {
-    if (pool.dtype != WF_DTYPE_BF16 || pool.block_size % 16 != 0) return false;
-    // slots are TMA coordinates
-    return (int64_t)pool.num_blocks * pool.block_size <= INT32_MAX && num_q_heads / pool.num_kv_heads <= 8;
-}
-
-// Units of at most 128 rows: two streams over the same rows; else two query tiles.
-TreeShape tree_tc_shape(int G, int max_q_len) {
-    const int tok = TM / G;
-    const int qt = max_q_len <= tok ? 1 : 2;
-    return TreeShape{qt * TM, qt * tok, TN, 1};
-}
-
-cudaError_t launch_tree_tc(const TreeParams& p, int D, int ctas, cudaStream_t stream) {
+cudaError_t launch_bf16(const TreeParams& p, int ctas, cudaStream_t stream) {
     const int tok = TM / p.G;
     const int box_tok = p.max_q_len < tok ? p.max_q_len : tok;   // drafts of a query tile's box
     CUtensorMap tq, tk, tv;
+    const uint64_t slots = (uint64_t)p.N * p.P;
+    const uint64_t row = (uint64_t)p.H_kv * D * 2;   // bytes of one pool slot
     cudaError_t e;
     {
         const uint64_t dims[3] = {(uint64_t)D, (uint64_t)p.H_q, (uint64_t)p.total_q};
@@ -811,9 +981,7 @@ cudaError_t launch_tree_tc(const TreeParams& p, int D, int ctas, cudaStream_t st
         e = encode_tiled_bf16(&tq, const_cast<void*>(p.q), 3, dims, strides, box);
         if (e != cudaSuccess) return e;
     }
-    const uint64_t slots = (uint64_t)p.N * p.P;
-    const uint64_t row = (uint64_t)p.H_kv * D * 2;   // bytes of one pool slot
-    if (D == 128) {
+    if constexpr (D == 128) {
         // (d 0-63, slot % 8, d half, slot / 8, head): a 16-slot box of one head holds both
         // halves of D as [slot/8 % 2][half][slot % 8][64]
         const uint64_t dims[5] = {64, 8, 2, slots / 8, (uint64_t)p.H_kv};
@@ -829,12 +997,91 @@ cudaError_t launch_tree_tc(const TreeParams& p, int D, int ctas, cudaStream_t st
         if (e == cudaSuccess) e = encode_tiled_bf16(&tv, const_cast<void*>(p.v_pool), 3, dims, strides, box);
     }
     if (e != cudaSuccess) return e;
-    const bool one = p.rows == TM;
-    if (D == 128)
-        return one ? launch_tc<128, 1>(tq, tk, tv, p, box_tok, ctas, stream)
-                   : launch_tc<128, 2>(tq, tk, tv, p, box_tok, ctas, stream);
-    return one ? launch_tc<64, 1>(tq, tk, tv, p, box_tok, ctas, stream)
-               : launch_tc<64, 2>(tq, tk, tv, p, box_tok, ctas, stream);
+    auto kern = paged_tree_tc_kernel<D, QT, false>;
+    const int smem = TtLayout<D, QT, false>::total;
+    e = allow_dynamic_smem((const void*)kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<ctas, kTcThreads, smem, stream>>>(tq, tk, tv, p, box_tok, NoScales{});
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_codes(TreeParams p, const HeadScales& sc, void* prep, int ctas, cudaStream_t stream) {
+    const int tok = TM / p.G;
+    const int box_tok = p.max_q_len < tok ? p.max_q_len : tok;
+    const uint64_t drafts = (uint64_t)p.B * p.max_q_len;
+    const uint64_t slots = (uint64_t)p.N * p.P, row = (uint64_t)p.H_kv * D;
+    unsigned char* parts = static_cast<unsigned char*>(prep);
+    float* q_inv = reinterpret_cast<float*>(parts + 2 * drafts * p.H_q * D);
+    p.q_inv = q_inv;
+    const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    CUtensorMap tq, tk, tv;
+    const uint64_t qdims[3] = {(uint64_t)D, (uint64_t)p.H_q, 2 * drafts};
+    const uint64_t qstrides[2] = {(uint64_t)D, (uint64_t)p.H_q * D};
+    const uint32_t qbox[3] = {(uint32_t)D, (uint32_t)p.G, (uint32_t)box_tok};
+    const uint64_t dims[3] = {(uint64_t)D, slots, (uint64_t)p.H_kv};
+    const uint64_t strides[2] = {row, (uint64_t)D};
+    const uint32_t box[3] = {(uint32_t)D, 16, 1};
+    cudaError_t e = encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, parts, 3, qdims, qstrides, qbox, swizzle);
+    if (e == cudaSuccess)
+        e = encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(p.k_pool), 3, dims, strides, box, swizzle);
+    if (e == cudaSuccess)
+        e = encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(p.v_pool), 3, dims, strides, box,
+                         CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+    auto kern = paged_tree_tc_kernel<D, 1, true>;
+    const int smem = TtLayout<D, 1, true>::total;
+    e = allow_dynamic_smem((const void*)kern, smem);
+    if (e != cudaSuccess) return e;
+    tree_q_parts_kernel<D><<<(unsigned)((drafts * p.H_q + 7) / 8), 256, 0, stream>>>(p, parts, q_inv);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // a programmatic dependent of the grid before it: its set-up overlaps
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p, box_tok, sc);
+}
+
+}  // namespace
+
+bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads) {
+    if (pool.dtype == WF_DTYPE_F32 || pool.block_size % 16 != 0) return false;
+    // slots are TMA coordinates
+    return (int64_t)pool.num_blocks * pool.block_size <= INT32_MAX && num_q_heads / pool.num_kv_heads <= 8;
+}
+
+// Units of at most 128 rows: two streams over the same rows; else two query tiles.  fp8
+// pools stay with 128 rows: the widened V leaves no room for a second query tile.
+TreeShape tree_tc_shape(int G, int max_q_len, bool codes) {
+    const int tok = TM / G;
+    const int qt = codes || max_q_len <= tok ? 1 : 2;
+    return TreeShape{qt * TM, qt * tok, TN, 1};
+}
+
+// fp8 pools: the q parts and the rows' factors.
+size_t tree_tc_prep_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, const wf_pool_desc& pool) {
+    const uint64_t rows = (uint64_t)B * (uint64_t)max_q_len;
+    if (rows > (uint64_t)INT32_MAX / 2) return SIZE_MAX;   // a draft's row is a TMA coordinate
+    return (size_t)(rows * num_q_heads) * (2 * pool.head_dim + 4);
+}
+
+cudaError_t launch_tree_tc(const TreeParams& p, const wf_pool_desc& pool, void* prep, int ctas, cudaStream_t stream) {
+    const bool d128 = pool.head_dim == 128;
+    if (pool.dtype == WF_DTYPE_FP8_E4M3) {
+        const HeadScales sc = head_scales(pool);
+        return d128 ? launch_codes<128>(p, sc, prep, ctas, stream) : launch_codes<64>(p, sc, prep, ctas, stream);
+    }
+    if (p.rows == TM)
+        return d128 ? launch_bf16<128, 1>(p, ctas, stream) : launch_bf16<64, 1>(p, ctas, stream);
+    return d128 ? launch_bf16<128, 2>(p, ctas, stream) : launch_bf16<64, 2>(p, ctas, stream);
 }
 
 }  // namespace wf

@@ -120,6 +120,10 @@ class Tree:
                     out[t, g] = w @ v
                     W[t, g] = w @ np.abs(v)
                     S[t, g] = (np.abs(k) @ np.abs(q[t, g])).max() * abs(self.scale)
+                    if self.pool == "fp8" and self.kernel() == wf.WF_KERNEL_TENSOR_CORES:
+                        # q goes to the tensor cores as two e4m3 parts: off by at most 2^-17 of the row's largest
+                        # element in each; `bound` multiplies S by (D + 4) 2^-24
+                        S[t, g] += np.abs(k).sum(-1).max() * np.abs(q[t, g]).max() * abs(self.scale) * 2.0 ** 7 / (self.D + 4)
         return out, W, S
 
     def device(self):
