@@ -83,9 +83,11 @@ struct TtLayout {
     static constexpr int HALF_OFF = 1024;                // bf16: offset of the second 64-wide half
     static constexpr int BOX = 16 * D * (CODES ? 1 : 2); // one 16-position box
     // slots of the K ring, the V ring and (CODES) the ring of V codes
-    static constexpr int KS = CODES ? (D == 128 ? 4 : 6) : D == 128 ? (QT == 1 ? 3 : 2) : 5;
-    static constexpr int VS = D == 128 ? 2 : CODES ? 3 : 5;
+    static constexpr int KS = D == 128 ? (CODES ? 4 : 2) : QT == 1 ? 6 : 5;
+    static constexpr int VS = D == 128 ? 2 : QT == 1 ? 4 : 5;
     static constexpr int RS = CODES ? (D == 128 ? 2 : 4) : 0;
+    // QT = 1: a slot belongs to one stream, which so sees every phase of its barriers (see ring_tiles)
+    static_assert(QT == 2 || (KS % 2 == 0 && VS % 2 == 0), "two streams share a ring of an odd number of slots");
     static constexpr int NSLOT = KS + VS;
     static constexpr int q = 0;
     static constexpr int k = q + QT * QTILE;
@@ -254,6 +256,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if constexpr (QT == 1) return (nt + 1 - t) >> 1;
         return t == 0 || it.rows_tok > tok_tile ? nt : 0;
     };
+    // Tiles of a piece in the rings.  QT = 1: an odd piece is followed by an empty tile, so
+    // that stream t's tiles always lie in slots of t's parity.  A parity wait tells a phase
+    // from the one two before it only for a waiter that is at most one phase ahead: a stream
+    // that met a slot after the other stream's tile in it could take the phase before that
+    // tile's for its own.
+    auto ring_tiles = [&](int nt) { return QT == 1 ? (nt + 1) & ~1 : nt; };
     auto tile_at = [&](int t, int u) { return QT == 1 ? 2 * u + t : u; };
     volatile unsigned char* wild_of = smem + L::wild;
     volatile unsigned char* okm_of = smem + L::okm;
@@ -290,13 +298,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
             const int h = it.h, kend = it.kend;
             int pos = it.j0 * TN + lane * 16;
-            int left = it.j1 - it.j0;
+            int real = it.j1 - it.j0;        // what is left of the piece, and of its tiles in the ring
+            int left = ring_tiles(real);
             int blk_next = lane < 8 && pos < kend ? __ldg(trow + pos / p.P) : 0;
 #pragma unroll 1
-            for (; left > 0; --left, pos += TN, ++g) {
+            for (; left > 0; --left, --real, pos += TN, ++g) {
                 const int blk = blk_next;
-                const bool in = lane < 8 && pos < kend;
-                if (left > 1 && lane < 8 && pos + TN < kend) blk_next = __ldg(trow + (pos + TN) / p.P);
+                const bool in = lane < 8 && real > 0 && pos < kend;
+                if (real > 1 && lane < 8 && pos + TN < kend) blk_next = __ldg(trow + (pos + TN) / p.P);
                 if (!mbar_wait(&empty[x], par)) {
                     if (lane == 0) fail();
                     ok = false;
@@ -414,11 +423,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const PieceRec& it = ring[i % kRing];
             const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
             bool wild = false;
+            const int j1 = it.j1, kend = it.kend, c0 = it.c;
+            // block ids are read one tile ahead
+            auto block_of = [&](int j) {
+                const int pos = j * TN + lane * 16;
+                return lane < 8 && j < j1 && pos < kend ? __ldg(trow + pos / p.P) : -1;
+            };
+            int blk_next = block_of(it.j0);
 #pragma unroll 1
-            for (int j = it.j0; j < it.j1; ++j) {
+            for (int j = it.j0, end = j + ring_tiles(j1 - j); j < end; ++j) {
                 const int k0 = j * TN;
-                const bool in = lane < 8 && k0 + lane * 16 < it.kend;
-                const int blk = in ? __ldg(trow + (k0 + lane * 16) / p.P) : -1;
+                const int blk = blk_next;
+                blk_next = block_of(j + 1);
                 const unsigned okm = __ballot_sync(0xffffffffu, (unsigned)blk < (unsigned)p.N);
                 if (CODES ? !mbar_wait(&raw_full[rx], rpar) || !mbar_wait(&v_empty[x], par ^ 1)
                           : !mbar_wait(&v_full[x], par)) {
@@ -427,20 +443,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 }
                 unsigned char* base = smem + L::v + x * L::VTILE;
-                const int r0 = min(TN, max(0, it.c - k0)), r1 = min(TN, it.kend - k0);
-                if constexpr (CODES) {
+                const int r0 = min(TN, max(0, c0 - k0)), r1 = min(TN, kend - k0);
+                if (j >= j1) {
+                    // the empty tile
+                } else if constexpr (CODES) {
                     const unsigned char* raw = smem + L::raw + rx * L::RAW;
                     constexpr int kRowChunks = D / 16;       // chunks of 16 codes
                     constexpr int kStep = 32 / kRowChunks;   // rows a warp covers at once
+                    constexpr int kRounds = TN / kStep;      // of the tile, dealt to the warps in turn
+                    constexpr int kBatch = 4;                // chunks in flight a lane
                     const int rr = lane / kRowChunks, ch = lane % kRowChunks;
                     const int cb = ch >> 2, cc = (ch & 3) * 2;
-#pragma unroll 2
-                    for (int r = fw * kStep + rr; r < TN; r += kFin * kStep) {
-                        uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                        if (r < r1 && ((okm >> (r >> 4)) & 1u)) {
-                            const uint4 c = ld_shared_v4(raw + r * D + ch * 16);
-                            widen16(c, lo, hi);
-                            if (nan_code(c)) {               // +-480 so far: NaN, or a draft's to be set aside
+#pragma unroll 1
+                    for (int y0 = fw; y0 < kRounds; y0 += kFin * kBatch) {
+                        uint4 c[kBatch];
+#pragma unroll
+                        for (int y = 0; y < kBatch; ++y) {
+                            const int r = (y0 + y * kFin) * kStep + rr;
+                            if (r < TN) c[y] = ld_shared_v4(raw + r * D + ch * 16);
+                        }
+#pragma unroll
+                        for (int y = 0; y < kBatch; ++y) {
+                            const int r = (y0 + y * kFin) * kStep + rr;
+                            if (r >= TN) break;
+                            if (r >= r1 || !((okm >> (r >> 4)) & 1u)) c[y] = make_uint4(0u, 0u, 0u, 0u);
+                            uint4 lo, hi;
+                            widen16(c[y], lo, hi);
+                            if (nan_code(c[y])) {            // +-480 so far: NaN, or a draft's to be set aside
                                 uint32_t* w[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
@@ -452,13 +481,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     }
                                 wild |= r >= r0;
                             }
+                            unsigned char* at = base + (r >> 3) * L::ATOM + cb * L::HALF_OFF + (r & 7) * 128;
+                            *reinterpret_cast<uint4*>(at + ((cc ^ (r & 7)) << 4)) = lo;
+                            *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (r & 7)) << 4)) = hi;
                         }
-                        unsigned char* at = base + (r >> 3) * L::ATOM + cb * L::HALF_OFF + (r & 7) * 128;
-                        *reinterpret_cast<uint4*>(at + ((cc ^ (r & 7)) << 4)) = lo;
-                        *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (r & 7)) << 4)) = hi;
                     }
                     tc::fence_proxy_async_smem();
-                } else if (okm != 0xffu || k0 + TN > it.c) {
+                } else if (okm != 0xffu || k0 + TN > c0) {
                     // 16-byte chunk cc of row r (its place within the swizzle does not matter);
                     // with every block id in range, the rows before the first draft stay
                     const int first = okm == (1u << ((r1 + 15) >> 4)) - 1u ? r0 : 0;
@@ -484,7 +513,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 wild = __any_sync(0xffffffffu, wild);
                 if (lane == 0) {
-                    if (j + 1 == it.j1) wild_of[(i % kRing) * 4 + fw] = wild ? 1 : 0;
+                    if (j + 1 == j1) wild_of[(i % kRing) * 4 + fw] = wild ? 1 : 0;
                     mbar_arrive(&v_ready[x]);
                     if constexpr (CODES) mbar_arrive(&raw_empty[rx]);
                 }
@@ -523,6 +552,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0) fail();
                 ok = false;
             }
+            // no lane may still be polling when lane 0 hands the barrier's slot on
+            __syncwarp();
             return ok;
         };
         auto step = [&](int& x, uint32_t& par, int n) {
@@ -531,6 +562,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 par ^= 1;
             }
         };
+        auto advance = [&]() {              // to the stream's next tile
+#pragma unroll
+            for (int k = 0; k < (QT == 1 ? 2 : 1); ++k) {
+                step(kx, kpar, L::KS);
+                step(vx, vpar, L::VS);
+            }
+        };
+        if (QT == 1 && t == 1) {            // the first tile is stream 0's
+            step(kx, kpar, L::KS);
+            step(vx, vpar, L::VS);
+        }
         for (int i = 0; ok && piece(i); ++i) {
             const PieceRec& it = ring[i % kRing];
             const int nt = steps(it, t), all = it.j1 - it.j0;
@@ -538,8 +580,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int u = 0; u < all && ok; ++u) {
                     if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
                     if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&v_empty[vx]);
-                    step(kx, kpar, L::KS);
-                    step(vx, vpar, L::VS);
+                    advance();
                 }
                 piece_done(i);
                 continue;
@@ -547,10 +588,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!need(&q_full[tq], qpar)) break;
             qpar ^= 1;
             if (nt == 0 && lane == 0) mbar_arrive(&q_empty[tq]);
-            if (QT == 1 && t == 1) {        // the first tile is stream 0's
-                step(kx, kpar, L::KS);
-                step(vx, vpar, L::VS);
-            }
 #pragma unroll 1
             for (int u = 0; u < nt && ok; ++u) {
                 if (!need(&k_full[kx], kpar)) break;
@@ -596,12 +633,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc::commit(&v_empty[vx]);
                 }
                 __syncwarp();
-                step(kx, kpar, L::KS);
-                step(vx, vpar, L::VS);
-                if (QT == 1 && 2 * u + t + 1 < all) {   // the other stream's tile
-                    step(kx, kpar, L::KS);
-                    step(vx, vpar, L::VS);
-                }
+                advance();
+            }
+            if (QT == 1 && ok && 2 * nt + t < ring_tiles(all)) {   // stream 1's empty tile: hand it back
+                if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
+                if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&v_empty[vx]);
+                advance();
             }
             piece_done(i);
         }
@@ -760,7 +797,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             }
             gs += nt;
-            g += it.j1 - it.j0;
+            g += ring_tiles(it.j1 - it.j0);
             const bool whole = it.j0 == 0 && it.j1 == it.nt;
             float w0 = 1.f, w1 = 0.f;                     // weights of the streams' O (QT = 1)
             const float2* ml = reinterpret_cast<const float2*>(smem + L::ml);

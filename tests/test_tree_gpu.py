@@ -244,6 +244,44 @@ def test_the_same_bytes_again_and_from_a_graph(name):
     R.check(other, d["out"])
 
 
+@pytest.mark.parametrize("pool,D", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64), ("f32", 64)])
+@pytest.mark.parametrize("drafts", [5, 40])
+def test_pieces_of_every_length_back_to_back(pool, D, drafts):
+    """Contexts of 1 to 17 tiles of 128 positions in an order that gives every CTA odd and even pieces, many calls
+    without a pause: each has to give the bytes of the first, and no wait may give up."""
+    r = np.random.default_rng(50)
+    cached = 128 * r.integers(0, 17, 70) + r.integers(0, 128, 70)
+    t = R.Tree([1], [1], 8, 2, D, 16, pool, seed=51, **(FP8 if pool == "fp8" else {}))
+    # the pools are random and shared: 2300 positions a request out of 300 blocks
+    t.cached, t.drafted = cached, np.full(70, drafts)
+    t.B, t.lens, t.cu = 70, (cached + drafts).astype(np.int32), (np.arange(71) * drafts).astype(np.int32)
+    t.T, t.max_q, t.max_len, t.N = 70 * drafts, drafts, int((cached + drafts).max()), 300
+    t.table = r.integers(0, 300, (70, -(-t.max_len // 16))).astype(np.int32)
+    t.k, t.v = (R.to_pool((64.0 if pool == "fp8" else 1.0) * r.standard_normal((300, 16, 2, D)), pool) for _ in range(2))
+    t.q = torch.from_numpy(r.standard_normal((t.T, 8, D))).float().to(R.act(pool))
+    t.words = -(-drafts // 32)
+    t.bits = r.integers(0, 2 ** 32, (t.T, t.words), dtype=np.uint32)
+    d = t.device()
+    ws = t.workspace()
+    first = t.run(d, ws).clone()
+    few = [0, 1, 2, 33, 69]
+    t2 = R.Tree([1], [1], 8, 2, D, 16, pool, seed=51, **(FP8 if pool == "fp8" else {}))
+    t2.__dict__.update(t.__dict__)
+    t2.cached, t2.drafted, t2.table = t.cached[few], t.drafted[few], t.table[few]
+    t2.B, t2.cu = 5, (np.arange(6) * drafts).astype(np.int32)
+    rows = np.concatenate([np.arange(drafts) + b * drafts for b in few])
+    t2.T, t2.q, t2.bits = len(rows), t.q[rows], t.bits[rows]
+    R.check(t2, first[torch.from_numpy(rows).cuda()])
+    for _ in range(60):
+        t.run(d, ws)
+    assert torch.equal(d["out"], first)
+    d["out"].fill_(7.0)
+    for _ in range(60):
+        t.run(d, ws)
+    assert torch.equal(d["out"], first)
+    assert wf.wf_device_status_fetch(d["status"]) == 0
+
+
 def test_two_streams_with_their_own_workspaces():
     a, b = CASES["several row blocks"](), CASES["many requests"]()
     da, db = a.device(), b.device()
