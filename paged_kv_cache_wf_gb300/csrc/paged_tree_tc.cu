@@ -162,10 +162,10 @@ __device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
     hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Whether one of 16 codes is NaN (S.1111.111).
-__device__ __forceinline__ bool nan_code(const uint4& c) {
-    auto n = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
-    return (n(c.x) | n(c.y) | n(c.z) | n(c.w)) != 0;
+// Not 0 when one of 16 codes is NaN (S.1111.111).
+__device__ __forceinline__ uint32_t nan_codes(const uint4& c) {
+    auto n = [](uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; };
+    return (n(c.x) | n(c.y) | n(c.z) | n(c.w)) & 0x80808080u;
 }
 
 struct NoScales {};
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(x_done, kSoftW);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&piece_full[i], 1);
-            mbar_init(&piece_empty[i], kTcThreads / 32 - 1);
+            mbar_init(&piece_empty[i], kTcThreads / 32 - 1);   // all warps but the walk's
         }
         fence_mbar_init();
         for (const CUtensorMap* m : {&tm_q, &tm_k, &tm_v})
@@ -449,41 +449,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 } else if constexpr (CODES) {
                     const unsigned char* raw = smem + L::raw + rx * L::RAW;
                     constexpr int kRowChunks = D / 16;       // chunks of 16 codes
-                    constexpr int kStep = 32 / kRowChunks;   // rows a warp covers at once
-                    constexpr int kRounds = TN / kStep;      // of the tile, dealt to the warps in turn
-                    constexpr int kBatch = 4;                // chunks in flight a lane
-                    const int rr = lane / kRowChunks, ch = lane % kRowChunks;
+                    constexpr int kStep = 32 / kRowChunks;   // rows a warp covers in a round: 4 or 8
+                    constexpr int kRounds = TN / kStep;
+                    const int ch = lane % kRowChunks, rr = lane / kRowChunks;
                     const int cb = ch >> 2, cc = (ch & 3) * 2;
+                    // round y: rows kStep y + rr; where two rounds make an 8-row atom (D = 128), the
+                    // odd one's rows are 4 further on, which flips bit 2 of a swizzled chunk's place
+                    const unsigned char* src = raw + rr * D + ch * 16;
+                    unsigned char* dst = base + cb * L::HALF_OFF + rr * 128;
+                    const int o0 = (cc ^ rr) << 4, o1 = ((cc + 1) ^ rr) << 4;
+                    auto out_at = [&](int y, int o) {
+                        return kStep == 8 ? dst + y * L::ATOM + o
+                                          : dst + (y >> 1) * L::ATOM + (y & 1) * 512 + (o ^ ((y & 1) << 6));
+                    };
+                    auto live = [&](int y) {
+                        const int row = kStep * y + rr;
+                        return row < r1 && ((okm >> (row >> 4)) & 1u);
+                    };
+                    constexpr int kBatch = 4;
+                    uint32_t nan = 0;
 #pragma unroll 1
                     for (int y0 = fw; y0 < kRounds; y0 += kFin * kBatch) {
                         uint4 c[kBatch];
 #pragma unroll
-                        for (int y = 0; y < kBatch; ++y) {
-                            const int r = (y0 + y * kFin) * kStep + rr;
-                            if (r < TN) c[y] = ld_shared_v4(raw + r * D + ch * 16);
+                        for (int k = 0; k < kBatch; ++k) {
+                            const int y = y0 + k * kFin;
+                            c[k] = make_uint4(0u, 0u, 0u, 0u);
+                            if (y < kRounds && live(y)) c[k] = ld_shared_v4(src + y * kStep * D);
                         }
 #pragma unroll
-                        for (int y = 0; y < kBatch; ++y) {
-                            const int r = (y0 + y * kFin) * kStep + rr;
-                            if (r >= TN) break;
-                            if (r >= r1 || !((okm >> (r >> 4)) & 1u)) c[y] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int k = 0; k < kBatch; ++k) {
+                            const int y = y0 + k * kFin;
+                            if (y >= kRounds) break;
                             uint4 lo, hi;
-                            widen16(c[y], lo, hi);
-                            if (nan_code(c[y])) {            // +-480 so far: NaN, or a draft's to be set aside
-                                uint32_t* w[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-#pragma unroll
-                                    for (int half = 0; half < 2; ++half) {
-                                        const uint32_t m = 0xffffu << (16 * half);
-                                        if (((*w[e] >> (16 * half)) & 0x7fffu) != 0x43f0u) continue;   // 480
-                                        *w[e] = r >= r0 ? *w[e] & ~m : *w[e] | m;
-                                    }
-                                wild |= r >= r0;
+                            widen16(c[k], lo, hi);
+                            nan |= nan_codes(c[k]);
+                            *reinterpret_cast<uint4*>(out_at(y, o0)) = lo;
+                            *reinterpret_cast<uint4*>(out_at(y, o1)) = hi;
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, nan != 0)) {
+                        // NaN codes stand as +-480: NaN, or 0 in a draft's row, which is set aside
+#pragma unroll 1
+                        for (int y = fw; y < kRounds; y += kFin) {
+                            if (!live(y)) continue;
+                            const bool draft = kStep * y + rr >= r0;
+#pragma unroll 1
+                            for (int e = 0; e < 16; ++e) {
+                                if ((src[y * kStep * D + e] & 0x7f) != 0x7f) continue;
+                                *reinterpret_cast<unsigned short*>(out_at(y, e < 8 ? o0 : o1) + (e & 7) * 2) =
+                                    draft ? 0 : 0x7fff;
+                                wild |= draft;
                             }
-                            unsigned char* at = base + (r >> 3) * L::ATOM + cb * L::HALF_OFF + (r & 7) * 128;
-                            *reinterpret_cast<uint4*>(at + ((cc ^ (r & 7)) << 4)) = lo;
-                            *reinterpret_cast<uint4*>(at + (((cc + 1) ^ (r & 7)) << 4)) = hi;
                         }
                     }
                     tc::fence_proxy_async_smem();
@@ -656,9 +673,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tok = (QT == 2 ? t * tok_tile : 0) + r / p.G;
         const bool row_fits = r < tok_tile * p.G;
         const int g_inv = (65536 + p.G - 1) / p.G;       // row / G for rows below 128
-        float scale = fabsf(p.scale_log2);
+        float scale = p.scale_log2;
         const bool negate = p.scale_log2 < 0.f;
         int4 rec = make_int4(0, 0, 0, 0);
+        const float fill = negate ? INFINITY : -INFINITY;   // of a masked score: a weight of 0
         int gs = 0, g = 0;   // steps of the stream and tiles before this piece
         bool ok = true;
         for (int i = 0; ok && piece(i); ++i) {
@@ -675,7 +693,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (i == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the q rows' factors
                 const int hs = min(it.h, kMaxScaleHeads - 1);
                 const int64_t row = ((int64_t)it.b * p.max_q_len + it.tok0 + tok) * p.H_q + it.h * p.G + r % p.G;
-                scale = fabsf(p.scale_log2) * sc.k[hs] * (row_valid ? __ldcg(p.q_inv + row) : 1.f);
+                scale = p.scale_log2 * sc.k[hs] * (row_valid ? __ldcg(p.q_inv + row) : 1.f);
                 v_scale = sc.v[hs];
             }
             float m_ref = -INFINITY, l_run = 0.f;
@@ -708,17 +726,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) tc::ld_32cols(sbase + w * 32, s[w]);
                     tc::wait_ld();
-                    if (negate) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s[w][e] = -s[w][e];
-                    }
                     if (masked) {
 #pragma unroll
                         for (int w = 0; w < 4; ++w)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) s[w][e] = (vis[w] >> e) & 1u ? s[w][e] : -INFINITY;
+                            for (int e = 0; e < 32; ++e) s[w][e] = (vis[w] >> e) & 1u ? s[w][e] : fill;
                     }
                     float m8[8];
 #pragma unroll
@@ -732,8 +744,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[3][e + 24]);
-                    const float mraw = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-                    const float mt = mraw == -INFINITY ? -INFINITY : mraw * scale;
+                    float top = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+                    if (negate) {   // the largest scaled score is the smallest score's
+                        top = INFINITY;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) top = fminf(top, s[w][e]);
+                    }
+                    const float mt = top * scale;
                     float alpha = 1.f;
                     if (m_ref == -INFINITY) {
                         m_ref = mt;
@@ -863,33 +882,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     if (!warp_live) continue;
-                    if (wild && row_valid) {
-                        // drafts whose V row is not finite: what was zeroed for P V, added to the
-                        // rows that see them
-                        const int d0 = max(0, j0 * TN - c), d1 = min(n, it.j1 * TN - c);
-                        for (int d = d0; d < d1; ++d) {
-                            const int pos = c + d;
-                            const int blk = __ldg(trow + pos / p.P);
-                            if ((unsigned)blk >= (unsigned)p.N || !tree_bit(p, q_row, d)) continue;
-                            const int64_t slot = (int64_t)blk * p.P + pos % p.P;
-                            const int64_t at = (slot * p.H_kv + it.h) * D + col;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                float x;
-                                if constexpr (CODES)
-                                    x = (static_cast<const unsigned char*>(p.v_pool)[at + e] & 0x7f) == 0x7f ? NAN : 0.f;
-                                else
-                                    x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pool)[at + e]);
-                                if (!(fabsf(x) < INFINITY)) o[e] += x;
-                            }
-                        }
-                    }
                     // through shared memory, so that a store writes whole lines: a thread has one
                     // row, and 32 rows a store would be 32 lines of 16 bytes
 #pragma unroll
                     for (int e4 = 0; e4 < 8; ++e4)
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((e4 ^ (lane & 7)) << 4)) =
                             make_float4(o[e4 * 4], o[e4 * 4 + 1], o[e4 * 4 + 2], o[e4 * 4 + 3]);
+                    if (wild && row_valid) {
+                        // drafts whose V row is not finite: what was zeroed for P V, added to the
+                        // rows that see them
+                        const int d0 = max(0, j0 * TN - c), d1 = min(n, it.j1 * TN - c);
+#pragma unroll 1
+                        for (int d = d0; d < d1; ++d) {
+                            const int pos = c + d;
+                            const int blk = __ldg(trow + pos / p.P);
+                            if ((unsigned)blk >= (unsigned)p.N || !tree_bit(p, q_row, d)) continue;
+                            const int64_t slot = (int64_t)blk * p.P + pos % p.P;
+                            const int64_t at = (slot * p.H_kv + it.h) * D + col;
+#pragma unroll 1
+                            for (int e = 0; e < 32; ++e) {
+                                float x;
+                                if constexpr (CODES)
+                                    x = (static_cast<const unsigned char*>(p.v_pool)[at + e] & 0x7f) == 0x7f ? NAN : 0.f;
+                                else
+                                    x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pool)[at + e]);
+                                float* y = reinterpret_cast<float*>(stage + lane * 128 + (((e >> 2) ^ (lane & 7)) << 4)) + (e & 3);
+                                if (!(fabsf(x) < INFINITY)) *y += x;
+                            }
+                        }
+                    }
                     __syncwarp();
                     if (whole) {
 #pragma unroll 2
