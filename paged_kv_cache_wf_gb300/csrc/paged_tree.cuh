@@ -100,9 +100,11 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
     const int per = (p.B + nthr - 1) / nthr;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     int64_t mine = 0;
+    // rolled: this runs once, and what it takes of the instruction cache is missed later
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) mine += tree_cost(p, tree_request(p, b, cta == 0), tile);
     int64_t incl = mine;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
@@ -110,6 +112,7 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
     int64_t before = 0, total = 0;
+#pragma unroll 4
     for (int w = 0; w < nwarp; ++w) {
         if (w < warp) before += scratch[w];
         total += scratch[w];
@@ -124,6 +127,7 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
     }
     if (s < e && first <= s && s < first + mine) {
         int64_t at = first;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int64_t c = tree_cost(p, tree_request(p, b, false), tile);
             if (s < at + c) {
@@ -215,6 +219,7 @@ __device__ __forceinline__ int tree_piece_slot(int cta, int j0) { return 2 * cta
 // head, last CTA that holds a piece, 1}.
 __device__ __forceinline__ int4 tree_record(const TreeParams& p, const TreeStart& st, const TreePiece& it, int cta) {
     int last = cta;
+#pragma unroll 1
     for (int64_t next = st.share * (cta + 1); next < it.end; next += st.share) ++last;
     return make_int4(it.b, it.qb * p.H_kv + it.h, last, 1);
 }

@@ -62,6 +62,15 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// mbar_wait in a rolled loop: unrolled, this kernel's waits take 50 KB of its instruction
+// cache.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < (1u << 21); ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+
 // A piece as the warps read it; nt = 0 ends the list.
 constexpr int kRing = 8;
 struct PieceRec {
@@ -200,10 +209,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     PieceRec* ring = reinterpret_cast<PieceRec*>(smem + L::ring);
     TreeStart* st = reinterpret_cast<TreeStart*>(smem + L::start);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::misc);
-    auto fail = [&]() {
-        report(p.dev_status, WF_DEV_TIMEOUT);
-        misc[1] = 1;
-    };
+    auto fail = [&]() { misc[1] = 1; };   // reported at the end
 
     if (warp == kMmaW) {
         tc::alloc(reinterpret_cast<uint32_t*>(smem + L::misc), L::TMEM_COLS);
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // the record of piece i, when it is there: false ends a warp's loop
     auto piece = [&](int i) -> bool {
         if (misc[1]) return false;
-        if (!mbar_wait(&piece_full[i % kRing], (i / kRing) & 1)) {
+        if (!bar_wait(&piece_full[i % kRing], (i / kRing) & 1)) {
             if (lane == 0) fail();
             return false;
         }
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int blk = blk_next;
                 const bool in = lane < 8 && real > 0 && pos < kend;
                 if (real > 1 && lane < 8 && pos + TN < kend) blk_next = __ldg(trow + (pos + TN) / p.P);
-                if (!mbar_wait(&empty[x], par)) {
+                if (!bar_wait(&empty[x], par)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
@@ -436,8 +442,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int blk = blk_next;
                 blk_next = block_of(j + 1);
                 const unsigned okm = __ballot_sync(0xffffffffu, (unsigned)blk < (unsigned)p.N);
-                if (CODES ? !mbar_wait(&raw_full[rx], rpar) || !mbar_wait(&v_empty[x], par ^ 1)
-                          : !mbar_wait(&v_full[x], par)) {
+                if (CODES ? !bar_wait(&raw_full[rx], rpar) || !bar_wait(&v_empty[x], par ^ 1)
+                          : !bar_wait(&v_full[x], par)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
@@ -551,13 +557,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // overwrites the columns P(u) lives in, and the tensor core executes one thread's
         // products in issue order.  One issuer for both streams was the bound at 16 products a
         // tile and stream.
-        constexpr uint32_t idS = tc::idesc_bf16_f32(TM, TN, 0, 0);
-        constexpr uint32_t idS8 = tc::idesc_e4m3_f32(TM, TN, 0, 0);
+        constexpr uint32_t idS = CODES ? tc::idesc_e4m3_f32(TM, TN, 0, 0) : tc::idesc_bf16_f32(TM, TN, 0, 0);
         constexpr uint32_t idO = tc::idesc_bf16_f32(TM, D, 0, 1);
         const int t = warp - kMmaW;
         const int tq = QT == 1 ? 0 : t;
-        const uint64_t qdesc = tc::sdesc_sw128(smem_u32(smem + L::q + tq * L::QTILE), 16, 1024);
-        const uint64_t kdesc = tc::sdesc_sw128(smem_u32(smem + L::k), 16, L::ATOM);
+        // K-major rows of 128 bytes, or (codes, D = 64) of 64
+        auto kmajor = [](uint32_t at, uint32_t atom) {
+            return CODES && D == 64 ? tc::sdesc_sw64(at, 16, 512) : tc::sdesc_sw128(at, 16, CODES ? 1024 : atom);
+        };
+        const uint64_t qdesc = kmajor(smem_u32(smem + L::q + tq * L::QTILE), 1024);
+        const uint64_t kdesc = kmajor(smem_u32(smem + L::k), L::ATOM);
         const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::v), L::HALF_OFF, L::ATOM);
         const uint32_t dS = tmem + t * L::SCOL, dO = tmem + L::OCOL + t * D;
         int kx = 0, vx = 0;                 // slots of the next tile
@@ -565,7 +574,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t qpar = 0, ppar = 0;
         bool ok = true;
         auto need = [&](uint64_t* bar, uint32_t par) {
-            if (ok && !mbar_wait(bar, par)) {
+            if (ok && !bar_wait(bar, par)) {
                 if (lane == 0) fail();
                 ok = false;
             }
@@ -606,51 +615,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             qpar ^= 1;
             if (nt == 0 && lane == 0) mbar_arrive(&q_empty[tq]);
 #pragma unroll 1
-            for (int u = 0; u < nt && ok; ++u) {
-                if (!need(&k_full[kx], kpar)) break;
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    if constexpr (CODES) {   // rows of D one-byte values: swizzled over their own width
-                        auto desc = [](uint32_t at) {
-                            return D == 128 ? tc::sdesc_sw128(at, 16, 1024) : tc::sdesc_sw64(at, 16, 512);
-                        };
-                        const uint64_t kd = desc(smem_u32(smem + L::k + kx * L::KTILE));
-                        const uint64_t qd = desc(smem_u32(smem + L::q));
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int kk = 0; kk < D / 32; ++kk)
-                                tc::mma_f8f6f4(dS, qd + (uint64_t)((part * TM * D + kk * 32) >> 4),
-                                               kd + (uint64_t)((kk * 32) >> 4), idS8, (part | kk) ? 1u : 0u);
-                    } else {
-                        const uint64_t kd = kdesc + (uint64_t)((kx * L::KTILE) >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
-                            const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
-                            tc::mma_f16(dS, qdesc + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS,
-                                        kk > 0 ? 1u : 0u);
-                        }
-                    }
-                    tc::commit(s_full(t));
-                    tc::commit(&k_empty[kx]);
-                    if (u + 1 == nt) tc::commit(&q_empty[tq]);
-                }
-                __syncwarp();
-                if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
-                ppar ^= 1;
-                tc::fence_after_sync();
-                if (lane == 0) {
+            for (int u = -1; u < nt && ok; ++u) {
+                // P V of step u ...
+                if (u >= 0) {
+                    if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
+                    ppar ^= 1;
+                    tc::fence_after_sync();
                     const uint64_t vd = vdesc + (uint64_t)((vx * L::VTILE) >> 4);
+                    if (lane == 0) {
 #pragma unroll
-                    for (int kk = 0; kk < TN / 16; ++kk)
-                        tc::mma_f16_tmem_a(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), vd + (uint64_t)((kk * 2 * L::ATOM) >> 4),
-                                           idO, (u > 0 || kk > 0) ? 1u : 0u);
-                    tc::commit(pv_done(t));
-                    tc::commit(&v_empty[vx]);
+                        for (int kk = 0; kk < TN / 16; ++kk)
+                            tc::mma_f16_tmem_a(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0),
+                                               vd + (uint64_t)((kk * 2 * L::ATOM) >> 4), idO,
+                                               (u > 0 || kk > 0) ? 1u : 0u);
+                        tc::commit(&v_empty[vx]);
+                        tc::commit(pv_done(t));
+                    }
+                    __syncwarp();
+                    advance();
                 }
-                __syncwarp();
-                advance();
+                // ... then S of step u + 1
+                if (u + 1 < nt) {
+                    if (!need(&k_full[kx], kpar)) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t kd = kdesc + (uint64_t)((kx * L::KTILE) >> 4);
+                        if constexpr (CODES) {       // the two parts of q, one after the other
+#pragma unroll
+                            for (int x = 0; x < 2 * D / 32; ++x) {
+                                const int part = x / (D / 32), kk = x % (D / 32);
+                                tc::mma_f8f6f4(dS, qdesc + (uint64_t)((part * TM * D + kk * 32) >> 4),
+                                               kd + (uint64_t)((kk * 32) >> 4), idS, x > 0 ? 1u : 0u);
+                            }
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
+                                const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
+                                tc::mma_f16(dS, qdesc + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS,
+                                            kk > 0 ? 1u : 0u);
+                            }
+                        }
+                        tc::commit(s_full(t));
+                        tc::commit(&k_empty[kx]);
+                        if (u + 2 == nt) tc::commit(&q_empty[tq]);
+                    }
+                    __syncwarp();
+                }
             }
             if (QT == 1 && ok && 2 * nt + t < ring_tiles(all)) {   // stream 1's empty tile: hand it back
                 if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
@@ -706,7 +717,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) vis[w] = row_valid ? mask_bits(mrow, p.W, k0 + 32 * w - c, n) : 0u;
                 }
-                if (!mbar_wait(s_full(t), (gs + u) & 1)) {
+                if (!bar_wait(s_full(t), (gs + u) & 1)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
@@ -761,7 +772,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         m_ref = mt;
                     }
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                        if (!mbar_wait(pv_done(t), (gs + u - 1) & 1)) fail();
+                        if (!bar_wait(pv_done(t), (gs + u - 1) & 1)) fail();
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
@@ -802,7 +813,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 __syncwarp();
                 // the first P of a piece lets P V overwrite O, which the last piece's join reads
-                if (QT == 1 && u == 0 && i > 0 && !mbar_wait(x_done, (i - 1) & 1)) {
+                if (QT == 1 && u == 0 && i > 0 && !bar_wait(x_done, (i - 1) & 1)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok) break;
             // ---- epilogue: the rows, or this piece of them ------------------------------
-            if (nt > 0 && !mbar_wait(pv_done(t), (gs + nt - 1) & 1)) {
+            if (nt > 0 && !bar_wait(pv_done(t), (gs + nt - 1) & 1)) {
                 if (lane == 0) fail();
                 break;
             }
@@ -821,7 +832,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float w0 = 1.f, w1 = 0.f;                     // weights of the streams' O (QT = 1)
             const float2* ml = reinterpret_cast<const float2*>(smem + L::ml);
             if constexpr (QT == 1) {
-                if (nt == 0 && i > 0 && !mbar_wait(x_done, (i - 1) & 1)) {
+                if (nt == 0 && i > 0 && !bar_wait(x_done, (i - 1) & 1)) {
                     if (lane == 0) fail();
                     break;
                 }
@@ -829,7 +840,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(x_ready);
-                if (!mbar_wait(x_ready, i & 1)) {
+                if (!bar_wait(x_ready, i & 1)) {
                     if (lane == 0) fail();
                     break;
                 }
@@ -953,6 +964,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     tc::fence_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && misc[1]) report(p.dev_status, WF_DEV_TIMEOUT);
     if (warp == kMmaW) {
         __syncwarp();
         tc::fence_after_sync();
