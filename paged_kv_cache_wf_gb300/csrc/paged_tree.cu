@@ -40,6 +40,7 @@ struct CcLayout {
     static constexpr int start = alpha + kCcRows * 4;
     static constexpr int scratch = start + (int)sizeof(TreeStart);
     static constexpr int total = scratch + 8 * (kCcThreads / 32);
+    static_assert(slot % 8 == 0 && start % 16 == 0 && scratch % 8 == 0, "misaligned shared memory");
 };
 
 template <typename E, int D>

@@ -74,26 +74,23 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, bool
     return r;
 }
 
-// a / b, b > 0; in 32 bits where a fits (a 64-bit division is some hundred instructions).
-__device__ __forceinline__ int64_t tree_div(int64_t a, int b) {
-    return (a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 __device__ __forceinline__ int64_t tree_cost(const TreeParams& p, const TreeReq& r, int tile) {
     if (r.n == 0) return 0;
     return (int64_t)((r.n + p.tokb - 1) / p.tokb) * p.H_kv * ((r.len + tile - 1) / tile + kTreeUnitCost);
 }
 
 // Where a CTA's stretch begins.  In shared memory, filled by tree_begin.
-struct TreeStart {
-    int64_t share;   // s
-    int64_t left;    // cost of this CTA's stretch
-    int64_t pos;     // its first cost position
-    int64_t off;     // that position within request b
+struct alignas(16) TreeStart {   // 64-bit scratch follows it in shared memory
+    int share;   // s
+    int left;    // cost of this CTA's stretch
+    int pos;     // its first cost position
+    int off;     // that position within request b
     int b;
 };
 
 // All threads of the CTA; `scratch` holds blockDim.x / 32 values.  Ends with a barrier.
+// Cost positions are 32-bit from here on: a batch of 2^31 tiles, which no memory holds but
+// shared blocks could make, is reported and not worked on.
 __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int cta, int ncta, TreeStart* st,
                                            int64_t* scratch) {
     const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nwarp = nthr >> 5;
@@ -117,19 +114,23 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    const int64_t share = tree_div(total + ncta - 1, ncta);
-    const int64_t s = min(share * cta, total), e = min(s + share, total);
-    const int64_t first = before + incl - mine;   // cost position of request b0
+    if (total > INT32_MAX) {
+        if (cta == 0 && tid == 0) report(p.dev_status, WF_DEV_BAD_SEQLEN);
+        total = mine = 0;
+    }
+    const uint32_t share = ((uint32_t)total + ncta - 1) / (uint32_t)ncta;
+    const int s = (int)min((int64_t)share * cta, total), e = (int)min((int64_t)s + share, total);
+    const int first = (int)(before + incl - mine);   // cost position of request b0
     if (tid == 0) {
-        st->share = share;
+        st->share = (int)share;
         st->left = e - s;
         st->pos = s;
     }
-    if (s < e && first <= s && s < first + mine) {
-        int64_t at = first;
+    if (s < e && first <= s && s < first + (int)mine) {
+        int at = first;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const int64_t c = tree_cost(p, tree_request(p, b, false), tile);
+            const int c = (int)tree_cost(p, tree_request(p, b, false), tile);
             if (s < at + c) {
                 st->b = b;
                 st->off = s - at;
@@ -148,13 +149,13 @@ struct TreePiece {
     int rows_tok;        // drafts of this row block
     int kend;            // positions of the request
     int j0, j1, nt;
-    int64_t end;         // cost position of the unit's end
+    int end;             // cost position of the unit's end
 };
 
 // Walks a CTA's pieces in order.  All lanes of a warp together; every warp that walks
 // sees the same pieces.
 struct TreeWalk {
-    int64_t pos, left, off;
+    int pos, left, off;
     int b, ready;        // ready: `r` holds request b
     TreeReq r;
 
@@ -169,7 +170,7 @@ struct TreeWalk {
                 ready = 1;
             }
             const int w = (r.len + tile - 1) / tile + kTreeUnitCost;
-            const int64_t units = r.n > 0 ? (int64_t)((r.n + p.tokb - 1) / p.tokb) * p.H_kv : 0;
+            const int units = r.n > 0 ? (r.n + p.tokb - 1) / p.tokb * p.H_kv : 0;
             if (off >= units * w) {
                 // the next request that has drafts: 32 looked at a round
                 off = 0;
@@ -185,9 +186,8 @@ struct TreeWalk {
                 if (b >= p.B) return false;   // not reached: the stretches end at W
                 continue;
             }
-            const int unit = (int)tree_div(off, w), x0 = (int)(off - (int64_t)unit * w);
-            const int64_t room = (int64_t)x0 + left;
-            const int x1 = (int)(room < w ? room : w);
+            const int unit = off / w, x0 = off - unit * w;
+            const int x1 = left < w - x0 ? x0 + left : w;
             it.end = pos - x0 + w;
             off += x1 - x0;
             pos += x1 - x0;
@@ -220,7 +220,7 @@ __device__ __forceinline__ int tree_piece_slot(int cta, int j0) { return 2 * cta
 __device__ __forceinline__ int4 tree_record(const TreeParams& p, const TreeStart& st, const TreePiece& it, int cta) {
     int last = cta;
 #pragma unroll 1
-    for (int64_t next = st.share * (cta + 1); next < it.end; next += st.share) ++last;
+    for (int64_t next = (int64_t)st.share * (cta + 1); next < it.end; next += st.share) ++last;
     return make_int4(it.b, it.qb * p.H_kv + it.h, last, 1);
 }
 

@@ -110,7 +110,7 @@ struct TtLayout {
     // piece_full[kRing], piece_empty[kRing]
     static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing;
     static constexpr int ring = bars + nbars * 8;        // [kRing] records of pieces
-    static constexpr int start = ring + kRing * (int)sizeof(PieceRec);
+    static constexpr int start = (ring + kRing * (int)sizeof(PieceRec) + 15) / 16 * 16;
     static constexpr int scratch = start + (int)sizeof(TreeStart);
     static constexpr int misc = scratch + 16 * 8;        // [0] TMEM address, [1] abort
     static constexpr int wild = misc + 16;               // [kRing]: a byte a finishing warp
@@ -118,7 +118,18 @@ struct TtLayout {
     static constexpr int total = okm + 16;
     static constexpr int SCOL = 128, OCOL = 256, TMEM_COLS = 512;
     static_assert(total <= 232448, "tree CTA exceeds shared memory");
+    static_assert(bars % 8 == 0 && ring % 8 == 0 && start % 16 == 0 && scratch % 8 == 0 && misc % 8 == 0 && wild % 4 == 0,
+                  "misaligned shared memory");
 };
+
+__device__ __forceinline__ void scale32(float (&o)[32], float w) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float2 y = __fmul2_rn(make_float2(o[e], o[e + 1]), make_float2(w, w));
+        o[e] = y.x;
+        o[e + 1] = y.y;
+    }
+}
 
 // 32 drafts' bits of a mask row from draft `first` on (which may lie before 0 or past the
 // row): bit x is draft first + x, set for positions before the drafts, clear past n.
@@ -142,6 +153,38 @@ __device__ __forceinline__ bool tame(uint32_t& w) {
     if ((e & 0xffff0000u) == 0x7f800000u) m |= 0xffff0000u;
     w &= ~m;
     return m != 0;
+}
+
+// tcgen05.mma with operand descriptors in halves: within a CTA only the low word, which
+// holds the address, changes, and adding to it is one instruction.  KIND 0: f16, A in
+// shared memory; 1: f16, A in tensor memory; 2: f8f6f4.
+template <int KIND>
+__device__ __forceinline__ void mma(uint32_t d_tmem, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                    uint32_t accumulate) {
+    if constexpr (KIND == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\t"
+            "mov.b64 y, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d_tmem),
+            "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else if constexpr (KIND == 0)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
 
 __device__ __forceinline__ void st_16words(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -621,13 +664,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
                     ppar ^= 1;
                     tc::fence_after_sync();
-                    const uint64_t vd = vdesc + (uint64_t)((vx * L::VTILE) >> 4);
+                    const uint32_t vd = (uint32_t)vdesc + ((vx * L::VTILE) >> 4);
                     if (lane == 0) {
 #pragma unroll
                         for (int kk = 0; kk < TN / 16; ++kk)
-                            tc::mma_f16_tmem_a(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0),
-                                               vd + (uint64_t)((kk * 2 * L::ATOM) >> 4), idO,
-                                               (u > 0 || kk > 0) ? 1u : 0u);
+                            mma<1>(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), 0u, vd + ((kk * 2 * L::ATOM) >> 4),
+                                   (uint32_t)(vdesc >> 32), idO, (u > 0 || kk > 0) ? 1u : 0u);
                         tc::commit(&v_empty[vx]);
                         tc::commit(pv_done(t));
                     }
@@ -639,21 +681,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!need(&k_full[kx], kpar)) break;
                     tc::fence_after_sync();
                     if (lane == 0) {
-                        const uint64_t kd = kdesc + (uint64_t)((kx * L::KTILE) >> 4);
+                        const uint32_t kd = (uint32_t)kdesc + ((kx * L::KTILE) >> 4), qd = (uint32_t)qdesc;
+                        const uint32_t khi = (uint32_t)(kdesc >> 32), qhi = (uint32_t)(qdesc >> 32);
                         if constexpr (CODES) {       // the two parts of q, one after the other
 #pragma unroll
                             for (int x = 0; x < 2 * D / 32; ++x) {
                                 const int part = x / (D / 32), kk = x % (D / 32);
-                                tc::mma_f8f6f4(dS, qdesc + (uint64_t)((part * TM * D + kk * 32) >> 4),
-                                               kd + (uint64_t)((kk * 32) >> 4), idS, x > 0 ? 1u : 0u);
+                                mma<2>(dS, qd + ((part * TM * D + kk * 32) >> 4), qhi, kd + ((kk * 32) >> 4), khi, idS,
+                                       x > 0 ? 1u : 0u);
                             }
                         } else {
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
                                 const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
-                                tc::mma_f16(dS, qdesc + (uint64_t)(qoff >> 4), kd + (uint64_t)(koff >> 4), idS,
-                                            kk > 0 ? 1u : 0u);
+                                mma<0>(dS, qd + (qoff >> 4), qhi, kd + (koff >> 4), khi, idS, kk > 0 ? 1u : 0u);
                             }
                         }
                         tc::commit(s_full(t));
@@ -876,20 +918,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     float o[32];
                     if (warp_live) {
                         if constexpr (QT == 1) {
-                            float o1[32];
                             tc::ld_32cols(tmem + lane_addr + L::OCOL + col, o);
-                            if (both) tc::ld_32cols(tmem + lane_addr + L::OCOL + D + col, o1);
                             tc::wait_ld();
+                            scale32(o, w0);
+                            if (both) {
+                                float o1[32];
+                                tc::ld_32cols(tmem + lane_addr + L::OCOL + D + col, o1);
+                                tc::wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                o[e] *= w0;
-                                if (both) o[e] += w1 * o1[e];
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 y = __ffma2_rn(make_float2(o1[e], o1[e + 1]), make_float2(w1, w1),
+                                                                make_float2(o[e], o[e + 1]));
+                                    o[e] = y.x;
+                                    o[e + 1] = y.y;
+                                }
                             }
                         } else {
                             tc::ld_32cols(obase + col, o);
                             tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= w0;
+                            scale32(o, w0);
                         }
                     }
                     if (!warp_live) continue;
