@@ -397,7 +397,7 @@ static bool tree_shape(const wf_pool_desc& pool, int32_t num_q_heads, int32_t ma
     const int G = num_q_heads / pool.num_kv_heads;
     if (G < 1 || G > 8) return false;
     *s = tree_tc_supported(pool, num_q_heads) ? tree_tc_shape(G, max_q_len, pool.dtype == WF_DTYPE_FP8_E4M3)
-                                              : TreeShape{kCcRows, kCcRows / G, kCcTile, 2};
+                                              : TreeShape{kCcRows, kCcRows / G, kCcTile, 2, 1};
     return true;
 }
 
@@ -466,6 +466,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint3
     p.W = a.mask_words;
     p.rows = s.rows;
     p.tokb = s.tokb;
+    p.ucost = s.ucost;
     p.q_inv = nullptr;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     // a masked score is -inf before it is scaled: a scale of 0 (equal weights) stands as the

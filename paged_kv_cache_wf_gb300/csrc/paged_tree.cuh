@@ -34,13 +34,14 @@ struct TreeParams {
     int32_t M, B, total_q, max_q_len, max_seq_len, H_q, H_kv, G, N, P, W;
     int32_t rows;    // rows of a row block in the workspace
     int32_t tokb;    // drafts of a row block
+    int32_t ucost;   // a unit's start and end, in tiles
     float scale_log2;
     const float* q_inv;   // fp8 pools on the tensor cores: factors of the prepared q rows
 };
 
 // Rows of a row block, drafts in it, tile and CTAs an SM of the kernel that runs a call.
 struct TreeShape {
-    int rows, tokb, tile, ctas_per_sm;
+    int rows, tokb, tile, ctas_per_sm, ucost;
 };
 
 // The tensor-core kernel (paged_tree_tc.cu).
@@ -52,7 +53,6 @@ cudaError_t launch_tree_tc(const TreeParams& p, const wf_pool_desc& pool, void* 
 namespace {
 
 constexpr int kTreeMaxSms = 160;    // SMs a launch may use (the workspace holds their CTAs' pieces)
-constexpr int kTreeUnitCost = 2;    // a unit's start and end, in tiles
 
 // A request's drafts and length, n = 0 for one that fails the checks.
 struct TreeReq {
@@ -76,7 +76,7 @@ __device__ __forceinline__ TreeReq tree_request(const TreeParams& p, int b, bool
 
 __device__ __forceinline__ int64_t tree_cost(const TreeParams& p, const TreeReq& r, int tile) {
     if (r.n == 0) return 0;
-    return (int64_t)((r.n + p.tokb - 1) / p.tokb) * p.H_kv * ((r.len + tile - 1) / tile + kTreeUnitCost);
+    return (int64_t)((r.n + p.tokb - 1) / p.tokb) * p.H_kv * ((r.len + tile - 1) / tile + p.ucost);
 }
 
 // Where a CTA's stretch begins.  In shared memory, filled by tree_begin.
@@ -169,7 +169,7 @@ struct TreeWalk {
                 r = tree_request(p, b, false);
                 ready = 1;
             }
-            const int w = (r.len + tile - 1) / tile + kTreeUnitCost;
+            const int w = (r.len + tile - 1) / tile + p.ucost;
             const int units = r.n > 0 ? (r.n + p.tokb - 1) / p.tokb * p.H_kv : 0;
             if (off >= units * w) {
                 // the next request that has drafts: 32 looked at a round
@@ -193,10 +193,10 @@ struct TreeWalk {
             pos += x1 - x0;
             left -= x1 - x0;
             // the unit's fixed cost stands before its tiles
-            it.j0 = max(0, x0 - kTreeUnitCost);
-            it.j1 = max(0, x1 - kTreeUnitCost);
+            it.j0 = max(0, x0 - p.ucost);
+            it.j1 = max(0, x1 - p.ucost);
             if (it.j0 >= it.j1) continue;
-            it.nt = w - kTreeUnitCost;
+            it.nt = w - p.ucost;
             it.b = b;
             it.qb = unit / p.H_kv;
             it.h = unit - it.qb * p.H_kv;
