@@ -169,6 +169,9 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of current_stream()'s time
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -212,6 +215,23 @@ def pool_desc(k_pool, k_scale=1.0, v_scale=1.0) -> wf_pool_desc:
     return d
 
 
+_descs = {}   # descriptors by pool geometry and per-tensor scales
+
+
+def _desc(k_pool, k_scale, v_scale):
+    """pool_desc, made once for each geometry and pair of per-tensor scales."""
+    try:
+        key = (k_pool.shape, k_pool.dtype, k_scale, v_scale)
+        d = _descs.get(key)
+    except TypeError:      # per-head scales (lists, arrays): made anew
+        return pool_desc(k_pool, k_scale, v_scale)
+    if d is None:
+        d = pool_desc(k_pool, k_scale, v_scale)
+        if isinstance(k_scale, (int, float)) and isinstance(v_scale, (int, float)) and len(_descs) < 1024:
+            _descs[key] = d
+    return d
+
+
 def _contig(*ts):
     for t in ts:
         if t is not None and not isinstance(t, int) and not t.is_contiguous():
@@ -233,16 +253,6 @@ def wf_reshape_and_cache(k, v, k_pool, v_pool, slot_mapping, dev_status=None, st
     _check("wf_reshape_and_cache", rc)
 
 
-def _token_stride(name, t, dt, n):
-    """Elements between the tokens of t [n, heads, D], whose heads and elements are dense."""
-    if t.dim() != 3 or t.shape[0] != n or t.dtype != dt:
-        raise ValueError(f"{name} must be [{n}, heads, D] of {dt}")
-    token, head, elt = t.stride()
-    if elt != 1 or (head != t.shape[2] and t.shape[1] > 1):
-        raise ValueError(f"{name}: heads and elements of a token must be dense")
-    return token if n > 1 else t.shape[1] * t.shape[2]
-
-
 def wf_qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps: float, cos_sin, positions, k_pool, v_pool,
                               slot_mapping, interleaved: bool = False, dev_status=None, stream=None, k_scale=1.0,
                               v_scale=1.0):
@@ -252,26 +262,34 @@ def wf_qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps: float, co
     import torch
     _contig(q_out, q_weight, k_weight, cos_sin, positions, k_pool, v_pool, slot_mapping)
     T, H_q, D = q.shape
-    N, P, H_kv, pool_D = k_pool.shape
-    dt = torch.bfloat16 if k_pool.dtype == torch.uint8 else k_pool.dtype
-    strides = [_token_stride(n, t, dt, T) for n, t in (("q", q), ("k", k), ("v", v))]
-    if q_out.shape != q.shape or q_out.dtype != dt or slot_mapping.shape[0] != T or D != pool_D or             k.shape[1:] != (H_kv, D) or v.shape[1:] != (H_kv, D) or slot_mapping.dtype != torch.int64:
-        raise ValueError("q_out is like q, k and v are [T, H_kv, D] of the pool, slot_mapping is [T] int64")
+    _, _, H_kv, pool_D = k_pool.shape
+    dt, pool_dt = q.dtype, k_pool.dtype
+    if D != pool_D or dt is not (torch.bfloat16 if pool_dt is torch.uint8 else pool_dt) or \
+            q_out.shape != q.shape or q_out.dtype is not dt or v_pool.shape != k_pool.shape or v_pool.dtype is not pool_dt:
+        raise ValueError("q, k, v and q_out have the pool's dtype (bf16 for fp8 pools) and head size, q_out is like q")
+    rows = (T, H_kv, D)
+    if k.shape != rows or v.shape != rows or k.dtype is not dt or v.dtype is not dt:
+        raise ValueError(f"k and v must be {list(rows)} of {dt}")
+    (qs, qh, qe), (ks, kh, ke), (vs, vh, ve) = q.stride(), k.stride(), v.stride()
+    if qe != 1 or ke != 1 or ve != 1 or (qh != D and H_q > 1) or ((kh != D or vh != D) and H_kv > 1):
+        raise ValueError("q, k, v: heads and elements of a token must be dense")
+    if slot_mapping.shape[0] != T or slot_mapping.dtype is not torch.int64:
+        raise ValueError(f"slot_mapping must be [{T}] int64")
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != dt or w.numel() != D):
+        if w is not None and (w.dtype is not dt or w.numel() != D):
             raise ValueError(f"norm weights must be [{D}] of {dt}")
-    rotary, rows = 0, 0
+    max_position = rotary = 0
     if cos_sin is not None:
-        rows, rotary = cos_sin.shape
-        if cos_sin.dtype != torch.float32 or positions.dtype != torch.int32 or positions.shape[0] != T:
+        max_position, rotary = cos_sin.shape
+        if cos_sin.dtype is not torch.float32 or positions.dtype is not torch.int32 or positions.shape[0] != T:
             raise ValueError("cos_sin must be [max_position, rotary_dim] float32 and positions [T] int32")
-    lib = load()
-    rc = lib.wf_qk_norm_rope_and_cache(_ptr(q_out), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2],
-                                       _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin), rows, rotary,
-                                       int(interleaved), _ptr(positions) if rotary else None, _ptr(k_pool),
-                                       _ptr(v_pool), _ptr(slot_mapping), T, H_q, pool_desc(k_pool, k_scale, v_scale),
-                                       _ptr(dev_status), _stream(stream))
-    _check("wf_qk_norm_rope_and_cache", rc)
+    rc = load().wf_qk_norm_rope_and_cache(
+        q_out.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight), eps,
+        _ptr(cos_sin), max_position, rotary, interleaved, _ptr(positions) if rotary else None, k_pool.data_ptr(),
+        v_pool.data_ptr(), slot_mapping.data_ptr(), T, H_q, _desc(k_pool, k_scale, v_scale), _ptr(dev_status),
+        _stream(stream))
+    if rc:
+        raise WfError("wf_qk_norm_rope_and_cache", rc)
 
 
 def wf_copy_blocks(k_pool, v_pool, block_pairs, dev_status=None, stream=None, k_scale=1.0,
@@ -350,20 +368,22 @@ def wf_paged_tree_decode(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_le
     """out, q [T_total, H_q, D] packed drafts; cu_q_lens [B+1] int32; seq_lens [B] int32 count the drafts; tree_mask
     [T_total, words] int32 (bit j of a row: draft j of its request is seen); workspace uint8 tensor."""
     _contig(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, tree_mask)
-    lib = load()
     T, H_q, D = q.shape
     B, M = block_tables.shape
-    if out.shape != q.shape or out.dtype != q.dtype or D != k_pool.shape[3] or tree_mask.shape[0] != T or \
-            tree_mask.element_size() != 4 or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or \
-            q.element_size() != max(2, k_pool.element_size()):
-        raise ValueError("out is like q [T, H_q, D] of the pool's dtype (bf16 for fp8 pools), tree_mask [T, words] of "
-                         "32-bit words, block_tables [B, M], seq_lens [B], cu_q_lens [B + 1]")
-    rc = lib.wf_paged_tree_decode(_ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), M,
-                                  _ptr(seq_lens), _ptr(cu_q_lens), _ptr(tree_mask), tree_mask.shape[1], B, T,
-                                  max_q_len, max_seq_len, H_q, scale, pool_desc(k_pool, k_scale, v_scale),
-                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
-                                  _stream(stream))
-    _check("wf_paged_tree_decode", rc)
+    rows, words = tree_mask.shape
+    if out.shape != q.shape or out.dtype is not q.dtype or D != k_pool.shape[3] or \
+            q.element_size() != max(2, k_pool.element_size()) or v_pool.shape != k_pool.shape or \
+            v_pool.dtype is not k_pool.dtype:
+        raise ValueError("out is like q [T, H_q, D] of the pool's dtype (bf16 for fp8 pools) and head size")
+    if rows != T or tree_mask.element_size() != 4 or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1:
+        raise ValueError("tree_mask is [T, words] of 32-bit words, block_tables [B, M], seq_lens [B], cu_q_lens [B + 1]")
+    rc = load().wf_paged_tree_decode(
+        out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), M,
+        seq_lens.data_ptr(), cu_q_lens.data_ptr(), tree_mask.data_ptr(), words, B, T, max_q_len, max_seq_len, H_q, scale,
+        _desc(k_pool, k_scale, v_scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status), _stream(stream))
+    if rc:
+        raise WfError("wf_paged_tree_decode", rc)
 
 
 def wf_keep_accepted(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted, num_accepted, new_seq_lens=None,
@@ -372,13 +392,16 @@ def wf_keep_accepted(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted
     of its drafts in both pools; new_seq_lens [B] int32 receives the kept lengths."""
     _contig(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted, num_accepted, new_seq_lens)
     B, M = block_tables.shape
-    if accepted.shape[0] != B or num_accepted.shape[0] != B or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 \
-            or (new_seq_lens is not None and new_seq_lens.shape[0] != B):
+    paths, depth = accepted.shape
+    if paths != B or num_accepted.shape[0] != B or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or \
+            v_pool.shape != k_pool.shape or (new_seq_lens is not None and new_seq_lens.shape[0] != B):
         raise ValueError("accepted [B, depth], num_accepted, seq_lens and new_seq_lens [B], cu_q_lens [B + 1]")
-    rc = load().wf_keep_accepted(_ptr(k_pool), _ptr(v_pool), _ptr(block_tables), M, _ptr(seq_lens), _ptr(cu_q_lens),
-                                 _ptr(accepted), accepted.shape[1], _ptr(num_accepted), _ptr(new_seq_lens), B,
-                                 pool_desc(k_pool, k_scale, v_scale), _ptr(dev_status), _stream(stream))
-    _check("wf_keep_accepted", rc)
+    rc = load().wf_keep_accepted(
+        k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), M, seq_lens.data_ptr(), cu_q_lens.data_ptr(),
+        accepted.data_ptr(), depth, num_accepted.data_ptr(), _ptr(new_seq_lens), B, _desc(k_pool, k_scale, v_scale),
+        _ptr(dev_status), _stream(stream))
+    if rc:
+        raise WfError("wf_keep_accepted", rc)
 
 
 WF_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024
