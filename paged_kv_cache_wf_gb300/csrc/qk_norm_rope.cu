@@ -11,11 +11,15 @@
 //
 // HBM-bound: every byte of q, k, v is read once and every result written once; doing
 // it in one pass saves the second read and write of q and k that separate norm,
-// rotation and scatter passes make.  A head row is D / VEC lanes of one 16-byte chunk
-// each, so a warp holds one, two or four rows; the sum of squares is a shuffle
-// reduction over the row's lanes, and a rotated pair's other half comes from the lane
-// that holds it (one shuffle a 32-bit word, of the raw chunk: both halves share the
-// row's norm factor).  A CTA works on IT rows a lane group of one token, so a lane
+// rotation and scatter passes make.  What has to be watched is the instruction count:
+// a form of 166 instructions a warp and row pair took 51 us for 8193 tokens of
+// Llama-3-8B heads into fp8 pools, whose bytes take 28.  So a head row is D / VEC lanes
+// of one 16-byte chunk each and a warp's rows are of one kind (each kind's rows are
+// padded to whole warps), which keeps the choice of q, k or v a branch of the warp;
+// arithmetic is on pairs (two fp32 operations an instruction); and an instance without
+// weights has no norm in it.  The sum of squares is a shuffle reduction over the row's
+// lanes, and a rotated pair's other half comes from the lane that holds it (one shuffle
+// a 32-bit word, of the raw chunk: both halves share the row's norm factor).  A lane
 // reads its cos and sin once for IT rows.
 #include "wf_internal.h"
 
@@ -26,7 +30,6 @@ namespace {
 struct RopeParams {
     RopeArgs a;
     int64_t num_slots;
-    int rows;          // H_q + 2 H_kv
     int H_kv;
     uint32_t* dev_status;
 };
@@ -48,50 +51,81 @@ __device__ __forceinline__ float widen_one<BF16>(const void* row, int e) {
     return __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(row) + e) << 16);
 }
 
+// A 16-byte chunk as pairs of floats, and back.
 template <typename E>
-__device__ __forceinline__ uint4 narrow_chunk(const float* f);
+__device__ __forceinline__ void to_pairs(const uint4& c, float2* f);
 template <>
-__device__ __forceinline__ uint4 narrow_chunk<F32>(const float* f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+__device__ __forceinline__ void to_pairs<F32>(const uint4& c, float2* f) {
+    f[0] = make_float2(__uint_as_float(c.x), __uint_as_float(c.y));
+    f[1] = make_float2(__uint_as_float(c.z), __uint_as_float(c.w));
 }
 template <>
-__device__ __forceinline__ uint4 narrow_chunk<BF16>(const float* f) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ void to_pairs<BF16>(const uint4& c, float2* f) {
+    f[0] = bf16x2_to_float2(c.x);
+    f[1] = bf16x2_to_float2(c.y);
+    f[2] = bf16x2_to_float2(c.z);
+    f[3] = bf16x2_to_float2(c.w);
+}
+template <typename E>
+__device__ __forceinline__ uint4 from_pairs(const float2* f);
+template <>
+__device__ __forceinline__ uint4 from_pairs<F32>(const float2* f) {
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                      __float_as_uint(f[1].y));
+}
+template <>
+__device__ __forceinline__ uint4 from_pairs<BF16>(const float2* f) {
+    return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                      pack_bf16x2(f[3].x, f[3].y));
 }
 
-__device__ __forceinline__ uint32_t codes4(const float* f, float inv) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * inv, f[1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2] * inv, f[3] * inv), __NV_SATFINITE, __NV_E4M3);
+// Four values -> their e4m3 codes.
+__device__ __forceinline__ uint32_t codes4(const float2& a, const float2& b, const float2& inv) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(__fmul2_rn(a, inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(__fmul2_rn(b, inv), __NV_SATFINITE, __NV_E4M3);
     return (lo & 0xffffu) | (hi << 16);
 }
 
-// WIDE: rotary_dim is a multiple of 16, so no pair's halves cross a chunk border at
-// different places and the table is read in 16-byte chunks.  Otherwise each element
+// A 16-byte chunk of weights.
+template <typename E>
+__device__ __forceinline__ void weight_pairs(const void* w, int chunk, float2* f) {
+    to_pairs<E>(__ldg(static_cast<const uint4*>(w) + chunk), f);
+}
+
+// Rows of one kind, in whole warps.
+template <typename E, int D>
+__host__ __device__ constexpr int padded_rows(int n) {
+    constexpr int RPW = 32 * E::kPerChunk / D > 0 ? 32 * E::kPerChunk / D : 1;
+    return (n + RPW - 1) / RPW * RPW;
+}
+
+// WIDE: rotary_dim is a multiple of 16, so a chunk's other halves lie in one chunk, at
+// the same places, and the table is read in 16-byte pieces.  Otherwise each element
 // fetches its pair's other half, its cos and its sin by itself.
-template <typename E, bool CODES, int D, int IT, bool WIDE>
+// CTA (t, y): token t, row places y RPB IT .. ; a place is q's rows, then k's, then v's.
+template <typename E, bool CODES, int D, int IT, bool WIDE, bool NORM>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p, const InvScales inv) {
-    constexpr int VEC = E::kPerChunk, LG = D / VEC, RPB = 256 / LG, WORDS = 4;
-    const int64_t t = blockIdx.x;
-    const int lg = threadIdx.x % LG;
-    const int row0 = blockIdx.y * (RPB * IT) + threadIdx.x / LG;
+    constexpr int VEC = E::kPerChunk, NP = VEC / 2, LG = D / VEC, RPB = 256 / LG;
+    const int lg = threadIdx.x % LG, lane = threadIdx.x & 31;
+    const int place0 = blockIdx.y * (RPB * IT) + threadIdx.x / LG;
     const int e0 = lg * VEC;
     const int H_q = p.a.num_q_heads;
-    const int64_t slot = __ldg(p.a.slot_mapping + t);
+    const int q_end = padded_rows<E, D>(H_q), k_end = q_end + padded_rows<E, D>(p.H_kv);
     const int rot = p.a.rotary_dim, half = rot >> 1;
+    const bool turned = e0 < rot, inter = p.a.interleaved != 0, low = e0 < half;
+    const int64_t t = blockIdx.x;
+    const int64_t slot = __ldg(p.a.slot_mapping + t);
     const int pos = rot > 0 ? __ldg(p.a.positions + t) : 0;
-    auto row_ptr = [&](int r) -> const char* {
-        const int64_t off = r < H_q            ? t * p.a.q_stride + (int64_t)r * D
-                            : r < H_q + p.H_kv ? t * p.a.k_stride + (int64_t)(r - H_q) * D
-                                               : t * p.a.v_stride + (int64_t)(r - H_q - p.H_kv) * D;
-        const void* base = r < H_q ? p.a.q : r < H_q + p.H_kv ? p.a.k : p.a.v;
-        return static_cast<const char*>(base) + off * E::kBytes;
-    };
     uint4 x[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int r = row0 + i * RPB;
-        x[i] = r < p.rows ? ld_global_stream(row_ptr(r) + lg * 16) : make_uint4(0u, 0u, 0u, 0u);
+        const int place = place0 + i * RPB;
+        const int kind = place < q_end ? 0 : place < k_end ? 1 : 2;
+        const int h = place - (kind == 0 ? 0 : kind == 1 ? q_end : k_end);
+        const char* base = static_cast<const char*>(kind == 0 ? p.a.q : kind == 1 ? p.a.k : p.a.v);
+        const int64_t stride = kind == 0 ? p.a.q_stride : kind == 1 ? p.a.k_stride : p.a.v_stride;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < (kind == 0 ? H_q : p.H_kv)) x[i] = ld_global_stream(base + (t * stride + h * D + e0) * E::kBytes);
     }
     if (slot < 0) return;   // padding token
     if (slot >= p.num_slots || (unsigned)pos >= (unsigned)(rot > 0 ? p.a.max_position : 1)) {
@@ -99,37 +133,34 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p, c
             report(p.dev_status, slot >= p.num_slots ? WF_DEV_BAD_SLOT : WF_DEV_BAD_POSITION);
         return;
     }
-    // cos and (signed) sin of this lane's elements, and the lane that holds their pairs
-    const bool turned = e0 < rot, inter = p.a.interleaved != 0;
+    // cos and (signed) sin of this lane's elements, and the lane that holds their other halves
     const float* table = p.a.cos_sin + (int64_t)pos * rot;
-    float c[VEC], s[VEC];
-    int mate = threadIdx.x & 31;
+    float2 c[NP], s[NP];
+    int mate = lane;
     if (turned) {
         if constexpr (WIDE) {
             if (inter) {
-                const float* tc = table + e0 / 2;
-                const float* ts = tc + half;
 #pragma unroll
-                for (int e = 0; e < VEC; e += 4) {
-                    const float2 cc = __ldg(reinterpret_cast<const float2*>(tc + e / 2));
-                    const float2 ss = __ldg(reinterpret_cast<const float2*>(ts + e / 2));
-                    c[e] = c[e + 1] = cc.x;
-                    c[e + 2] = c[e + 3] = cc.y;
-                    s[e] = -ss.x; s[e + 1] = ss.x;
-                    s[e + 2] = -ss.y; s[e + 3] = ss.y;
+                for (int e = 0; e < NP; e += 2) {
+                    const float2 cc = __ldg(reinterpret_cast<const float2*>(table + e0 / 2 + e));
+                    const float2 ss = __ldg(reinterpret_cast<const float2*>(table + half + e0 / 2 + e));
+                    c[e] = make_float2(cc.x, cc.x);
+                    c[e + 1] = make_float2(cc.y, cc.y);
+                    s[e] = make_float2(-ss.x, ss.x);
+                    s[e + 1] = make_float2(-ss.y, ss.y);
                 }
             } else {
-                const bool low = e0 < half;
                 const float* tc = table + (low ? e0 : e0 - half);
-                const float* ts = tc + half;
-                mate += low ? half / VEC : -(half / VEC);
+                const float sign = low ? -1.f : 1.f;
+                mate = low ? lane + half / VEC : lane - half / VEC;
 #pragma unroll
-                for (int e = 0; e < VEC; e += 4) {
-                    const float4 cc = __ldg(reinterpret_cast<const float4*>(tc + e));
-                    const float4 ss = __ldg(reinterpret_cast<const float4*>(ts + e));
-                    c[e] = cc.x; c[e + 1] = cc.y; c[e + 2] = cc.z; c[e + 3] = cc.w;
-                    s[e] = low ? -ss.x : ss.x; s[e + 1] = low ? -ss.y : ss.y;
-                    s[e + 2] = low ? -ss.z : ss.z; s[e + 3] = low ? -ss.w : ss.w;
+                for (int e = 0; e < NP; e += 2) {
+                    const float4 cc = __ldg(reinterpret_cast<const float4*>(tc + 2 * e));
+                    const float4 ss = __ldg(reinterpret_cast<const float4*>(tc + half + 2 * e));
+                    c[e] = make_float2(cc.x, cc.y);
+                    c[e + 1] = make_float2(cc.z, cc.w);
+                    s[e] = __fmul2_rn(make_float2(ss.x, ss.y), make_float2(sign, sign));
+                    s[e + 1] = __fmul2_rn(make_float2(ss.z, ss.w), make_float2(sign, sign));
                 }
             }
         } else {
@@ -138,112 +169,132 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p, c
                 const int g = e0 + e;
                 const bool first = inter ? (g & 1) == 0 : g < half;
                 const int i = inter ? g >> 1 : first ? g : g - half;
-                c[e] = g < rot ? __ldg(table + i) : 1.f;
-                const float sn = g < rot ? __ldg(table + half + i) : 0.f;
-                s[e] = first ? -sn : sn;
+                const float cs = g < rot ? __ldg(table + i) : 1.f;
+                float sn = g < rot ? __ldg(table + half + i) : 0.f;
+                if (first) sn = -sn;
+                if (e & 1) {
+                    c[e / 2].y = cs;
+                    s[e / 2].y = sn;
+                } else {
+                    c[e / 2].x = cs;
+                    s[e / 2].x = sn;
+                }
             }
         }
     }
+    const int64_t slot_row = slot * p.H_kv * D + e0, token_row = t * H_q * D + e0;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int r = row0 + i * RPB;
-        const bool live = r < p.rows;
-        const bool is_q = r < H_q, is_k = !is_q && r < H_q + p.H_kv;
-        const int h = is_q ? r : is_k ? r - H_q : r - H_q - p.H_kv;
-        float y[VEC];
-        widen_chunk<E>(x[i], y);
-        const void* w = is_q ? p.a.q_weight : is_k ? p.a.k_weight : nullptr;
-        float ss = 0.f;
+        const int place = place0 + i * RPB;
+        if (place >= k_end) {                       // V: as it is
+            const int h = place - k_end;
+            if (h >= p.H_kv) continue;
+            char* out = static_cast<char*>(p.a.v_pool) + (slot_row + h * D) * (CODES ? 1 : E::kBytes);
+            if constexpr (CODES) {
+                const float f = inv.v[min(h, kMaxScaleHeads - 1)];
+                float2 y[NP];
+                to_pairs<E>(x[i], y);
+                *reinterpret_cast<uint2*>(out) = make_uint2(codes4(y[0], y[1], make_float2(f, f)),
+                                                            codes4(y[NP - 2], y[NP - 1], make_float2(f, f)));
+            } else {
+                st_global_v4(out, x[i]);
+            }
+            continue;
+        }
+        const bool is_q = place < q_end;
+        const int h = is_q ? place : place - q_end;
+        const bool live = h < (is_q ? H_q : p.H_kv);
+        const void* w = is_q ? p.a.q_weight : p.a.k_weight;
+        float2 y[NP], z[NP];
+        to_pairs<E>(x[i], y);
+        if (WIDE && rot > 0 && !inter) {
+            uint4 m;
+            m.x = __shfl_sync(0xffffffffu, x[i].x, mate);
+            m.y = __shfl_sync(0xffffffffu, x[i].y, mate);
+            m.z = __shfl_sync(0xffffffffu, x[i].z, mate);
+            m.w = __shfl_sync(0xffffffffu, x[i].w, mate);
+            to_pairs<E>(m, z);
+        }
+        float rs = 1.f;
+        if (NORM && w != nullptr) {
+            float2 sq = __fmul2_rn(y[0], y[0]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) ss += y[e] * y[e];
+            for (int e = 1; e < NP; ++e) sq = __ffma2_rn(y[e], y[e], sq);
+            float ss = sq.x + sq.y;
 #pragma unroll
-        for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rs = w != nullptr ? rsqrtf(ss * (1.f / D) + p.a.eps) : 1.f;
-        // the other halves, raw: from the lane that holds them
-        float z[VEC];
-        if constexpr (WIDE) {
-            uint32_t m[WORDS] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            rs = rsqrtf(ss * (1.f / D) + p.a.eps);
+            const float2 r2 = make_float2(rs, rs);
+            float2 f[NP];
+            weight_pairs<E>(w, lg, f);
 #pragma unroll
-            for (int k = 0; k < WORDS; ++k) m[k] = __shfl_sync(0xffffffffu, m[k], mate);
-            widen_chunk<E>(make_uint4(m[0], m[1], m[2], m[3]), z);
+            for (int e = 0; e < NP; ++e) y[e] = __fmul2_rn(__fmul2_rn(y[e], r2), f[e]);
+            if (WIDE && !inter && turned) {
+                weight_pairs<E>(w, lg + mate - lane, f);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) z[e] = __fmul2_rn(__fmul2_rn(z[e], r2), f[e]);
+            }
         }
         if (!live) continue;
-        if (w != nullptr) {
-            float f[VEC];
-            widen_chunk<E>(__ldg(reinterpret_cast<const uint4*>(w) + lg), f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = y[e] * rs * f[e];
-        }
-        if (turned && (is_q || is_k)) {
+        if (turned) {
             if (inter) {   // pairs lie side by side in the chunk, normed already
 #pragma unroll
-                for (int e = 0; e < VEC; e += 2) {
-                    z[e] = y[e + 1];
-                    z[e + 1] = y[e];
-                }
-            } else if constexpr (WIDE) {
-                if (w != nullptr) {
-                    float f[VEC];
-                    widen_chunk<E>(__ldg(reinterpret_cast<const uint4*>(w) + (lg + mate - (int)(threadIdx.x & 31))), f);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) z[e] = z[e] * rs * f[e];
-                }
-            } else {
-                const char* src = row_ptr(r);
+                for (int e = 0; e < NP; ++e) z[e] = make_float2(y[e].y, y[e].x);
+            } else if constexpr (!WIDE) {
+                const char* row = static_cast<const char*>(is_q ? p.a.q : p.a.k) +
+                                  (t * (is_q ? p.a.q_stride : p.a.k_stride) + h * D) * E::kBytes;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int g = e0 + e;
                     const int o = g < half ? g + half : g - half;
                     float b = 0.f;
                     if (g < rot) {
-                        b = widen_one<E>(src, o);
-                        if (w != nullptr) b = b * rs * widen_one<E>(w, o);
+                        b = widen_one<E>(row, o);
+                        if (NORM && w != nullptr) b = b * rs * widen_one<E>(w, o);
                     }
-                    z[e] = b;
+                    if (e & 1) z[e / 2].y = b;
+                    else z[e / 2].x = b;
                 }
             }
-            if constexpr (WIDE) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) y[e] = y[e] * c[e] + z[e] * s[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (e0 + e < rot) y[e] = y[e] * c[e] + z[e] * s[e];
+            for (int e = 0; e < NP; ++e) {
+                const float2 r2 = __ffma2_rn(z[e], s[e], __fmul2_rn(y[e], c[e]));
+                if (WIDE || e0 + 2 * e + 1 < rot) y[e] = r2;   // rotary_dim is even: a pair is in or out
             }
         }
         if (is_q) {
-            st_global_v4(static_cast<char*>(p.a.q_out) + ((t * H_q + h) * D + e0) * E::kBytes, narrow_chunk<E>(y));
+            st_global_v4(static_cast<char*>(p.a.q_out) + (token_row + h * D) * E::kBytes, from_pairs<E>(y));
+        } else if constexpr (CODES) {
+            const float f = inv.k[min(h, kMaxScaleHeads - 1)];
+            *reinterpret_cast<uint2*>(static_cast<char*>(p.a.k_pool) + slot_row + h * D) =
+                make_uint2(codes4(y[0], y[1], make_float2(f, f)), codes4(y[NP - 2], y[NP - 1], make_float2(f, f)));
         } else {
-            char* pool = static_cast<char*>(is_k ? p.a.k_pool : p.a.v_pool);
-            const int64_t at = (slot * p.H_kv + h) * D + e0;
-            if constexpr (CODES) {
-                const int hs = min(h, kMaxScaleHeads - 1);
-                const float iv = is_k ? inv.k[hs] : inv.v[hs];
-                *reinterpret_cast<uint2*>(pool + at) = make_uint2(codes4(y, iv), codes4(y + 4, iv));
-            } else {
-                st_global_v4(pool + at * E::kBytes, narrow_chunk<E>(y));
-            }
+            st_global_v4(static_cast<char*>(p.a.k_pool) + (slot_row + h * D) * E::kBytes, from_pairs<E>(y));
         }
     }
 }
 
 template <typename E, bool CODES, int D, int IT>
-cudaError_t launch_rows(const RopeParams& p, const InvScales& inv, cudaStream_t stream) {
+cudaError_t launch_rows(const RopeParams& p, const InvScales& inv, int places, cudaStream_t stream) {
     constexpr int RPB = 256 / (D / E::kPerChunk);
-    const dim3 grid((unsigned)p.a.num_tokens, (unsigned)((p.rows + RPB * IT - 1) / (RPB * IT)));
-    if (p.a.rotary_dim % 16 == 0)
-        qk_norm_rope_kernel<E, CODES, D, IT, true><<<grid, 256, 0, stream>>>(p, inv);
+    const dim3 grid((unsigned)p.a.num_tokens, (unsigned)((places + RPB * IT - 1) / (RPB * IT)));
+    const bool norm = p.a.q_weight != nullptr || p.a.k_weight != nullptr;
+    if (p.a.rotary_dim % 16 != 0)
+        qk_norm_rope_kernel<E, CODES, D, IT, false, true><<<grid, 256, 0, stream>>>(p, inv);
+    else if (norm)
+        qk_norm_rope_kernel<E, CODES, D, IT, true, true><<<grid, 256, 0, stream>>>(p, inv);
     else
-        qk_norm_rope_kernel<E, CODES, D, IT, false><<<grid, 256, 0, stream>>>(p, inv);
+        qk_norm_rope_kernel<E, CODES, D, IT, true, false><<<grid, 256, 0, stream>>>(p, inv);
     return cudaGetLastError();
 }
 
 template <typename E, bool CODES, int D>
 cudaError_t launch_width(const RopeParams& p, const InvScales& inv, cudaStream_t stream) {
     constexpr int RPB = 256 / (D / E::kPerChunk);
-    const int64_t one = (int64_t)p.a.num_tokens * ((p.rows + RPB - 1) / RPB);
-    if (one <= 4 * (int64_t)num_sms()) return launch_rows<E, CODES, D, 1>(p, inv, stream);
-    return launch_rows<E, CODES, D, 3>(p, inv, stream);
+    const int places = padded_rows<E, D>(p.a.num_q_heads) + 2 * padded_rows<E, D>(p.H_kv);
+    const int64_t one = (int64_t)p.a.num_tokens * ((places + RPB - 1) / RPB);
+    if (one <= 4 * (int64_t)num_sms()) return launch_rows<E, CODES, D, 1>(p, inv, places, stream);
+    return launch_rows<E, CODES, D, 3>(p, inv, places, stream);
 }
 
 }  // namespace
@@ -254,7 +305,6 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, const wf_pool_desc& pool, uin
     p.a = a;
     p.num_slots = (int64_t)pool.num_blocks * pool.block_size;
     p.H_kv = pool.num_kv_heads;
-    p.rows = a.num_q_heads + 2 * pool.num_kv_heads;
     p.dev_status = dev_status;
     InvScales inv;
     const bool codes = pool.dtype == WF_DTYPE_FP8_E4M3;
