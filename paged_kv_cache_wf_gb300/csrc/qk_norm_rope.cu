@@ -12,15 +12,14 @@
 // HBM-bound: every byte of q, k, v is read once and every result written once; doing
 // it in one pass saves the second read and write of q and k that separate norm,
 // rotation and scatter passes make.  What has to be watched is the instruction count:
-// a form of 166 instructions a warp and row pair took 51 us for 8193 tokens of
-// Llama-3-8B heads into fp8 pools, whose bytes take 28.  So a head row is D / VEC lanes
-// of one 16-byte chunk each and a warp's rows are of one kind (each kind's rows are
-// padded to whole warps), which keeps the choice of q, k or v a branch of the warp;
-// arithmetic is on pairs (two fp32 operations an instruction); and an instance without
-// weights has no norm in it.  The sum of squares is a shuffle reduction over the row's
-// lanes, and a rotated pair's other half comes from the lane that holds it (one shuffle
-// a 32-bit word, of the raw chunk: both halves share the row's norm factor).  A lane
-// reads its cos and sin once for IT rows.
+// with one 16-byte chunk a lane, pairs exchanged by shuffle, 8193 tokens of Llama-3-8B
+// heads into fp8 pools, whose bytes take 28 us, took 41 us (51 us before the rows of a
+// warp were of one kind).  So a lane has two chunks of a head row, both halves of its
+// pairs, and no element passes from lane to lane; a warp's rows are of one kind (each
+// kind's rows are padded to whole warps), which keeps the choice of q, k or v a branch
+// of the warp; arithmetic is on pairs (two fp32 operations an instruction); an instance
+// without weights has no norm in it.  The sum of squares is a shuffle reduction over the
+// row's lanes.  A lane reads its cos and sin once for IT rows.
 #include "wf_internal.h"
 
 namespace wf {
@@ -86,37 +85,50 @@ __device__ __forceinline__ uint32_t codes4(const float2& a, const float2& b, con
     return (lo & 0xffffu) | (hi << 16);
 }
 
-// A 16-byte chunk of weights.
-template <typename E>
-__device__ __forceinline__ void weight_pairs(const void* w, int chunk, float2* f) {
-    to_pairs<E>(__ldg(static_cast<const uint4*>(w) + chunk), f);
+// A chunk's codes.
+template <int NP>
+__device__ __forceinline__ void store_codes(char* out, const float2* y, float inv) {
+    const float2 f = make_float2(inv, inv);
+    static_assert(NP == 4 || NP == 2, "a chunk is 8 or 4 elements");
+    if constexpr (NP == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(codes4(y[0], y[1], f), codes4(y[2], y[3], f));
+    else
+        *reinterpret_cast<uint32_t*>(out) = codes4(y[0], y[1], f);
 }
+
+constexpr int kThreads = 128;
 
 // Rows of one kind, in whole warps.
 template <typename E, int D>
 __host__ __device__ constexpr int padded_rows(int n) {
-    constexpr int RPW = 32 * E::kPerChunk / D > 0 ? 32 * E::kPerChunk / D : 1;
+    constexpr int RPW = 32 * 2 * E::kPerChunk / D;
     return (n + RPW - 1) / RPW * RPW;
 }
 
-// WIDE: rotary_dim is a multiple of 16, so a chunk's other halves lie in one chunk, at
-// the same places, and the table is read in 16-byte pieces.  Otherwise each element
-// fetches its pair's other half, its cos and its sin by itself.
+// WIDE: rotary_dim is a multiple of 16, so the other halves of a chunk's elements are one
+// chunk, at the same places, and the table is read in 16-byte pieces.  Otherwise each
+// element fetches its pair's other half, its cos and its sin by itself.
 // CTA (t, y): token t, row places y RPB IT .. ; a place is q's rows, then k's, then v's.
 template <typename E, bool CODES, int D, int IT, bool WIDE, bool NORM>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p, const InvScales inv) {
-    constexpr int VEC = E::kPerChunk, NP = VEC / 2, LG = D / VEC, RPB = 256 / LG;
-    const int lg = threadIdx.x % LG, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeParams p, const InvScales inv) {
+    constexpr int VEC = E::kPerChunk, NP = VEC / 2, LG = D / VEC / 2, RPB = kThreads / LG;
+    const int l = threadIdx.x % LG;
     const int place0 = blockIdx.y * (RPB * IT) + threadIdx.x / LG;
-    const int e0 = lg * VEC;
     const int H_q = p.a.num_q_heads;
     const int q_end = padded_rows<E, D>(H_q), k_end = q_end + padded_rows<E, D>(p.H_kv);
     const int rot = p.a.rotary_dim, half = rot >> 1;
-    const bool turned = e0 < rot, inter = p.a.interleaved != 0, low = e0 < half;
+    const bool inter = p.a.interleaved != 0;
+    // the lane's chunks start at elements ea and eb: the halves of its pairs, or (interleaved,
+    // not WIDE, past rotary_dim) neighbours
+    const int hc = half / VEC;
+    const bool halves = WIDE && !inter && l < hc;
+    const int ea = (halves ? l : 2 * l) * VEC;
+    const int eb = halves ? ea + half : ea + VEC;
+    const bool turned = halves || (inter && ea < rot) || (!WIDE && ea < rot);
     const int64_t t = blockIdx.x;
     const int64_t slot = __ldg(p.a.slot_mapping + t);
     const int pos = rot > 0 ? __ldg(p.a.positions + t) : 0;
-    uint4 x[IT];
+    uint4 xa[IT], xb[IT];
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int place = place0 + i * RPB;
@@ -124,8 +136,12 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p, c
         const int h = place - (kind == 0 ? 0 : kind == 1 ? q_end : k_end);
         const char* base = static_cast<const char*>(kind == 0 ? p.a.q : kind == 1 ? p.a.k : p.a.v);
         const int64_t stride = kind == 0 ? p.a.q_stride : kind == 1 ? p.a.k_stride : p.a.v_stride;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < (kind == 0 ? H_q : p.H_kv)) x[i] = ld_global_stream(base + (t * stride + h * D + e0) * E::kBytes);
+        xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < (kind == 0 ? H_q : p.H_kv)) {
+            const char* row = base + (t * stride + h * D) * E::kBytes;
+            xa[i] = ld_global_stream(row + ea * E::kBytes);
+            xb[i] = ld_global_stream(row + eb * E::kBytes);
+        }
     }
     if (slot < 0) return;   // padding token
     if (slot >= p.num_slots || (unsigned)pos >= (unsigned)(rot > 0 ? p.a.max_position : 1)) {
@@ -133,71 +149,40 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p, c
             report(p.dev_status, slot >= p.num_slots ? WF_DEV_BAD_SLOT : WF_DEV_BAD_POSITION);
         return;
     }
-    // cos and (signed) sin of this lane's elements, and the lane that holds their other halves
+    // halves: cos and sin of the NP * 2 pairs.  Interleaved: of the VEC pairs of both chunks, NP
+    // of each: c[0 .. NP / 2) two pairs' cos of chunk a each, the rest of chunk b
     const float* table = p.a.cos_sin + (int64_t)pos * rot;
     float2 c[NP], s[NP];
-    int mate = lane;
-    if (turned) {
-        if constexpr (WIDE) {
-            if (inter) {
+    if (WIDE && turned) {
+        const float* tc = table + (inter ? ea / 2 : ea);
 #pragma unroll
-                for (int e = 0; e < NP; e += 2) {
-                    const float2 cc = __ldg(reinterpret_cast<const float2*>(table + e0 / 2 + e));
-                    const float2 ss = __ldg(reinterpret_cast<const float2*>(table + half + e0 / 2 + e));
-                    c[e] = make_float2(cc.x, cc.x);
-                    c[e + 1] = make_float2(cc.y, cc.y);
-                    s[e] = make_float2(-ss.x, ss.x);
-                    s[e + 1] = make_float2(-ss.y, ss.y);
-                }
-            } else {
-                const float* tc = table + (low ? e0 : e0 - half);
-                const float sign = low ? -1.f : 1.f;
-                mate = low ? lane + half / VEC : lane - half / VEC;
-#pragma unroll
-                for (int e = 0; e < NP; e += 2) {
-                    const float4 cc = __ldg(reinterpret_cast<const float4*>(tc + 2 * e));
-                    const float4 ss = __ldg(reinterpret_cast<const float4*>(tc + half + 2 * e));
-                    c[e] = make_float2(cc.x, cc.y);
-                    c[e + 1] = make_float2(cc.z, cc.w);
-                    s[e] = __fmul2_rn(make_float2(ss.x, ss.y), make_float2(sign, sign));
-                    s[e + 1] = __fmul2_rn(make_float2(ss.z, ss.w), make_float2(sign, sign));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int g = e0 + e;
-                const bool first = inter ? (g & 1) == 0 : g < half;
-                const int i = inter ? g >> 1 : first ? g : g - half;
-                const float cs = g < rot ? __ldg(table + i) : 1.f;
-                float sn = g < rot ? __ldg(table + half + i) : 0.f;
-                if (first) sn = -sn;
-                if (e & 1) {
-                    c[e / 2].y = cs;
-                    s[e / 2].y = sn;
-                } else {
-                    c[e / 2].x = cs;
-                    s[e / 2].x = sn;
-                }
-            }
+        for (int e = 0; e < NP; e += 2) {
+            const float4 cc = __ldg(reinterpret_cast<const float4*>(tc + 2 * e));
+            const float4 ss = __ldg(reinterpret_cast<const float4*>(tc + half + 2 * e));
+            c[e] = make_float2(cc.x, cc.y);
+            c[e + 1] = make_float2(cc.z, cc.w);
+            s[e] = make_float2(ss.x, ss.y);
+            s[e + 1] = make_float2(ss.z, ss.w);
         }
     }
-    const int64_t slot_row = slot * p.H_kv * D + e0, token_row = t * H_q * D + e0;
+    const int64_t slot_row = slot * p.H_kv * D, token_row = t * H_q * D;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int place = place0 + i * RPB;
+        float2 a[NP], b[NP];
         if (place >= k_end) {                       // V: as it is
             const int h = place - k_end;
             if (h >= p.H_kv) continue;
             char* out = static_cast<char*>(p.a.v_pool) + (slot_row + h * D) * (CODES ? 1 : E::kBytes);
             if constexpr (CODES) {
                 const float f = inv.v[min(h, kMaxScaleHeads - 1)];
-                float2 y[NP];
-                to_pairs<E>(x[i], y);
-                *reinterpret_cast<uint2*>(out) = make_uint2(codes4(y[0], y[1], make_float2(f, f)),
-                                                            codes4(y[NP - 2], y[NP - 1], make_float2(f, f)));
+                to_pairs<E>(xa[i], a);
+                to_pairs<E>(xb[i], b);
+                store_codes<NP>(out + ea, a, f);
+                store_codes<NP>(out + eb, b, f);
             } else {
-                st_global_v4(out, x[i]);
+                st_global_v4(out + ea * E::kBytes, xa[i]);
+                st_global_v4(out + eb * E::kBytes, xb[i]);
             }
             continue;
         }
@@ -205,92 +190,99 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p, c
         const int h = is_q ? place : place - q_end;
         const bool live = h < (is_q ? H_q : p.H_kv);
         const void* w = is_q ? p.a.q_weight : p.a.k_weight;
-        float2 y[NP], z[NP];
-        to_pairs<E>(x[i], y);
-        if (WIDE && rot > 0 && !inter) {
-            uint4 m;
-            m.x = __shfl_sync(0xffffffffu, x[i].x, mate);
-            m.y = __shfl_sync(0xffffffffu, x[i].y, mate);
-            m.z = __shfl_sync(0xffffffffu, x[i].z, mate);
-            m.w = __shfl_sync(0xffffffffu, x[i].w, mate);
-            to_pairs<E>(m, z);
-        }
+        to_pairs<E>(xa[i], a);
+        to_pairs<E>(xb[i], b);
         float rs = 1.f;
         if (NORM && w != nullptr) {
-            float2 sq = __fmul2_rn(y[0], y[0]);
+            float2 sq = __fmul2_rn(a[0], a[0]);
 #pragma unroll
-            for (int e = 1; e < NP; ++e) sq = __ffma2_rn(y[e], y[e], sq);
+            for (int e = 1; e < NP; ++e) sq = __ffma2_rn(a[e], a[e], sq);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) sq = __ffma2_rn(b[e], b[e], sq);
             float ss = sq.x + sq.y;
 #pragma unroll
             for (int o = LG / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             rs = rsqrtf(ss * (1.f / D) + p.a.eps);
             const float2 r2 = make_float2(rs, rs);
             float2 f[NP];
-            weight_pairs<E>(w, lg, f);
+            to_pairs<E>(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(w) + ea * E::kBytes)), f);
 #pragma unroll
-            for (int e = 0; e < NP; ++e) y[e] = __fmul2_rn(__fmul2_rn(y[e], r2), f[e]);
-            if (WIDE && !inter && turned) {
-                weight_pairs<E>(w, lg + mate - lane, f);
+            for (int e = 0; e < NP; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], r2), f[e]);
+            to_pairs<E>(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(w) + eb * E::kBytes)), f);
 #pragma unroll
-                for (int e = 0; e < NP; ++e) z[e] = __fmul2_rn(__fmul2_rn(z[e], r2), f[e]);
-            }
+            for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(__fmul2_rn(b[e], r2), f[e]);
         }
         if (!live) continue;
-        if (turned) {
-            if (inter) {   // pairs lie side by side in the chunk, normed already
+        if (WIDE && turned) {
+            if (!inter) {          // (a, b) -> (a cos - b sin, b cos + a sin)
 #pragma unroll
-                for (int e = 0; e < NP; ++e) z[e] = make_float2(y[e].y, y[e].x);
-            } else if constexpr (!WIDE) {
-                const char* row = static_cast<const char*>(is_q ? p.a.q : p.a.k) +
-                                  (t * (is_q ? p.a.q_stride : p.a.k_stride) + h * D) * E::kBytes;
+                for (int e = 0; e < NP; ++e) {
+                    const float2 y = __fmul2_rn(a[e], c[e]), z = __fmul2_rn(b[e], c[e]);
+                    const float2 n = make_float2(-s[e].x, -s[e].y), a0 = a[e];
+                    a[e] = __ffma2_rn(b[e], n, y);
+                    b[e] = __ffma2_rn(a0, s[e], z);
+                }
+            } else {               // the same within each pair of neighbours
+                auto turn = [](float2& x, float cs, float sn) {
+                    x = __ffma2_rn(make_float2(x.y, x.x), make_float2(-sn, sn), __fmul2_rn(x, make_float2(cs, cs)));
+                };
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const int g = e0 + e;
-                    const int o = g < half ? g + half : g - half;
-                    float b = 0.f;
-                    if (g < rot) {
-                        b = widen_one<E>(row, o);
-                        if (NORM && w != nullptr) b = b * rs * widen_one<E>(w, o);
-                    }
-                    if (e & 1) z[e / 2].y = b;
-                    else z[e / 2].x = b;
+                for (int e = 0; e < NP; ++e) {
+                    const float2 ca = c[e / 2], sa = s[e / 2], cb = c[(NP + e) / 2], sb = s[(NP + e) / 2];
+                    turn(a[e], (e & 1) ? ca.y : ca.x, (e & 1) ? sa.y : sa.x);
+                    turn(b[e], (e & 1) ? cb.y : cb.x, (e & 1) ? sb.y : sb.x);
                 }
             }
+        } else if (!WIDE && turned) {
+            const char* row = static_cast<const char*>(is_q ? p.a.q : p.a.k) +
+                              (t * (is_q ? p.a.q_stride : p.a.k_stride) + h * D) * E::kBytes;
+            auto one = [&](float x, int g) -> float {      // element g, normed, turned with its pair's other half
+                if (g >= rot) return x;
+                const bool first = inter ? (g & 1) == 0 : g < half;
+                const int pair = inter ? g >> 1 : first ? g : g - half;
+                const int o = inter ? g ^ 1 : first ? g + half : g - half;
+                float y = widen_one<E>(row, o);
+                if (NORM && w != nullptr) y = y * rs * widen_one<E>(w, o);
+                const float sn = __ldg(table + half + pair);
+                return fmaf(y, first ? -sn : sn, x * __ldg(table + pair));
+            };
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
-                const float2 r2 = __ffma2_rn(z[e], s[e], __fmul2_rn(y[e], c[e]));
-                if (WIDE || e0 + 2 * e + 1 < rot) y[e] = r2;   // rotary_dim is even: a pair is in or out
+                a[e] = make_float2(one(a[e].x, ea + 2 * e), one(a[e].y, ea + 2 * e + 1));
+                b[e] = make_float2(one(b[e].x, eb + 2 * e), one(b[e].y, eb + 2 * e + 1));
             }
         }
-        if (is_q) {
-            st_global_v4(static_cast<char*>(p.a.q_out) + (token_row + h * D) * E::kBytes, from_pairs<E>(y));
-        } else if constexpr (CODES) {
+        if (CODES && !is_q) {
             const float f = inv.k[min(h, kMaxScaleHeads - 1)];
-            *reinterpret_cast<uint2*>(static_cast<char*>(p.a.k_pool) + slot_row + h * D) =
-                make_uint2(codes4(y[0], y[1], make_float2(f, f)), codes4(y[NP - 2], y[NP - 1], make_float2(f, f)));
+            char* out = static_cast<char*>(p.a.k_pool) + slot_row + h * D;
+            store_codes<NP>(out + ea, a, f);
+            store_codes<NP>(out + eb, b, f);
         } else {
-            st_global_v4(static_cast<char*>(p.a.k_pool) + (slot_row + h * D) * E::kBytes, from_pairs<E>(y));
+            char* out = is_q ? static_cast<char*>(p.a.q_out) + (token_row + h * D) * E::kBytes
+                             : static_cast<char*>(p.a.k_pool) + (slot_row + h * D) * E::kBytes;
+            st_global_v4(out + ea * E::kBytes, from_pairs<E>(a));
+            st_global_v4(out + eb * E::kBytes, from_pairs<E>(b));
         }
     }
 }
 
 template <typename E, bool CODES, int D, int IT>
 cudaError_t launch_rows(const RopeParams& p, const InvScales& inv, int places, cudaStream_t stream) {
-    constexpr int RPB = 256 / (D / E::kPerChunk);
+    constexpr int RPB = kThreads / (D / E::kPerChunk / 2);
     const dim3 grid((unsigned)p.a.num_tokens, (unsigned)((places + RPB * IT - 1) / (RPB * IT)));
     const bool norm = p.a.q_weight != nullptr || p.a.k_weight != nullptr;
     if (p.a.rotary_dim % 16 != 0)
-        qk_norm_rope_kernel<E, CODES, D, IT, false, true><<<grid, 256, 0, stream>>>(p, inv);
+        qk_norm_rope_kernel<E, CODES, D, IT, false, true><<<grid, kThreads, 0, stream>>>(p, inv);
     else if (norm)
-        qk_norm_rope_kernel<E, CODES, D, IT, true, true><<<grid, 256, 0, stream>>>(p, inv);
+        qk_norm_rope_kernel<E, CODES, D, IT, true, true><<<grid, kThreads, 0, stream>>>(p, inv);
     else
-        qk_norm_rope_kernel<E, CODES, D, IT, true, false><<<grid, 256, 0, stream>>>(p, inv);
+        qk_norm_rope_kernel<E, CODES, D, IT, true, false><<<grid, kThreads, 0, stream>>>(p, inv);
     return cudaGetLastError();
 }
 
 template <typename E, bool CODES, int D>
 cudaError_t launch_width(const RopeParams& p, const InvScales& inv, cudaStream_t stream) {
-    constexpr int RPB = 256 / (D / E::kPerChunk);
+    constexpr int RPB = kThreads / (D / E::kPerChunk / 2);
     const int places = padded_rows<E, D>(p.a.num_q_heads) + 2 * padded_rows<E, D>(p.H_kv);
     const int64_t one = (int64_t)p.a.num_tokens * ((places + RPB - 1) / RPB);
     if (one <= 4 * (int64_t)num_sms()) return launch_rows<E, CODES, D, 1>(p, inv, places, stream);
