@@ -30,11 +30,14 @@
 // that its largest magnitude lies in [128, 256), into hi = e4m3(q) and lo = e4m3(q - hi).
 // hi keeps four of a bf16 value's eight significant bits and lo the rest, so their sum is
 // the row up to 2^-10 (a 2^-17 part of its largest value).  The row's power of two and
-// the K scale go into the exponent's factor.  V codes are widened to bf16, which is
-// exact, by the finishing warps, into the ring that P V reads; the V scale multiplies
-// the outputs.  Widening K too would cost twice the finishing warps' work, and splitting
-// the weights into two e4m3 parts would cost the softmax warps more conversions than
-// they have time for.
+// the K scale go into the exponent's factor.  V codes are widened to fp16, which is exact
+// and which the hardware converts two at a time, by the finishing warps, into the ring
+// that P V reads, and the weights (at most 2^8, see kLazyMax) are rounded to fp16, whose
+// step is an eighth of bf16's; the V scale multiplies the outputs.  To bf16 there is no
+// conversion, and shifting and scaling the codes there took the call from 94 us (V not
+// widened) to 135 us, batch of 64.  Widening K too would cost twice the finishing warps'
+// work, and splitting the weights into two e4m3 parts would cost the softmax warps more
+// conversions than they have time for.
 #include <cuda.h>
 
 #include <type_traits>
@@ -196,22 +199,9 @@ __device__ __forceinline__ void st_16words(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 
-// 16 e4m3 codes -> 16 bf16 values (two 16-byte chunks), exactly: a code's exponent and
-// mantissa bits stand in a bf16 as a value 2^-120 times its own.  The NaN codes come out
-// as +-480.
-__device__ __forceinline__ void widen16(const uint4& c, uint4& lo, uint4& hi) {
-    const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-    uint32_t o[8];
-    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));   // 2^120
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t t = __byte_perm(in[i >> 1], 0u, (i & 1) ? 0x3424 : 0x1404);   // codes in the upper bytes
-        uint32_t u = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
-        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), up);
-        o[i] = *reinterpret_cast<const uint32_t*>(&y);
-    }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Not 0 when one of 16 codes is NaN (S.1111.111).
@@ -530,25 +520,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int k = 0; k < kBatch; ++k) {
                             const int y = y0 + k * kFin;
                             if (y >= kRounds) break;
-                            uint4 lo, hi;
-                            widen16(c[k], lo, hi);
-                            nan |= nan_codes(c[k]);
-                            *reinterpret_cast<uint4*>(out_at(y, o0)) = lo;
-                            *reinterpret_cast<uint4*>(out_at(y, o1)) = hi;
+                            uint32_t v[8];
+                            e4m3x16_to_f16(c[k], v);
+                            if (kStep * y + rr >= r0) nan |= nan_codes(c[k]);
+                            *reinterpret_cast<uint4*>(out_at(y, o0)) = make_uint4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<uint4*>(out_at(y, o1)) = make_uint4(v[4], v[5], v[6], v[7]);
                         }
                     }
                     if (__any_sync(0xffffffffu, nan != 0)) {
-                        // NaN codes stand as +-480: NaN, or 0 in a draft's row, which is set aside
+                        // a draft's NaN elements are set aside
 #pragma unroll 1
                         for (int y = fw; y < kRounds; y += kFin) {
-                            if (!live(y)) continue;
-                            const bool draft = kStep * y + rr >= r0;
+                            if (!live(y) || kStep * y + rr < r0) continue;
 #pragma unroll 1
                             for (int e = 0; e < 16; ++e) {
                                 if ((src[y * kStep * D + e] & 0x7f) != 0x7f) continue;
-                                *reinterpret_cast<unsigned short*>(out_at(y, e < 8 ? o0 : o1) + (e & 7) * 2) =
-                                    draft ? 0 : 0x7fff;
-                                wild |= draft;
+                                *reinterpret_cast<unsigned short*>(out_at(y, e < 8 ? o0 : o1) + (e & 7) * 2) = 0;
+                                wild = true;
                             }
                         }
                     }
@@ -601,7 +589,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // products in issue order.  One issuer for both streams was the bound at 16 products a
         // tile and stream.
         constexpr uint32_t idS = CODES ? tc::idesc_e4m3_f32(TM, TN, 0, 0) : tc::idesc_bf16_f32(TM, TN, 0, 0);
-        constexpr uint32_t idO = tc::idesc_bf16_f32(TM, D, 0, 1);
+        constexpr uint32_t idO = CODES ? tc::idesc_f16_f32(TM, D, 0, 1) : tc::idesc_bf16_f32(TM, D, 0, 1);
         const int t = warp - kMmaW;
         const int tq = QT == 1 ? 0 : t;
         // K-major rows of 128 bytes, or (codes, D = 64) of 64
@@ -843,7 +831,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const float2 x = __ffma2_rn(make_float2(s[w][2 * v], s[w][2 * v + 1]), sc2, nm2);
                             const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
                             ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
-                            pw[v] = pack_bf16x2(e2.x, e2.y);
+                            pw[v] = CODES ? pack_f16x2(e2.x, e2.y) : pack_bf16x2(e2.x, e2.y);
                         }
                         st_16words(sbase + (w >> 1) * 64 + (w & 1) * 16, pw);
                     }
