@@ -212,6 +212,20 @@ __device__ __forceinline__ uint32_t nan_codes(const uint4& c) {
 
 struct NoScales {};
 
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// x, the same in all lanes, as a value that the compiler knows to be.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
 template <int D, int QT, bool CODES>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -616,7 +630,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // tile and stream.
         constexpr uint32_t idS = CODES ? tc::idesc_e4m3_f32(TM, TN, 0, 0) : tc::idesc_bf16_f32(TM, TN, 0, 0);
         constexpr uint32_t idO = CODES ? tc::idesc_f16_f32(TM, D, 0, 1) : tc::idesc_bf16_f32(TM, D, 0, 1);
-        const int t = warp - kMmaW;
+        // An MMA takes its operands from uniform registers.  The slots and parities here are the
+        // same in all lanes, and are kept so that the compiler sees it: otherwise each of a
+        // product's operands is moved over, MMA by MMA, and issuing took longer than computing.
+        const int t = uniform(warp) - kMmaW;
         const int tq = QT == 1 ? 0 : t;
         // K-major rows of 128 bytes, or (codes, D = 64) of 64
         auto kmajor = [](uint32_t at, uint32_t atom) {
@@ -625,18 +642,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint64_t qdesc = kmajor(smem_u32(smem + L::q + tq * L::QTILE), 1024);
         const uint64_t kdesc = kmajor(smem_u32(smem + L::k), L::ATOM);
         const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::v), L::HALF_OFF, L::ATOM);
-        const uint32_t dS = tmem + t * L::SCOL, dO = tmem + L::OCOL + t * D;
+        const uint32_t tm = (uint32_t)uniform((int)tmem);
+        const uint32_t dS = tm + t * L::SCOL, dO = tm + L::OCOL + t * D;
         int kx = 0, vx = 0;                 // slots of the next tile
         uint32_t kpar = 0, vpar = 0;        // and their parities
         uint32_t qpar = 0, ppar = 0;
         bool ok = true;
         auto need = [&](uint64_t* bar, uint32_t par) {
-            if (ok && !bar_wait(bar, par)) {
+            // no lane may still be polling when one hands the barrier's slot on
+            if (ok && !__all_sync(0xffffffffu, bar_wait(bar, par))) {
                 if (lane == 0) fail();
                 ok = false;
             }
-            // no lane may still be polling when lane 0 hands the barrier's slot on
-            __syncwarp();
             return ok;
         };
         auto step = [&](int& x, uint32_t& par, int n) {
@@ -656,9 +673,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             step(kx, kpar, L::KS);
             step(vx, vpar, L::VS);
         }
-        for (int i = 0; ok && piece(i); ++i) {
+        for (int i = 0; ok && __all_sync(0xffffffffu, piece(i)); ++i) {
             const PieceRec& it = ring[i % kRing];
-            const int nt = steps(it, t), all = it.j1 - it.j0;
+            const int nt = uniform(steps(it, t)), all = uniform(it.j1 - it.j0);
             if (QT == 2 && nt == 0) {       // no rows: hand the tiles on as they land
                 for (int u = 0; u < all && ok; ++u) {
                     if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
@@ -679,7 +696,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ppar ^= 1;
                     tc::fence_after_sync();
                     const uint32_t vd = (uint32_t)vdesc + ((vx * L::VTILE) >> 4);
-                    if (lane == 0) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < TN / 16; ++kk)
                             mma<1>(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), 0u, vd + ((kk * 2 * L::ATOM) >> 4),
@@ -694,7 +711,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (u + 1 < nt) {
                     if (!need(&k_full[kx], kpar)) break;
                     tc::fence_after_sync();
-                    if (lane == 0) {
+                    if (elect_one()) {
                         const uint32_t kd = (uint32_t)kdesc + ((kx * L::KTILE) >> 4), qd = (uint32_t)qdesc;
                         const uint32_t khi = (uint32_t)(kdesc >> 32), qhi = (uint32_t)(qdesc >> 32);
                         if constexpr (CODES) {       // the two parts of q, one after the other
