@@ -363,11 +363,90 @@ __global__ void __launch_bounds__(256) paged_tree_join_kernel(const TreeParams p
     store_out<A, VPL>(static_cast<char*>(p.out) + (row * D + lane * VPL) * A::kBytes, o);
 }
 
+// The same for row blocks of many rows, in one wave: a warp takes every 8 gridDim.y-th row,
+// kManyRows at once and two pieces of each at a time (nearly all units of a large batch
+// have two).  Of the kernel above, 4864 CTAs (152 units of 256 rows) are four waves of three
+// dependent loads each: 281 us for the whole call against 275 with this one.  Its code is longer
+// and, cold at every call, costs more than it saves on smaller blocks: 152 units of 128 rows
+// take 35.4 us with it and 34.7 without.
+constexpr int kManyRows = 2, kManyCtasPerSm = 4;
+
+template <typename A, int D>
+__global__ void __launch_bounds__(256, kManyCtasPerSm) paged_tree_join_many_kernel(const TreeParams p) {
+    constexpr int VPL = D / 32;
+    using Vec = typename std::conditional<VPL == 4, float4, float2>::type;
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 rec = __ldcg(p.ws_rec + blockIdx.x);
+    if (rec.w == 0) return;
+    const int q_begin = __ldg(p.cu_q_lens + rec.x), n = __ldg(p.cu_q_lens + rec.x + 1) - q_begin;
+    const int qb = rec.y / p.H_kv, h = rec.y - qb * p.H_kv;
+    const int i0 = qb * p.tokb;
+    const int rows = min(p.tokb, n - i0) * p.G;
+    const int first = blockIdx.x, cnt = rec.z - first + 1, step = 8 * gridDim.y;
+#pragma unroll 1
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += kManyRows * step) {
+        float M[kManyRows], den[kManyRows] = {}, o[kManyRows][VPL] = {};
+#pragma unroll
+        for (int k = 0; k < kManyRows; ++k) M[k] = -INFINITY;
+#pragma unroll 1
+        for (int u0 = 0; u0 < cnt; u0 += 2) {
+            Vec x[kManyRows][2];
+            float2 ml[kManyRows][2];
+#pragma unroll
+            for (int k = 0; k < kManyRows; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    // a row or piece past the last reads the last one
+                    const int i = min(u0 + u, cnt - 1);
+                    const int64_t at = (int64_t)tree_piece_slot(first + i, i) * p.rows + min(r + k * step, rows - 1);
+                    ml[k][u] = __ldcg(p.ws_ml + at);
+                    x[k][u] = __ldcg(reinterpret_cast<const Vec*>(p.ws_o + at * D) + lane);
+                }
+#pragma unroll
+            for (int k = 0; k < kManyRows; ++k) {
+                if (u0 + 1 == cnt) ml[k][1] = make_float2(-INFINITY, 0.f);
+                const float mn = fmaxf(M[k], fmaxf(ml[k][0].x, ml[k][1].x));
+                // as above: without a maximum a sum is 0, or NaN, which has to stay
+                const float a = M[k] == -INFINITY ? 1.f : exp2f(M[k] - mn);
+                den[k] *= a;
+#pragma unroll
+                for (int e = 0; e < VPL; ++e) o[k][e] *= a;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (ml[k][u].y == 0.f) continue;
+                    const float w = ml[k][u].x == -INFINITY ? 1.f : exp2f(ml[k][u].x - mn);
+                    den[k] += w * ml[k][u].y;
+                    o[k][0] += w * x[k][u].x;
+                    o[k][1] += w * x[k][u].y;
+                    if constexpr (VPL == 4) {
+                        o[k][2] += w * x[k][u].z;
+                        o[k][3] += w * x[k][u].w;
+                    }
+                }
+                M[k] = mn;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kManyRows; ++k) {
+            const int rk = r + k * step;
+            if (rk >= rows) break;
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) o[k][e] = den[k] == 0.f ? 0.f : o[k][e] / den[k];
+            const int64_t row = (int64_t)(q_begin + i0 + rk / p.G) * p.H_q + h * p.G + rk % p.G;
+            store_out<A, VPL>(static_cast<char*>(p.out) + (row * D + lane * VPL) * A::kBytes, o[k]);
+        }
+    }
+}
+
 template <typename A, int D>
 cudaError_t launch_join(const TreeParams& p, int ctas, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
     // rows a row block can have: all of them, or those of max_q_len drafts
-    cfg.gridDim = dim3(ctas, ((p.max_q_len < p.tokb ? p.max_q_len : p.tokb) * p.G + 7) / 8);
+    const int y = ((p.max_q_len < p.tokb ? p.max_q_len : p.tokb) * p.G + 7) / 8;
+    const int64_t all = (int64_t)p.B * p.H_kv * ((p.max_q_len + p.tokb - 1) / p.tokb);   // units at most
+    const bool many = y * (all < ctas ? all : ctas) > 16 * (int64_t)num_sms();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, many ? kManyCtasPerSm * num_sms() / ctas : y);   // `ctas` is at most two an SM
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -375,7 +454,8 @@ cudaError_t launch_join(const TreeParams& p, int ctas, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_tree_join_kernel<A, D>, p);
+    return many ? cudaLaunchKernelEx(&cfg, paged_tree_join_many_kernel<A, D>, p)
+                : cudaLaunchKernelEx(&cfg, paged_tree_join_kernel<A, D>, p);
 }
 
 template <typename E, typename A, int D>

@@ -245,7 +245,7 @@ def test_the_same_bytes_again_and_from_a_graph(name):
 
 
 @pytest.mark.parametrize("pool,D", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64), ("f32", 64)])
-@pytest.mark.parametrize("drafts", [5, 40])
+@pytest.mark.parametrize("drafts", [5, 40, 64])
 def test_pieces_of_every_length_back_to_back(pool, D, drafts):
     """Contexts of 1 to 17 tiles of 128 positions in an order that gives every CTA odd and even pieces, many calls
     without a pause: each has to give the bytes of the first, and no wait may give up."""
