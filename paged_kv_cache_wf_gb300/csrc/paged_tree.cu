@@ -18,83 +18,133 @@ namespace {
 // ---------------------------------------------------------------------------
 // CUDA cores
 // ---------------------------------------------------------------------------
-// A CTA takes 32 rows against 64 positions at a time: K and V rows are widened to fp32
-// in shared memory (each element once), S = Q K^T is a 2 x 4 register tile a thread,
-// O += P V a 2 x (D / 16) one, both fed by 16-byte shared-memory reads.  The FMA pipe is
-// the bound: 2 * 32 * D FMAs a position and head against 2 * D elements read.
-constexpr int kCcRows = 32;
+// A CTA takes 8 RPW rows against 64 positions at a time, a warp RPW of the rows, so that S,
+// the softmax and P V of a row never leave its warp: lane l has positions l and l + 32 of S and
+// columns l D / 32 .. of O.  K and V rows of the next tile are on their way in registers
+// meanwhile; they are widened to fp32 into shared memory once for all warps.
 constexpr int kCcTile = 64;
-constexpr int kCcThreads = 256;
+constexpr int kCcWarps = 8;
+constexpr int kCcThreads = 32 * kCcWarps;
 
-template <int D>
+template <int D, int RPW>
 struct CcLayout {
-    static constexpr int KS = D + 4;            // row stride of K in floats: 16 rows meet in two conflict-free reads
-    static constexpr int SS = kCcTile + 4;      // row stride of S
+    static constexpr int rows = kCcWarps * RPW;
+    static constexpr int KS = D + 4;            // row stride of K in floats: eight rows meet in one conflict-free read
     static constexpr int q = 0;
-    static constexpr int k = q + kCcRows * D * 4;
+    static constexpr int k = q + rows * D * 4;
     static constexpr int v = k + kCcTile * KS * 4;
-    static constexpr int s = v + kCcTile * D * 4;
-    static constexpr int vis = s + kCcRows * SS * 4;          // [rows][2] words: positions of the tile a row sees
-    static constexpr int slot = vis + kCcRows * 8;            // [tile] int64 slot, -1: not there
-    static constexpr int alpha = slot + kCcTile * 8;          // [rows]
-    static constexpr int start = alpha + kCcRows * 4;
+    static constexpr int p = v + kCcTile * D * 4;
+    static constexpr int slot = p + rows * kCcTile * 4;       // 3 x [tile] int64 slot, -1: not there
+    static constexpr int start = slot + 3 * kCcTile * 8;
     static constexpr int scratch = start + (int)sizeof(TreeStart);
-    static constexpr int total = scratch + 8 * (kCcThreads / 32);
+    static constexpr int total = scratch + 8 * kCcWarps;
     static_assert(slot % 8 == 0 && start % 16 == 0 && scratch % 8 == 0, "misaligned shared memory");
 };
 
-template <typename E, int D>
-__device__ __forceinline__ void cc_load_row(float* dst, const char* pool, int64_t elem, int chunk) {
-    const uint4 c = ld_global_stream(pool + elem * E::kBytes + chunk * 16);
+// 16 bytes of a pool row in fp32.
+template <typename E>
+__device__ __forceinline__ void cc_widen(const uint4& c, float (&f)[16 / E::kBytes]) {
     if constexpr (E::kBytes == 1) {
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 a = e4m3x2_to_float2(w[i]), b = e4m3x2_to_float2(w[i] >> 16);
-            *reinterpret_cast<float4*>(dst + chunk * 16 + i * 4) = make_float4(a.x, a.y, b.x, b.y);
+            f[4 * i] = a.x;
+            f[4 * i + 1] = a.y;
+            f[4 * i + 2] = b.x;
+            f[4 * i + 3] = b.y;
         }
     } else {
-        float f[E::kPerChunk];
         widen_chunk<E>(c, f);
-#pragma unroll
-        for (int i = 0; i < E::kPerChunk; i += 4)
-            *reinterpret_cast<float4*>(dst + chunk * E::kPerChunk + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
     }
 }
 
+template <int VPL>
+__device__ __forceinline__ void cc_row(float (&f)[VPL], const float* from) {
+    if constexpr (VPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(from);
+        f[0] = x.x;
+        f[1] = x.y;
+        f[2] = x.z;
+        f[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2*>(from);
+        f[0] = x.x;
+        f[1] = x.y;
+    }
+}
+
+// CTAs an SM: as many as the registers that the next tile and the rows take leave room for.
+constexpr int cc_ctas_per_sm(int bytes, int D, int rpw) { return bytes == 4 && D == 128 && rpw == 4 ? 1 : 2; }
+
+// Rows of a warp: the fewest that hold all rows of a request's drafts under a KV head.
+constexpr int cc_rows_per_warp(int64_t rows) { return rows <= kCcWarps ? 1 : 4; }
+
 // E: pool elements, A: q and out elements.
-template <typename E, typename A, int D>
-__global__ void __launch_bounds__(kCcThreads, 2) paged_tree_kernel(const TreeParams p, const HeadScales sc) {
-    using L = CcLayout<D>;
+template <typename E, typename A, int D, int RPW>
+__global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
+    paged_tree_kernel(const TreeParams p, const HeadScales sc) {
+    using L = CcLayout<D, RPW>;
     extern __shared__ __align__(16) unsigned char smem[];
     float* sq = reinterpret_cast<float*>(smem + L::q);
     float* sk = reinterpret_cast<float*>(smem + L::k);
     float* sv = reinterpret_cast<float*>(smem + L::v);
-    float* ss = reinterpret_cast<float*>(smem + L::s);
-    uint32_t* svis = reinterpret_cast<uint32_t*>(smem + L::vis);
+    float* sp = reinterpret_cast<float*>(smem + L::p);
     int64_t* sslot = reinterpret_cast<int64_t*>(smem + L::slot);
-    float* salpha = reinterpret_cast<float*>(smem + L::alpha);
     TreeStart* st = reinterpret_cast<TreeStart*>(smem + L::start);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tx = tid & 15, ty = tid >> 4;
     const int cta = blockIdx.x;
-    constexpr int kChunks = D * E::kBytes / 16;     // 16-byte chunks of a K or V row
-    constexpr int kDt = D / 16;                     // outputs of a thread in a row
+    constexpr int VPL = D / 32;                     // outputs of a lane in a row
+    constexpr int kPC = 16 / E::kBytes;             // elements of a 16-byte chunk
+    constexpr int kChunks = D / kPC;                // chunks of a K or V row
+    constexpr int kStep = kCcThreads / kChunks;     // rows that the threads load at once
+    constexpr int kPer = kCcTile / kStep;           // chunks of a thread in a tile, of K and of V
+    const int lrow = tid / kChunks, lch = tid % kChunks;
     tree_begin(p, kCcTile, cta, gridDim.x, st, reinterpret_cast<int64_t*>(smem + L::scratch));
     int4 rec = make_int4(0, 0, 0, 0);
     TreeWalk walk(*st);
     TreePiece it;
+#pragma unroll 1
     while (walk.next(p, kCcTile, it)) {
         const int i0 = it.qb * p.tokb;
         const int R = it.rows_tok * p.G;
         const float qscale = E::kBytes == 1 ? p.scale_log2 * sc.k[min(it.h, kMaxScaleHeads - 1)] : p.scale_log2;
         const float vscale = E::kBytes == 1 ? sc.v[min(it.h, kMaxScaleHeads - 1)] : 1.f;
-        // row r: draft i0 + r / G, query head h G + r % G
-        for (int x = tid; x < kCcRows * (D / A::kPerChunk); x += kCcThreads) {
-            const int r = x / (D / A::kPerChunk), ch = x % (D / A::kPerChunk);
-            float f[A::kPerChunk];
+        const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
+        const auto look_up = [&](int j) {   // slots of tile j, threads 0 .. 63
+            const int pos = j * kCcTile + tid;
+            int64_t slot = -1;
+            if (pos < it.kend) {
+                const int blk = __ldg(trow + pos / p.P);
+                if ((unsigned)blk < (unsigned)p.N)
+                    slot = (int64_t)blk * p.P + pos % p.P;
+                else
+                    report(p.dev_status, WF_DEV_BAD_BLOCK);
+            }
+            sslot[j % 3 * kCcTile + tid] = slot;
+        };
+        uint4 kr[kPer], vr[kPer];
+        const auto load = [&](int j) {      // this thread's chunks of tile j
 #pragma unroll
-            for (int e = 0; e < A::kPerChunk; ++e) f[e] = 0.f;
+            for (int i = 0; i < kPer; ++i) {
+                const int64_t slot = sslot[j % 3 * kCcTile + lrow + i * kStep];
+                kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+                if (slot >= 0) {
+                    const int64_t at = ((slot * p.H_kv + it.h) * D + lch * kPC) * E::kBytes;
+                    kr[i] = ld_global_stream(static_cast<const char*>(p.k_pool) + at);
+                    vr[i] = ld_global_stream(static_cast<const char*>(p.v_pool) + at);
+                }
+            }
+        };
+        __syncthreads();   // the last piece's slots and q rows are read
+        if (tid < kCcTile) {
+            look_up(it.j0);
+            if (it.j0 + 1 < it.j1) look_up(it.j0 + 1);
+        }
+        // row r: draft i0 + r / G, query head h G + r % G
+        for (int x = tid; x < L::rows * (D / A::kPerChunk); x += kCcThreads) {
+            const int r = x / (D / A::kPerChunk), ch = x % (D / A::kPerChunk);
+            float f[A::kPerChunk] = {};
             if (r < R) {
                 const int64_t row = (int64_t)(it.q_begin + i0 + r / p.G) * p.H_q + it.h * p.G + r % p.G;
                 widen_chunk<A>(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.q) +
@@ -103,193 +153,146 @@ __global__ void __launch_bounds__(kCcThreads, 2) paged_tree_kernel(const TreePar
 #pragma unroll
             for (int e = 0; e < A::kPerChunk; ++e) sq[r * D + ch * A::kPerChunk + e] = f[e];
         }
-        float o[2][kDt];
+        __syncthreads();
+        load(it.j0);
+        // rows warp + 8 a; the maximum is the same in all lanes, the sum a lane's own positions'
+        float o[RPW][VPL] = {}, m_run[RPW], l_run[RPW] = {};
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int d = 0; d < kDt; ++d) o[a][d] = 0.f;
-        // the softmax state of rows 4 * warp .. 4 * warp + 3, the same in all lanes
-        float m_run[4], l_run[4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            m_run[a] = -INFINITY;
-            l_run[a] = 0.f;
-        }
-        const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
+        for (int a = 0; a < RPW; ++a) m_run[a] = -INFINITY;
+#pragma unroll 1
         for (int j = it.j0; j < it.j1; ++j) {
             const int k0 = j * kCcTile;
-            __syncthreads();   // the last tile is consumed
-            if (tid < kCcTile) {
-                const int pos = k0 + tid;
-                int64_t slot = -1;
-                if (pos < it.kend) {
-                    const int blk = __ldg(trow + pos / p.P);
-                    if ((unsigned)blk < (unsigned)p.N)
-                        slot = (int64_t)blk * p.P + pos % p.P;
-                    else
-                        report(p.dev_status, WF_DEV_BAD_BLOCK);
-                }
-                sslot[tid] = slot;
-            }
-            __syncthreads();
+            if (j != it.j0) __syncthreads();   // the last tile is consumed
             bool wild = false;   // a draft's V row holds an infinity or NaN
-            for (int x = tid; x < kCcTile * kChunks; x += kCcThreads) {
-                const int r = x / kChunks, ch = x % kChunks;
-                const int64_t slot = sslot[r];
-                float* kd = sk + r * L::KS;
-                float* vd = sv + r * D;
-                if (slot >= 0) {
-                    const int64_t elem = (slot * p.H_kv + it.h) * D;
-                    cc_load_row<E, D>(kd, static_cast<const char*>(p.k_pool), elem, ch);
-                    cc_load_row<E, D>(vd, static_cast<const char*>(p.v_pool), elem, ch);
-                    if (k0 + r >= it.c) {
 #pragma unroll
-                        for (int e = 0; e < 16 / E::kBytes; ++e) wild |= !(fabsf(vd[ch * (16 / E::kBytes) + e]) < INFINITY);
-                    }
-                } else {
+            for (int i = 0; i < kPer; ++i) {
+                const int r = lrow + i * kStep;
+                float f[kPC];
+                cc_widen<E>(kr[i], f);
 #pragma unroll
-                    for (int e = 0; e < 16 / E::kBytes; ++e) {
-                        kd[ch * (16 / E::kBytes) + e] = 0.f;
-                        vd[ch * (16 / E::kBytes) + e] = 0.f;
-                    }
+                for (int e = 0; e < kPC; e += 4)
+                    *reinterpret_cast<float4*>(sk + r * L::KS + lch * kPC + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                cc_widen<E>(vr[i], f);
+#pragma unroll
+                for (int e = 0; e < kPC; e += 4)
+                    *reinterpret_cast<float4*>(sv + r * D + lch * kPC + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                if (k0 + r >= it.c) {
+#pragma unroll
+                    for (int e = 0; e < kPC; ++e) wild |= !(fabsf(f[e]) < INFINITY);
                 }
-            }
-            if (tid < 2 * kCcRows) {   // positions k0 + 32 * half .. of the tile that row r sees
-                const int r = tid >> 1, half = tid & 1;
-                uint32_t w = 0;
-                if (r < R) {
-                    const int row = it.q_begin + i0 + r / p.G;
-                    for (int x = 0; x < 32; ++x) {
-                        const int pos = k0 + half * 32 + x;
-                        if (sslot[half * 32 + x] < 0) continue;
-                        if (pos < it.c || tree_bit(p, row, pos - it.c)) w |= 1u << x;
-                    }
-                }
-                svis[tid] = w;
             }
             wild = __syncthreads_or(wild) != 0;
-            // ---- S = Q K^T: rows 2 ty + {0, 1}, positions tx + 16 {0 .. 3} ----
-            float acc[2][4];
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[a][c] = 0.f;
+            if (j + 1 < it.j1) load(j + 1);
+            if (j + 2 < it.j1 && tid < kCcTile) look_up(j + 2);
+            if (warp < R) {
+                // ---- S = Q K^T ----
+                float s[RPW][2] = {};
 #pragma unroll 4
-            for (int d = 0; d < D; d += 4) {
-                float4 qa[2], kb[4];
+                for (int d = 0; d < D; d += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(sk + lane * L::KS + d);
+                    const float4 y = *reinterpret_cast<const float4*>(sk + (lane + 32) * L::KS + d);
 #pragma unroll
-                for (int a = 0; a < 2; ++a) qa[a] = *reinterpret_cast<const float4*>(sq + (2 * ty + a) * D + d);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) kb[c] = *reinterpret_cast<const float4*>(sk + (tx + 16 * c) * L::KS + d);
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        acc[a][c] = fmaf(qa[a].x, kb[c].x, acc[a][c]);
-                        acc[a][c] = fmaf(qa[a].y, kb[c].y, acc[a][c]);
-                        acc[a][c] = fmaf(qa[a].z, kb[c].z, acc[a][c]);
-                        acc[a][c] = fmaf(qa[a].w, kb[c].w, acc[a][c]);
+                    for (int a = 0; a < RPW; ++a) {
+                        const float4 q = *reinterpret_cast<const float4*>(sq + (warp + kCcWarps * a) * D + d);
+                        s[a][0] = fmaf(q.x, x.x, s[a][0]);
+                        s[a][1] = fmaf(q.x, y.x, s[a][1]);
+                        s[a][0] = fmaf(q.y, x.y, s[a][0]);
+                        s[a][1] = fmaf(q.y, y.y, s[a][1]);
+                        s[a][0] = fmaf(q.z, x.z, s[a][0]);
+                        s[a][1] = fmaf(q.z, y.z, s[a][1]);
+                        s[a][0] = fmaf(q.w, x.w, s[a][0]);
+                        s[a][1] = fmaf(q.w, y.w, s[a][1]);
                     }
-            }
+                }
+                // ---- online softmax ----
+                uint32_t sees[RPW][2];
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+                for (int a = 0; a < RPW; ++a) {
+                    const int r = warp + kCcWarps * a;
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) ss[(2 * ty + a) * L::SS + tx + 16 * c] = acc[a][c] * qscale;
-            __syncthreads();
-            // ---- online softmax: warp w has rows 4 w .. 4 w + 3, lane l positions l and l + 32 ----
+                    for (int u = 0; u < 2; ++u) {
+                        const int pos = k0 + lane + 32 * u;
+                        const bool there = r < R && sslot[j % 3 * kCcTile + lane + 32 * u] >= 0 &&
+                                           (pos < it.c || tree_bit(p, it.q_begin + i0 + r / p.G, pos - it.c));
+                        sees[a][u] = __ballot_sync(0xffffffffu, there);
+                        s[a][u] = there ? s[a][u] * qscale : -INFINITY;
+                        mx = fmaxf(mx, s[a][u]);
+                    }
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const int r = 4 * warp + a;
-                const bool v0 = (svis[2 * r] >> lane) & 1u, v1 = (svis[2 * r + 1] >> lane) & 1u;
-                const float s0 = v0 ? ss[r * L::SS + lane] : -INFINITY;
-                const float s1 = v1 ? ss[r * L::SS + lane + 32] : -INFINITY;
-                float mx = fmaxf(s0, s1);
+                    for (int w = 16; w >= 1; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                    const float mn = fmaxf(m_run[a], mx);
+                    const float mu = mn == -INFINITY ? 0.f : mn;
+                    const float al = m_run[a] == -INFINITY ? 0.f : exp2f(m_run[a] - mu);
+                    l_run[a] *= al;
 #pragma unroll
-                for (int w = 16; w >= 1; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                const float mn = fmaxf(m_run[a], mx);
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                const float al = m_run[a] == -INFINITY ? 0.f : exp2f(m_run[a] - mu);
-                const float e0 = v0 ? exp2f(s0 - mu) : 0.f, e1 = v1 ? exp2f(s1 - mu) : 0.f;
-                float sum = e0 + e1;
+                    for (int u = 0; u < 2; ++u) {
+                        const float e = (sees[a][u] >> lane) & 1u ? exp2f(s[a][u] - mu) : 0.f;
+                        l_run[a] += e;
+                        sp[r * kCcTile + lane + 32 * u] = e;
+                    }
 #pragma unroll
-                for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-                l_run[a] = l_run[a] * al + sum;
-                m_run[a] = mn;
-                ss[r * L::SS + lane] = e0;
-                ss[r * L::SS + lane + 32] = e1;
-                if (lane == 0) salpha[r] = al;
-            }
-            __syncthreads();
-            // ---- O = O alpha + P V: rows 2 ty + {0, 1}, columns 4 (tx + 16 i) .. ----
-            const float a0 = salpha[2 * ty], a1 = salpha[2 * ty + 1];
+                    for (int d = 0; d < VPL; ++d) o[a][d] *= al;
+                    m_run[a] = mn;
+                }
+                __syncwarp();
+                // ---- O = O alpha + P V ----
+                if (!wild) {
+#pragma unroll 4
+                    for (int x = 0; x < kCcTile; x += 4) {
+                        float4 w[RPW];
 #pragma unroll
-            for (int d = 0; d < kDt; ++d) {
-                o[0][d] *= a0;
-                o[1][d] *= a1;
-            }
-            if (!wild) {
-#pragma unroll 2
-                for (int x = 0; x < kCcTile; x += 4) {
-                    const float4 p0 = *reinterpret_cast<const float4*>(ss + 2 * ty * L::SS + x);
-                    const float4 p1 = *reinterpret_cast<const float4*>(ss + (2 * ty + 1) * L::SS + x);
-                    const float w0[4] = {p0.x, p0.y, p0.z, p0.w}, w1[4] = {p1.x, p1.y, p1.z, p1.w};
+                        for (int a = 0; a < RPW; ++a)
+                            w[a] = *reinterpret_cast<const float4*>(sp + (warp + kCcWarps * a) * kCcTile + x);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                        for (int u = 0; u < 4; ++u) {
+                            float vf[VPL];
+                            cc_row<VPL>(vf, sv + (x + u) * D + lane * VPL);
 #pragma unroll
-                        for (int c = 0; c < kDt / 4; ++c) {
-                            const float4 vv = *reinterpret_cast<const float4*>(sv + (x + u) * D + 4 * (tx + 16 * c));
-                            const float vf[4] = {vv.x, vv.y, vv.z, vv.w};
+                            for (int a = 0; a < RPW; ++a) {
+                                const float wu = u == 0 ? w[a].x : u == 1 ? w[a].y : u == 2 ? w[a].z : w[a].w;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                o[0][4 * c + e] = fmaf(w0[u], vf[e], o[0][4 * c + e]);
-                                o[1][4 * c + e] = fmaf(w1[u], vf[e], o[1][4 * c + e]);
+                                for (int e = 0; e < VPL; ++e) o[a][e] = fmaf(wu, vf[e], o[a][e]);
                             }
                         }
-                }
-            } else {   // 0 * NaN must not reach a row that does not see the draft
-                for (int x = 0; x < kCcTile; ++x)
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        if (!((svis[2 * (2 * ty + a) + (x >> 5)] >> (x & 31)) & 1u)) continue;
-                        const float w = ss[(2 * ty + a) * L::SS + x];
-#pragma unroll
-                        for (int c = 0; c < kDt / 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[a][4 * c + e] = fmaf(w, sv[x * D + 4 * (tx + 16 * c) + e], o[a][4 * c + e]);
                     }
+                } else {   // 0 * NaN must not reach a row that does not see the draft
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll 1
+                        for (int x = 0; x < 32; ++x)
+#pragma unroll
+                            for (int a = 0; a < RPW; ++a) {
+                                if (!((sees[a][u] >> x) & 1u)) continue;
+                                const float w = sp[(warp + kCcWarps * a) * kCcTile + 32 * u + x];
+#pragma unroll
+                                for (int e = 0; e < VPL; ++e)
+                                    o[a][e] = fmaf(w, sv[(32 * u + x) * D + lane * VPL + e], o[a][e]);
+                            }
+                }
             }
         }
         // ---- the rows, or this piece of them ----
-        __syncthreads();
-        if (lane < 4) salpha[4 * warp + lane] = lane == 0 ? l_run[0] : lane == 1 ? l_run[1] : lane == 2 ? l_run[2] : l_run[3];
         const bool whole = it.j0 == 0 && it.j1 == it.nt;
         const int piece = tree_piece_slot(cta, it.j0);
-        if (!whole) {
-            if (lane < 4) {
-                const float m = lane == 0 ? m_run[0] : lane == 1 ? m_run[1] : lane == 2 ? m_run[2] : m_run[3];
-                p.ws_ml[(int64_t)piece * p.rows + 4 * warp + lane] = make_float2(m, salpha[4 * warp + lane]);
-            }
-            if (it.j0 == 0) rec = tree_record(p, *st, it, cta);
-        }
-        __syncthreads();
+        if (!whole && it.j0 == 0) rec = tree_record(p, *st, it, cta);
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const int r = 2 * ty + a;
+        for (int a = 0; a < RPW; ++a) {
+            const int r = warp + kCcWarps * a;
             if (r >= R) continue;
-            const float l = salpha[r];
+            float l = l_run[a];
+#pragma unroll
+            for (int w = 16; w >= 1; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
             const float f = whole ? (l == 0.f ? 0.f : vscale / l) : vscale;
-            const int64_t row = (int64_t)(it.q_begin + i0 + r / p.G) * p.H_q + it.h * p.G + r % p.G;
 #pragma unroll
-            for (int c = 0; c < kDt / 4; ++c) {
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = l == 0.f ? 0.f : o[a][4 * c + e] * f;
-                const int col = 4 * (tx + 16 * c);
-                if (whole)
-                    store_out<A, 4>(static_cast<char*>(p.out) + (row * D + col) * A::kBytes, y);
-                else
-                    store_out<F32, 4>(p.ws_o + ((int64_t)piece * p.rows + r) * D + col, y);
+            for (int e = 0; e < VPL; ++e) o[a][e] = l == 0.f ? 0.f : o[a][e] * f;
+            if (whole) {
+                const int64_t row = (int64_t)(it.q_begin + i0 + r / p.G) * p.H_q + it.h * p.G + r % p.G;
+                store_out<A, VPL>(static_cast<char*>(p.out) + (row * D + lane * VPL) * A::kBytes, o[a]);
+            } else {
+                const int64_t row = (int64_t)piece * p.rows + r;
+                store_out<F32, VPL>(p.ws_o + row * D + lane * VPL, o[a]);
+                if (lane == 0) p.ws_ml[row] = make_float2(m_run[a], l);
             }
         }
     }
@@ -458,10 +461,10 @@ cudaError_t launch_join(const TreeParams& p, int ctas, cudaStream_t stream) {
                 : cudaLaunchKernelEx(&cfg, paged_tree_join_kernel<A, D>, p);
 }
 
-template <typename E, typename A, int D>
-cudaError_t launch_cc(const TreeParams& p, const HeadScales& sc, int ctas, cudaStream_t stream) {
-    auto kern = paged_tree_kernel<E, A, D>;
-    const int smem = CcLayout<D>::total;
+template <typename E, typename A, int D, int RPW>
+cudaError_t launch_cc_rows(const TreeParams& p, const HeadScales& sc, int ctas, cudaStream_t stream) {
+    auto kern = paged_tree_kernel<E, A, D, RPW>;
+    const int smem = CcLayout<D, RPW>::total;
     cudaError_t err = allow_dynamic_smem((const void*)kern, smem);
     if (err != cudaSuccess) return err;
     kern<<<ctas, kCcThreads, smem, stream>>>(p, sc);
@@ -470,14 +473,24 @@ cudaError_t launch_cc(const TreeParams& p, const HeadScales& sc, int ctas, cudaS
     return launch_join<A, D>(p, ctas, stream);
 }
 
+template <typename E, typename A, int D>
+cudaError_t launch_cc(const TreeParams& p, const HeadScales& sc, int ctas, cudaStream_t stream) {
+    return p.rows == kCcWarps ? launch_cc_rows<E, A, D, 1>(p, sc, ctas, stream)
+                              : launch_cc_rows<E, A, D, 4>(p, sc, ctas, stream);
+}
+
 }  // namespace
 
 static bool tree_shape(const wf_pool_desc& pool, int32_t num_q_heads, int32_t max_q_len, TreeShape* s) {
     if (num_q_heads % pool.num_kv_heads != 0) return false;
     const int G = num_q_heads / pool.num_kv_heads;
     if (G < 1 || G > 8) return false;
-    *s = tree_tc_supported(pool, num_q_heads) ? tree_tc_shape(G, max_q_len, pool.dtype == WF_DTYPE_FP8_E4M3)
-                                              : TreeShape{kCcRows, kCcRows / G, kCcTile, 2, 1};
+    if (tree_tc_supported(pool, num_q_heads)) {
+        *s = tree_tc_shape(G, max_q_len, pool.dtype == WF_DTYPE_FP8_E4M3);
+    } else {
+        const int rpw = cc_rows_per_warp((int64_t)max_q_len * G), bytes = pool.dtype == WF_DTYPE_F32 ? 4 : 2;
+        *s = TreeShape{kCcWarps * rpw, kCcWarps * rpw / G, kCcTile, cc_ctas_per_sm(bytes, pool.head_dim, rpw), 1};
+    }
     return true;
 }
 
