@@ -21,7 +21,10 @@ namespace {
 // A CTA takes 8 RPW rows against 64 positions at a time, a warp RPW of the rows, so that S,
 // the softmax and P V of a row never leave its warp: lane l has positions l and l + 32 of S and
 // columns l D / 32 .. of O.  K and V rows of the next tile are on their way in registers
-// meanwhile; they are widened to fp32 into shared memory once for all warps.
+// meanwhile; they are widened to fp32 into shared memory once for all warps.  With 4 rows a
+// warp the shared-memory reads bound it (12 cycles a step of S against 8 of FMAs): packed FMAs
+// take 177 us where these take 181 (8 requests of up to 61 drafts, 128-wide fp32).  With 1, for
+// chains and small trees, it is the start and the join.
 constexpr int kCcTile = 64;
 constexpr int kCcWarps = 8;
 constexpr int kCcThreads = 32 * kCcWarps;
@@ -77,8 +80,9 @@ __device__ __forceinline__ void cc_row(float (&f)[VPL], const float* from) {
 // CTAs an SM: as many as the registers that the next tile and the rows take leave room for.
 constexpr int cc_ctas_per_sm(int bytes, int D, int rpw) { return bytes == 4 && D == 128 && rpw == 4 ? 1 : 2; }
 
-// Rows of a warp: the fewest that hold all rows of a request's drafts under a KV head.
-constexpr int cc_rows_per_warp(int64_t rows) { return rows <= kCcWarps ? 1 : 4; }
+// Rows of a warp: the fewest that hold all rows of a request's drafts under a KV head, 4 at most
+// (64-wide fp32 heads: 8 rows 13.6 us with 1, 14.9 with 2; 14 rows 53 us with 2, 73 with 4).
+constexpr int cc_rows_per_warp(int64_t rows) { return rows <= kCcWarps ? 1 : rows <= 2 * kCcWarps ? 2 : 4; }
 
 // E: pool elements, A: q and out elements.
 template <typename E, typename A, int D, int RPW>
@@ -475,8 +479,11 @@ cudaError_t launch_cc_rows(const TreeParams& p, const HeadScales& sc, int ctas, 
 
 template <typename E, typename A, int D>
 cudaError_t launch_cc(const TreeParams& p, const HeadScales& sc, int ctas, cudaStream_t stream) {
-    return p.rows == kCcWarps ? launch_cc_rows<E, A, D, 1>(p, sc, ctas, stream)
-                              : launch_cc_rows<E, A, D, 4>(p, sc, ctas, stream);
+    switch (p.rows / kCcWarps) {
+        case 1: return launch_cc_rows<E, A, D, 1>(p, sc, ctas, stream);
+        case 2: return launch_cc_rows<E, A, D, 2>(p, sc, ctas, stream);
+        default: return launch_cc_rows<E, A, D, 4>(p, sc, ctas, stream);
+    }
 }
 
 }  // namespace

@@ -57,6 +57,14 @@ CASES = {
     "fp32 any mask": T([0, 3], [40, 35], 6, 2, 64, 16, "f32", seed=28, density=0.1),
     "fp32 group of 8, blocks of 5": T([64, 30], [9, 20], 8, 1, 64, 5, "f32", seed=29),
     "fp32 peaked": T([300, 40], [9, 20], 8, 2, 128, 16, "f32", seed=30, q_size=30.0),
+    # rows of a warp of the CUDA-core kernel
+    "fp32, 8 rows d128": T([64, 300, 1, 0], [4, 1, 2, 3], 8, 4, 128, 16, "f32", seed=52),
+    "fp32, 16 rows": T([64, 300, 1, 0], [16, 1, 9, 11], 3, 3, 64, 16, "f32", seed=53),
+    "fp32, 16 rows d128 any mask": T([0, 70], [7, 5], 4, 2, 128, 48, "f32", seed=54, density=0.3),
+    "blocks of 7, 8 rows": T([64, 300, 1, 0], [2, 1, 2, 1], 8, 2, 64, 7, "bf16", seed=55),
+    "blocks of 7, 16 rows": T([64, 130], [5, 3], 6, 2, 128, 7, "bf16", seed=56),
+    "fp8 blocks of 7, 8 rows": T([64, 130], [1, 1], 16, 2, 128, 7, "fp8", seed=57, **FP8),
+    "fp8 blocks of 7, 16 rows": T([64, 130, 0], [2, 1, 2], 8, 1, 64, 7, "fp8", seed=58, **FP8),
     # fp8
     "fp8": T([64, 300, 1], [7, 33, 5], 8, 2, 128, 16, "fp8", seed=31, **FP8),
     "fp8 d64": T([64, 300, 0], [7, 70, 30], 8, 2, 64, 16, "fp8", seed=32, **FP8),
