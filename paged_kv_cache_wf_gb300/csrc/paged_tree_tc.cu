@@ -1017,7 +1017,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     } else {
-#pragma unroll 2
+#pragma unroll
                         for (int k = 0; k < 8; ++k) {           // 4 rows of 128 bytes a store
                             const int rr = k * 4 + (lane >> 3), cc = lane & 7;
                             const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
