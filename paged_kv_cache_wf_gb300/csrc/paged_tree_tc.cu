@@ -1053,65 +1053,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // q [rows of all requests, D] bf16 -> the e4m3 parts of q 2^e_r, row r of a request b and
 // draft i at ((b max_q_len + i) H_q + head): hi, then (B max_q_len H_q rows on) lo; and
-// q_inv = 2^-e_r.  A warp a row, lane l holding elements VL l .. VL l + VL - 1.
+// q_inv = 2^-e_r.  A request's rows lie together on both sides, so a CTA takes
+// kPartRows of one request and a lane 8 elements of each of its kPartStep-th rows, whose loads
+// stand before their first use: at a row a warp, 6144 CTAs came in five waves of two dependent
+// loads each.
+constexpr int kPartThreads = 256, kPartPer = 4;
 template <int D>
-__global__ void __launch_bounds__(256) tree_q_parts_kernel(const TreeParams p, unsigned char* __restrict__ parts,
-                                                           float* __restrict__ q_inv) {
-    constexpr int VL = D / 32;
+constexpr int kPartStep = kPartThreads / (D / 8);
+template <int D>
+constexpr int kPartRows = kPartStep<D> * kPartPer;
+
+template <int D>
+__global__ void __launch_bounds__(kPartThreads) tree_q_parts_kernel(const TreeParams p, unsigned char* __restrict__ parts,
+                                                                    float* __restrict__ q_inv, uint32_t chunks) {
+    constexpr int kLanes = D / 8;
     // the attention grid may start its set-up now; it waits for this grid before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t di = w / p.H_q;                    // (request, draft)
-    const int b = (int)(di / p.max_q_len), i = (int)(di % p.max_q_len), hq = (int)(w % p.H_q);
-    if (b >= p.B) return;
+    const int b = (int)(blockIdx.x / chunks);
     const TreeReq req = tree_request(p, b, false);
-    if (i >= req.n) return;
-    const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)(req.q_begin + i) * p.H_q + hq) * D;
-    float x[VL];
-    if constexpr (VL == 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row) + lane);
-        const float2 a = bf16x2_to_float2(v.x), c = bf16x2_to_float2(v.y);
-        x[0] = a.x; x[1] = a.y; x[2] = c.x; x[3] = c.y;
-    } else {
-        const float2 a = bf16x2_to_float2(__ldg(reinterpret_cast<const uint32_t*>(row) + lane));
-        x[0] = a.x; x[1] = a.y;
-    }
-    float top = 0.f;
+    const int64_t live = (int64_t)req.n * p.H_q;
+    const int l = threadIdx.x % kLanes;
+    const int64_t r0 = (int64_t)(blockIdx.x % chunks) * kPartRows<D> + threadIdx.x / kLanes;   // row of the request
+    if (r0 - threadIdx.x / kLanes >= live) return;
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)req.q_begin * p.H_q * D;
+    const int64_t all = (int64_t)p.B * p.max_q_len * p.H_q, to0 = (int64_t)b * p.max_q_len * p.H_q;
+    uint4 raw[kPartPer];
 #pragma unroll
-    for (int e = 0; e < VL; ++e) top = fmaxf(top, fabsf(x[e]));
+    for (int k = 0; k < kPartPer; ++k) {
+        const int64_t r = r0 + k * kPartStep<D>;
+        raw[k] = r < live ? __ldg(reinterpret_cast<const uint4*>(from + r * D) + l) : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    int ex = 0;
-    if (top > 0.f && top < INFINITY) {
-        // floor(log2 top) from the exponent bits; 2^ex and 2^-ex stay normal numbers
-        const int E = max(-126, (int)((__float_as_uint(top) >> 23) & 0xffu) - 127);
-        ex = min(126, max(-126, 7 - E));
-    }
-    const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-    uint32_t hi = 0, lo = 0;
+    for (int k = 0; k < kPartPer; ++k) {
+        const int64_t r = r0 + k * kPartStep<D>;
+        float x[8];
+        widen_chunk<BF16>(raw[k], x);
+        float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < VL; e += 2) {
-        float a = x[e] * up, c = x[e + 1] * up;
-        // the format has no infinities: they count as NaN here, as q K^T of one would be
-        if (!(fabsf(a) < INFINITY)) a = NAN;
-        if (!(fabsf(c) < INFINITY)) c = NAN;
-        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
-        const float2 back = e4m3x2_to_float2(h2);
-        const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, c - back.y), __NV_SATFINITE, __NV_E4M3) &
-                            0xffffu;
-        hi |= h2 << (8 * e);
-        lo |= l2 << (8 * e);
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+        for (int o = kLanes / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        int ex = 0;
+        if (top > 0.f && top < INFINITY) {
+            // floor(log2 top) from the exponent bits; 2^ex and 2^-ex stay normal numbers
+            const int E = max(-126, (int)((__float_as_uint(top) >> 23) & 0xffu) - 127);
+            ex = min(126, max(-126, 7 - E));
+        }
+        const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+        uint32_t hi[2] = {}, lo[2] = {};
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float a = x[e] * up, c = x[e + 1] * up;
+            // the format has no infinities: they count as NaN here, as q K^T of one would be
+            if (!(fabsf(a) < INFINITY)) a = NAN;
+            if (!(fabsf(c) < INFINITY)) c = NAN;
+            const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3) & 0xffffu;
+            const float2 back = e4m3x2_to_float2(h2);
+            const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, c - back.y), __NV_SATFINITE, __NV_E4M3) &
+                                0xffffu;
+            hi[e / 4] |= h2 << (8 * (e & 3));
+            lo[e / 4] |= l2 << (8 * (e & 3));
+        }
+        if (r >= live) continue;
+        *reinterpret_cast<uint2*>(parts + (to0 + r) * D + 8 * l) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(parts + (all + to0 + r) * D + 8 * l) = make_uint2(lo[0], lo[1]);
+        if (l == 0) q_inv[to0 + r] = __uint_as_float((uint32_t)(127 - ex) << 23);
     }
-    const int64_t rows = (int64_t)p.B * p.max_q_len * p.H_q;
-    if constexpr (VL == 4) {
-        *reinterpret_cast<uint32_t*>(parts + w * D + 4 * lane) = hi;
-        *reinterpret_cast<uint32_t*>(parts + (rows + w) * D + 4 * lane) = lo;
-    } else {
-        *reinterpret_cast<unsigned short*>(parts + w * D + 2 * lane) = (unsigned short)hi;
-        *reinterpret_cast<unsigned short*>(parts + (rows + w) * D + 2 * lane) = (unsigned short)lo;
-    }
-    if (lane == 0) q_inv[w] = __uint_as_float((uint32_t)(127 - ex) << 23);
 }
 
 template <int D, int QT>
@@ -1181,7 +1188,8 @@ cudaError_t launch_codes(TreeParams p, const HeadScales& sc, void* prep, int cta
     const int smem = TtLayout<D, 1, true>::total;
     e = allow_dynamic_smem((const void*)kern, smem);
     if (e != cudaSuccess) return e;
-    tree_q_parts_kernel<D><<<(unsigned)((drafts * p.H_q + 7) / 8), 256, 0, stream>>>(p, parts, q_inv);
+    const uint32_t chunks = (uint32_t)(((uint64_t)p.max_q_len * p.H_q + kPartRows<D> - 1) / kPartRows<D>);
+    tree_q_parts_kernel<D><<<p.B * chunks, kPartThreads, 0, stream>>>(p, parts, q_inv, chunks);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // a programmatic dependent of the grid before it: its set-up overlaps
