@@ -1121,6 +1121,12 @@ __global__ void __launch_bounds__(kPartThreads) tree_q_parts_kernel(const TreePa
     }
 }
 
+// A pool row of one head is 128 bytes or fewer (fp8, and 64-wide bf16): an L2 miss that fetches
+// 256 brings a part of the next head, which the CTA that wants it may come for too late (303 MB
+// read from memory for 251 wanted, 64 requests over fp8: 107.2 us, and 105.4 this way; 64-wide
+// bf16 40.9 and 40.4 us).
+constexpr CUtensorMapL2promotion kNarrowRows = CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+
 template <int D, int QT>
 cudaError_t launch_bf16(const TreeParams& p, int ctas, cudaStream_t stream) {
     const int tok = TM / p.G;
@@ -1148,8 +1154,8 @@ cudaError_t launch_bf16(const TreeParams& p, int ctas, cudaStream_t stream) {
         const uint64_t dims[3] = {(uint64_t)D, slots, (uint64_t)p.H_kv};
         const uint64_t strides[2] = {row, (uint64_t)D * 2};
         const uint32_t box[3] = {64, 16, 1};
-        e = encode_tiled_bf16(&tk, const_cast<void*>(p.k_pool), 3, dims, strides, box);
-        if (e == cudaSuccess) e = encode_tiled_bf16(&tv, const_cast<void*>(p.v_pool), 3, dims, strides, box);
+        e = encode_tiled_bf16(&tk, const_cast<void*>(p.k_pool), 3, dims, strides, box, kNarrowRows);
+        if (e == cudaSuccess) e = encode_tiled_bf16(&tv, const_cast<void*>(p.v_pool), 3, dims, strides, box, kNarrowRows);
     }
     if (e != cudaSuccess) return e;
     auto kern = paged_tree_tc_kernel<D, QT, false>;
@@ -1179,10 +1185,11 @@ cudaError_t launch_codes(TreeParams p, const HeadScales& sc, void* prep, int cta
     const uint32_t box[3] = {(uint32_t)D, 16, 1};
     cudaError_t e = encode_tiled(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, parts, 3, qdims, qstrides, qbox, swizzle);
     if (e == cudaSuccess)
-        e = encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(p.k_pool), 3, dims, strides, box, swizzle);
+        e = encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(p.k_pool), 3, dims, strides, box, swizzle,
+                         kNarrowRows);
     if (e == cudaSuccess)
         e = encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(p.v_pool), 3, dims, strides, box,
-                         CU_TENSOR_MAP_SWIZZLE_NONE);
+                         CU_TENSOR_MAP_SWIZZLE_NONE, kNarrowRows);
     if (e != cudaSuccess) return e;
     auto kern = paged_tree_tc_kernel<D, 1, true>;
     const int smem = TtLayout<D, 1, true>::total;

@@ -44,12 +44,14 @@ cudaError_t allow_dynamic_smem(const void* kernel, int bytes) {
 }
 
 cudaError_t encode_tiled_bf16(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
-                              const uint64_t* strides, const uint32_t* box) {
-    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box);
+                              const uint64_t* strides, const uint32_t* box, CUtensorMapL2promotion promotion) {
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B, promotion);
 }
 
 cudaError_t encode_tiled(CUtensorMap* map, CUtensorMapDataType type, void* base, int rank, const uint64_t* dims,
-                         const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+                         const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                         CUtensorMapL2promotion promotion) {
     static std::mutex mu;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     {
@@ -73,7 +75,7 @@ cudaError_t encode_tiled(CUtensorMap* map, CUtensorMapDataType type, void* base,
     }
     const CUresult r = fn(map, type, (cuuint32_t)rank, base, d, s, bx, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

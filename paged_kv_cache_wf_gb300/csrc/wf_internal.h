@@ -22,11 +22,14 @@ cudaError_t allow_dynamic_smem(const void* kernel, int bytes);
 
 // Encode a tiled TMA descriptor for a bf16 tensor (128-byte swizzle, no OOB fill).
 // dims[0] is the contiguous dimension; strides[] are bytes for dims 1..rank-1.
+// `promotion`: the bytes an L2 miss fetches.
 cudaError_t encode_tiled_bf16(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
-                              const uint64_t* strides, const uint32_t* box);
+                              const uint64_t* strides, const uint32_t* box,
+                              CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 cudaError_t encode_tiled(CUtensorMap* map, CUtensorMapDataType type, void* base, int rank, const uint64_t* dims,
                          const uint64_t* strides, const uint32_t* box,
-                         CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+                         CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+                         CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 cudaError_t launch_reshape_and_cache(const void* k, const void* v, void* k_pool, void* v_pool,
                                      const int64_t* slot_mapping, int32_t num_tokens,
