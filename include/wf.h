@@ -137,7 +137,7 @@ wf_status wf_reshape_and_cache(const void* k, const void* v, void* k_pool, void*
  * (tiny-vllm-py, "KV Cache": the cache holds RoPE-rotated K and plain V; weft, "Cache
  *  layouts": write = scatter via slot_mapping)
  *
- *   q_out        [T, H_q, D] dense: the normed and rotated queries (must not overlap q)
+ *   q_out        [T, H_q, D] dense: the normed and rotated queries (must not overlap q, k or v)
  *   q            [T, H_q, D], k and v [T, H_kv, D]: heads and elements of a token are
  *                dense; *_stride is the distance between tokens in elements (at least
  *                the token's own size when T > 1, a multiple of 16 bytes), so the three
@@ -305,7 +305,8 @@ size_t wf_paged_tree_decode_workspace_size(int32_t B, int32_t num_q_heads, int32
  *  have no drafts)
  *
  *   out, q     [T_total, H_q, D]: request b owns rows cu_q_lens[b] .. cu_q_lens[b+1]-1,
- *              its n_b drafts.  Rows past cu_q_lens[B] are neither read nor written.
+ *              its n_b drafts.  Rows past cu_q_lens[B] are not written.  out must not
+ *              overlap q.
  *   cu_q_lens  [B+1] int32, cu_q_lens[0] = 0, non-decreasing, cu_q_lens[B] <= T_total
  *   seq_lens   [B] int32: tokens of request b in the pool INCLUDING its n_b drafts,
  *              already written: with c_b = seq_lens[b] - n_b, draft j lies at cache
@@ -314,7 +315,7 @@ size_t wf_paged_tree_decode_workspace_size(int32_t B, int32_t num_q_heads, int32
  *              0 .. c_b - 1 and to every c_b + j, j < n_b, whose bit j % 32 of word
  *              j / 32 is set.  Bits of j >= n_b are ignored; a row's own bit is not
  *              implied.  mask_words >= ceil(max_q_len / 32).
- *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b]
+ *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b], below 2^31 - 1024
  *   workspace  device scratch of >= wf_paged_tree_decode_workspace_size(B, H_q,
  *              max_q_len, max_seq_len, pool) bytes, 16-byte aligned; needs no
  *              initialisation.  Calls that overlap in time must not share one.

@@ -85,6 +85,11 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 wf_status check_pool(const wf_pool_desc& pool) {
     if (pool.num_blocks < 1 || pool.block_size < 1 || pool.block_size > 1024 ||
         pool.num_kv_heads < 1)
@@ -181,11 +186,12 @@ wf_status wf_qk_norm_rope_and_cache(void* q_out, const void* q, int64_t q_stride
         q_stride = qrow;
         k_stride = v_stride = krow;
     }
-    // every q row is read by several threads while others write q_out
-    const uintptr_t o0 = reinterpret_cast<uintptr_t>(q_out), o1 = o0 + (uintptr_t)(num_tokens * qrow * act);
-    const uintptr_t i0 = reinterpret_cast<uintptr_t>(q),
-                    i1 = i0 + (uintptr_t)(((int64_t)(num_tokens - 1) * q_stride + qrow) * act);
-    if (o0 < i1 && i0 < o1) return WF_ERR_INVALID_ARG;
+    // a row is read by several threads while others write q_out
+    const int64_t out_bytes = num_tokens * qrow * act, last = num_tokens - 1;
+    if (overlap(q_out, out_bytes, q, (last * q_stride + qrow) * act) ||
+        overlap(q_out, out_bytes, k, (last * k_stride + krow) * act) ||
+        overlap(q_out, out_bytes, v, (last * v_stride + krow) * act))
+        return WF_ERR_INVALID_ARG;
     const wf::RopeArgs a{q_out, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos_sin, max_position,
                          rotary_dim, interleaved, positions, k_pool, v_pool, slot_mapping, num_tokens, num_q_heads};
     return from_cuda(wf::launch_qk_norm_rope(a, pool, dev_status, stream));
@@ -368,6 +374,8 @@ wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, con
     if (num_q_heads / pool.num_kv_heads > 8) return WF_ERR_UNSUPPORTED;
     if ((int64_t)max_seq_len > (int64_t)max_blocks_per_seq * pool.block_size || max_q_len > max_seq_len)
         return WF_ERR_INVALID_ARG;
+    // positions are 32-bit and looked at a tile past the end
+    if (max_seq_len >= INT32_MAX - 1023) return WF_ERR_INVALID_ARG;
     if (mask_words < 0 || (int64_t)mask_words * 32 < max_q_len) return WF_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return WF_ERR_INVALID_ARG;
     if (B == 0 || total_q == 0 || max_q_len == 0) return WF_OK;
@@ -380,6 +388,8 @@ wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, con
     const size_t need = wf::tree_workspace_bytes(B, num_q_heads, max_q_len, max_seq_len, pool);
     if (need == 0) return WF_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return WF_ERR_WORKSPACE;
+    const int64_t rows_bytes = (int64_t)total_q * num_q_heads * pool.head_dim * (pool.dtype == WF_DTYPE_F32 ? 4 : 2);
+    if (overlap(out, rows_bytes, q, rows_bytes)) return WF_ERR_INVALID_ARG;
     const wf::TreeArgs a{out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, tree_mask,
                          mask_words, B, total_q, max_q_len, max_seq_len, num_q_heads, scale, workspace};
     return from_cuda(wf::launch_paged_tree(a, pool, dev_status, stream));

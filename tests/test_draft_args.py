@@ -70,6 +70,31 @@ def test_tree_refusals(lib):
         assert call(**bad) == wf.WF_ERR_WORKSPACE, bad
 
 
+def test_outputs_over_inputs_and_lengths_that_leave_no_room_are_refused(lib):
+    d = _desc(N=10, P=16, H=2, D=64)
+    need = wf.wf_paged_tree_decode_workspace_size(2, 8, 7, 64, d)
+    rows = 10 * 8 * 64 * 2
+    far = FAKE + (1 << 30)
+
+    def tree(out, msl=64, M=4, wsb=need):
+        return lib.wf_paged_tree_decode(out, far, FAKE, FAKE, FAKE, M, FAKE, FAKE, FAKE, 1, 2, 10, 7, msl, 8, 0.1, d, FAKE,
+                                        wsb, None, None)
+
+    for at in (far, far + rows - 16, far - rows + 16):
+        assert tree(at) == wf.WF_ERR_INVALID_ARG
+    for msl in (2 ** 31 - 1, 2 ** 31 - 1024):
+        assert tree(FAKE, msl=msl, M=1 << 27, wsb=1 << 40) == wf.WF_ERR_INVALID_ARG
+    assert tree(FAKE, msl=2 ** 31 - 1025, M=1 << 27, wsb=0) == wf.WF_ERR_WORKSPACE     # the largest that passes
+
+    def rope(qo, T=3):
+        return lib.wf_qk_norm_rope_and_cache(qo, FAKE, 768, FAKE + 1024, 768, FAKE + 1280, 768, None, None, 0.0, None, 0, 0,
+                                             0, None, far, far, far, T, 8, d, None, None)
+
+    for qo in (FAKE + 1024, FAKE + 1280, FAKE + 1264 + 256):     # the k and v parts of one token, T = 1
+        assert rope(qo, 1) == wf.WF_ERR_INVALID_ARG
+    assert rope(FAKE + 3 * 768 * 2 - 16) == wf.WF_ERR_INVALID_ARG   # the last token's v
+
+
 def test_tree_workspace_size(lib):
     d = _desc(N=100, P=16, H=8, D=128)
     size = wf.wf_paged_tree_decode_workspace_size
