@@ -135,18 +135,21 @@ class Tree:
         return d
 
     def scales(self):
-        return dict(k_scale=self.ks, v_scale=self.vs) if self.pool == "fp8" else {}
+        if self.pool != "fp8":
+            return {}
+        # one scale, or an array [H_kv, 1]
+        return {n: x if isinstance(x, float) else x.ravel().tolist() for n, x in (("k_scale", self.ks), ("v_scale", self.vs))}
 
     def workspace(self):
         desc = wf.wf_pool_desc(self.N, self.P, self.H_kv, self.D, {"f32": 0, "bf16": 1, "fp8": 2}[self.pool],
-                               self.ks, self.vs)
+                               float(np.max(self.ks)), float(np.max(self.vs)))
         n = wf.wf_paged_tree_decode_workspace_size(self.B, self.H_q, self.max_q, self.max_len, desc)
         # what it holds before a call must not matter
         return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
 
     def kernel(self):
         desc = wf.wf_pool_desc(self.N, self.P, self.H_kv, self.D, {"f32": 0, "bf16": 1, "fp8": 2}[self.pool],
-                               self.ks, self.vs)
+                               float(np.max(self.ks)), float(np.max(self.vs)))
         return wf.wf_paged_tree_decode_kernel(desc, self.H_q)
 
     def run(self, d, ws, stream=None):
