@@ -7,9 +7,10 @@
 // constant for its start and end.  All units stand in a row, request by request
 // (row block, then KV head innermost), and CTA k of n takes the stretch [s k, s (k + 1))
 // of their total cost W, s = ceil(W / n): every CTA gets the same share of tiles
-// whatever the lengths, and at most the first and the last unit of a stretch are cut.  A cut unit's pieces leave their running maximum, sum and unnormalised outputs
-// in the workspace, two pieces a CTA at most, so the workspace does not grow with the
-// context; the joining kernel adds them up in position order.
+// whatever the lengths, and at most the first and the last unit of a stretch are cut.  A
+// cut unit's pieces leave their running maximum, sum and unnormalised outputs in the
+// workspace, two pieces a CTA at most, so the workspace does not grow with the context;
+// the joining kernel adds them up in position order.
 // Fixed spans (as the decode's) would write a row's partial every few hundred
 // positions: at 64 drafts of 4 heads that is as many bytes as the K and V they read.
 #pragma once

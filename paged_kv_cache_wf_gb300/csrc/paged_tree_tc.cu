@@ -16,6 +16,13 @@
 //           half of the columns.
 //   QT = 2  (up to 256 rows a unit): one 128-row query tile each, on the same tiles, so
 //           a loaded tile serves 256 rows.
+// Device time of a call, and of its bytes at the copy peak: 32 requests of 1-16 drafts 34.7
+// and 18.1 us, 118 of 33-61 drafts (QT = 2) 276 and 190 us, 64 of 3-13 drafts of 64-wide heads
+// 40.5 and 15.5 us, 64 of 8-24 drafts over fp8 105.5 and 37.0 us; one request of 8 drafts 11.3 us.
+// What is left: 5.5 us from launch to the first product (division of the work, first block ids,
+// first tiles, cold code); 2-5 us around every piece's end, where its streams wait for one
+// another and O is joined; 2-10 us of the join; and with long pieces the chain S -> softmax ->
+// P V of a stream, 4600 clocks a 128-wide tile of which the softmax is 2700, for two streams.
 // 16 warps: 0-7 softmax (stream t = warp / 4), 8 K loads, 9 V loads, 10 the walk over the
 // CTA's pieces (a ring of records that the other warps read) and the query tiles, 11 and
 // 12 MMA issue (a stream each), 13-15 the V tiles' finish.  The softmax warps take
@@ -332,418 +339,419 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(&piece_empty[i % kRing]);
     };
     if (warp >= kSoftW) {
-    regs_down<kOtherRegs>();
-    if (warp == kKW || warp == kVW) {
-        // ============================= K and V loads =================================
-        // one 16-position box a lane; block ids are read one tile ahead
-        const bool isv = warp == kVW;
-        const CUtensorMap* tm = isv ? &tm_v : &tm_k;
-        const int nslots = !isv ? L::KS : CODES ? L::RS : L::VS;
-        const int slot_bytes = !isv ? L::KTILE : CODES ? L::RAW : L::VTILE;
-        unsigned char* slots = smem + (!isv ? L::k : CODES ? L::raw : L::v);
-        uint64_t* full = !isv ? k_full : CODES ? raw_full : v_full;
-        uint64_t* empty = !isv ? k_empty : CODES ? raw_empty : v_empty;
-        int x = 0, g = 0;       // slot and number of the next tile
-        uint32_t par = 1;       // parity of the slot's last release: 1 passes before the first
-        bool ok = true;
-        for (int i = 0; ok && piece(i); ++i) {
-            const PieceRec& it = ring[i % kRing];
-            const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
-            const int h = it.h, kend = it.kend;
-            int pos = it.j0 * TN + lane * 16;
-            int real = it.j1 - it.j0;        // what is left of the piece, and of its tiles in the ring
-            int left = ring_tiles(real);
-            int blk_next = lane < 8 && pos < kend ? __ldg(trow + pos / p.P) : 0;
+        regs_down<kOtherRegs>();
+        if (warp == kKW || warp == kVW) {
+            // ============================= K and V loads =================================
+            // one 16-position box a lane; block ids are read one tile ahead
+            const bool isv = warp == kVW;
+            const CUtensorMap* tm = isv ? &tm_v : &tm_k;
+            const int nslots = !isv ? L::KS : CODES ? L::RS : L::VS;
+            const int slot_bytes = !isv ? L::KTILE : CODES ? L::RAW : L::VTILE;
+            unsigned char* slots = smem + (!isv ? L::k : CODES ? L::raw : L::v);
+            uint64_t* full = !isv ? k_full : CODES ? raw_full : v_full;
+            uint64_t* empty = !isv ? k_empty : CODES ? raw_empty : v_empty;
+            int x = 0, g = 0;       // slot and number of the next tile
+            uint32_t par = 1;       // parity of the slot's last release: 1 passes before the first
+            bool ok = true;
+            for (int i = 0; ok && piece(i); ++i) {
+                const PieceRec& it = ring[i % kRing];
+                const int32_t* trow = p.block_tables + (int64_t)it.b * p.M;
+                const int h = it.h, kend = it.kend;
+                int pos = it.j0 * TN + lane * 16;
+                int real = it.j1 - it.j0;        // what is left of the piece, and of its tiles in the ring
+                int left = ring_tiles(real);
+                int blk_next = lane < 8 && pos < kend ? __ldg(trow + pos / p.P) : 0;
 #pragma unroll 1
-            for (; left > 0; --left, --real, pos += TN, ++g) {
-                const int blk = blk_next;
-                const bool in = lane < 8 && real > 0 && pos < kend;
-                if (real > 1 && lane < 8 && pos + TN < kend) blk_next = __ldg(trow + (pos + TN) / p.P);
-                if (!bar_wait(&empty[x], par)) {
-                    if (lane == 0) fail();
-                    ok = false;
-                    break;
-                }
-                const bool okb = in && (unsigned)blk < (unsigned)p.N;
-                if (in && !okb && !isv) report(p.dev_status, WF_DEV_BAD_BLOCK);
-                const unsigned okm = __ballot_sync(0xffffffffu, okb);
-                if (lane == 0) {
-                    // 16 tiles on, the tile's readers are past it
-                    okm_of[(isv ? 16 : 0) + (g & 15)] = (unsigned char)okm;
-                    mbar_arrive_expect_tx(&full[x], (uint32_t)__popc(okm) * (uint32_t)L::BOX);
-                }
-                __syncwarp();
-                if (okb) {
-                    const int slot = blk * p.P + pos % p.P;   // a multiple of 16
-                    unsigned char* dst = slots + x * slot_bytes + lane * L::BOX;
-                    if constexpr (L::NC == 2 && !CODES)
-                        tma_load_5d(dst, tm, 0, 0, 0, slot >> 3, h, &full[x]);
-                    else
-                        tma_load_3d_nohint(dst, tm, 0, slot, h, &full[x]);
-                }
-                if (++x == nslots) {
-                    x = 0;
-                    par ^= 1;
-                }
-            }
-            piece_done(i);
-        }
-    } else if (warp == kWalkW) {
-        // ============================= walk, query tiles =============================
-        // publishes records as far ahead as the ring allows and loads each piece's query
-        // tiles once the products that read the tiles before are done
-        TreeWalk walk(*st);
-        TreePiece it;
-        bool more = true;
-        int made = 0, asked = 0, second = 0;   // records, pieces whose tiles are asked for, second tiles
-        int t = 0;
-        uint32_t idle = 0;
-        while (!misc[1] && (more || asked < made)) {
-            bool did = false;
-            if (more && (made < kRing || __shfl_sync(0xffffffffu, (int)mbar_test(&piece_empty[made % kRing],
-                                                                                  (made / kRing - 1) & 1), 0))) {
-                more = walk.next(p, TN, it);
-                if (lane == 0) {
-                    PieceRec& e = ring[made % kRing];
-                    e.nt = more ? it.nt : 0;
-                    if (more) {
-                        e.b = it.b;
-                        e.h = it.h;
-                        e.tok0 = it.qb * p.tokb;
-                        e.q_row = it.q_begin + e.tok0;
-                        e.n = it.n;
-                        e.rows_tok = it.rows_tok;
-                        e.c = it.c;
-                        e.kend = it.kend;
-                        e.j0 = it.j0;
-                        e.j1 = it.j1;
-                        e.last = it.j0 == 0 && it.j1 < it.nt ? tree_record(p, *st, it, cta).z : 0;
+                for (; left > 0; --left, --real, pos += TN, ++g) {
+                    const int blk = blk_next;
+                    const bool in = lane < 8 && real > 0 && pos < kend;
+                    if (real > 1 && lane < 8 && pos + TN < kend) blk_next = __ldg(trow + (pos + TN) / p.P);
+                    if (!bar_wait(&empty[x], par)) {
+                        if (lane == 0) fail();
+                        ok = false;
+                        break;
                     }
-                    mbar_arrive(&piece_full[made % kRing]);
-                }
-                __syncwarp();
-                if (more) ++made;
-                did = true;
-            }
-            if (asked < made) {
-                const PieceRec& e = ring[asked % kRing];
-                if (CODES && asked == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the q parts
-                const int prev = t == 0 ? asked : second;
-                if (prev == 0 || __shfl_sync(0xffffffffu, (int)mbar_test(&q_empty[t], (prev - 1) & 1), 0)) {
+                    const bool okb = in && (unsigned)blk < (unsigned)p.N;
+                    if (in && !okb && !isv) report(p.dev_status, WF_DEV_BAD_BLOCK);
+                    const unsigned okm = __ballot_sync(0xffffffffu, okb);
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&q_full[t], (uint32_t)(2 * D * box_tok * p.G));
-                        if constexpr (CODES) {
-#pragma unroll
-                            for (int part = 0; part < 2; ++part)   // hi rows, then lo rows
-                                tma_load_3d_nohint(smem + L::q + part * (TM * D), &tm_q, 0, e.h * p.G,
-                                                   (part * p.B + e.b) * p.max_q_len + e.tok0, &q_full[t]);
-                        } else {
-#pragma unroll
-                            for (int cb = 0; cb < L::NC; ++cb)
-                                tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64,
-                                                   e.h * p.G, e.q_row + t * tok_tile, &q_full[t]);
-                        }
+                        // 16 tiles on, the tile's readers are past it
+                        okm_of[(isv ? 16 : 0) + (g & 15)] = (unsigned char)okm;
+                        mbar_arrive_expect_tx(&full[x], (uint32_t)__popc(okm) * (uint32_t)L::BOX);
                     }
                     __syncwarp();
-                    if (QT == 2 && t == 0 && e.rows_tok > tok_tile) {
-                        t = 1;
-                    } else {
-                        second += t;
-                        t = 0;
-                        ++asked;
+                    if (okb) {
+                        const int slot = blk * p.P + pos % p.P;   // a multiple of 16
+                        unsigned char* dst = slots + x * slot_bytes + lane * L::BOX;
+                        if constexpr (L::NC == 2 && !CODES)
+                            tma_load_5d(dst, tm, 0, 0, 0, slot >> 3, h, &full[x]);
+                        else
+                            tma_load_3d_nohint(dst, tm, 0, slot, h, &full[x]);
                     }
+                    if (++x == nslots) {
+                        x = 0;
+                        par ^= 1;
+                    }
+                }
+                piece_done(i);
+            }
+        } else if (warp == kWalkW) {
+            // ============================= walk, query tiles =============================
+            // publishes records as far ahead as the ring allows and loads each piece's query
+            // tiles once the products that read the tiles before are done
+            TreeWalk walk(*st);
+            TreePiece it;
+            bool more = true;
+            int made = 0, asked = 0, second = 0;   // records, pieces whose tiles are asked for, second tiles
+            int t = 0;
+            uint32_t idle = 0;
+            while (!misc[1] && (more || asked < made)) {
+                bool did = false;
+                if (more && (made < kRing || __shfl_sync(0xffffffffu, (int)mbar_test(&piece_empty[made % kRing],
+                                                                                      (made / kRing - 1) & 1), 0))) {
+                    more = walk.next(p, TN, it);
+                    if (lane == 0) {
+                        PieceRec& e = ring[made % kRing];
+                        e.nt = more ? it.nt : 0;
+                        if (more) {
+                            e.b = it.b;
+                            e.h = it.h;
+                            e.tok0 = it.qb * p.tokb;
+                            e.q_row = it.q_begin + e.tok0;
+                            e.n = it.n;
+                            e.rows_tok = it.rows_tok;
+                            e.c = it.c;
+                            e.kend = it.kend;
+                            e.j0 = it.j0;
+                            e.j1 = it.j1;
+                            e.last = it.j0 == 0 && it.j1 < it.nt ? tree_record(p, *st, it, cta).z : 0;
+                        }
+                        mbar_arrive(&piece_full[made % kRing]);
+                    }
+                    __syncwarp();
+                    if (more) ++made;
                     did = true;
                 }
-            }
-            if (did) {
-                idle = 0;
-            } else {
-                if (++idle > (1u << 24)) {
-                    if (lane == 0) fail();
-                    break;
-                }
-                __nanosleep(64);
-            }
-        }
-    } else if (warp >= kFinW) {
-        // ============================= V finish ======================================
-        // a third of a tile's rows each, dealt in turn
-        const int fw = warp - kFinW;
-        int x = 0, rx = 0, g = 0;       // slots of the V ring and of the ring of codes; tile
-        uint32_t par = 0, rpar = 0;
-        bool ok = true;
-        for (int i = 0; ok && piece(i); ++i) {
-            const PieceRec& it = ring[i % kRing];
-            bool wild = false;
-            const int j1 = it.j1, kend = it.kend, c0 = it.c;
-#pragma unroll 1
-            for (int j = it.j0, end = j + ring_tiles(j1 - j); j < end; ++j) {
-                const int k0 = j * TN;
-                if (CODES ? !bar_wait(&raw_full[rx], rpar) || !bar_wait(&v_empty[x], par ^ 1)
-                          : !bar_wait(&v_full[x], par)) {
-                    if (lane == 0) fail();
-                    ok = false;
-                    break;
-                }
-                const unsigned okm = okm_of[16 + (g & 15)];
-                ++g;
-                unsigned char* base = smem + L::v + x * L::VTILE;
-                const int r0 = min(TN, max(0, c0 - k0)), r1 = min(TN, kend - k0);
-                if (j >= j1) {
-                    // the empty tile
-                } else if constexpr (CODES) {
-                    const unsigned char* raw = smem + L::raw + rx * L::RAW;
-                    constexpr int kRowChunks = D / 16;       // chunks of 16 codes
-                    constexpr int kStep = 32 / kRowChunks;   // rows a warp covers in a round: 4 or 8
-                    constexpr int kRounds = TN / kStep;
-                    const int ch = lane % kRowChunks, rr = lane / kRowChunks;
-                    const int cb = ch >> 2, cc = (ch & 3) * 2;
-                    // round y: rows kStep y + rr; where two rounds make an 8-row atom (D = 128), the
-                    // odd one's rows are 4 further on, which flips bit 2 of a swizzled chunk's place
-                    const unsigned char* src = raw + rr * D + ch * 16;
-                    unsigned char* dst = base + cb * L::HALF_OFF + rr * 128;
-                    const int o0 = (cc ^ rr) << 4, o1 = ((cc + 1) ^ rr) << 4;
-                    auto out_at = [&](int y, int o) {
-                        return kStep == 8 ? dst + y * L::ATOM + o
-                                          : dst + (y >> 1) * L::ATOM + (y & 1) * 512 + (o ^ ((y & 1) << 6));
-                    };
-                    auto live = [&](int y) {
-                        const int row = kStep * y + rr;
-                        return row < r1 && ((okm >> (row >> 4)) & 1u);
-                    };
-                    uint32_t nan = 0;
-                    if (okm == 0xffu && k0 + TN <= c0) {
-                        // All of it cached context: nothing to look for, every place a constant from
-                        // the warp's own, so a round is a load, eight conversions and two stores.  (These
-                        // warps are few and run in order: with the checks of the other form in it, the
-                        // call took 136 us instead of 117, batch of 64.)
-                        const unsigned char* from = src + fw * kStep * D;
-                        unsigned char* even[2] = {out_at(fw, o0), out_at(fw, o1)};
-                        unsigned char* odd[2] = {out_at(fw + kFin, o0), out_at(fw + kFin, o1)};
-                        constexpr int kMine = (kRounds + kFin - 1) / kFin;   // the last may be past the tile
-                        constexpr int kPair = kStep == 8 ? 2 * kFin * L::ATOM : kFin * L::ATOM;   // two rounds on
-                        constexpr int kBatch = (kMine + 1) / 2;
+                if (asked < made) {
+                    const PieceRec& e = ring[asked % kRing];
+                    if (CODES && asked == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the q parts
+                    const int prev = t == 0 ? asked : second;
+                    if (prev == 0 || __shfl_sync(0xffffffffu, (int)mbar_test(&q_empty[t], (prev - 1) & 1), 0)) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&q_full[t], (uint32_t)(2 * D * box_tok * p.G));
+                            if constexpr (CODES) {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                                for (int part = 0; part < 2; ++part)   // hi rows, then lo rows
+                                    tma_load_3d_nohint(smem + L::q + part * (TM * D), &tm_q, 0, e.h * p.G,
+                                                       (part * p.B + e.b) * p.max_q_len + e.tok0, &q_full[t]);
+                            } else {
+#pragma unroll
+                                for (int cb = 0; cb < L::NC; ++cb)
+                                    tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64,
+                                                       e.h * p.G, e.q_row + t * tok_tile, &q_full[t]);
+                            }
+                        }
+                        __syncwarp();
+                        if (QT == 2 && t == 0 && e.rows_tok > tok_tile) {
+                            t = 1;
+                        } else {
+                            second += t;
+                            t = 0;
+                            ++asked;
+                        }
+                        did = true;
+                    }
+                }
+                if (did) {
+                    idle = 0;
+                } else {
+                    if (++idle > (1u << 24)) {
+                        if (lane == 0) fail();
+                        break;
+                    }
+                    __nanosleep(64);
+                }
+            }
+        } else if (warp >= kFinW) {
+            // ============================= V finish ======================================
+            // a third of a tile's rows each, dealt in turn
+            const int fw = warp - kFinW;
+            int x = 0, rx = 0, g = 0;       // slots of the V ring and of the ring of codes; tile
+            uint32_t par = 0, rpar = 0;
+            bool ok = true;
+            for (int i = 0; ok && piece(i); ++i) {
+                const PieceRec& it = ring[i % kRing];
+                bool wild = false;
+                const int j1 = it.j1, kend = it.kend, c0 = it.c;
+#pragma unroll 1
+                for (int j = it.j0, end = j + ring_tiles(j1 - j); j < end; ++j) {
+                    const int k0 = j * TN;
+                    if (CODES ? !bar_wait(&raw_full[rx], rpar) || !bar_wait(&v_empty[x], par ^ 1)
+                              : !bar_wait(&v_full[x], par)) {
+                        if (lane == 0) fail();
+                        ok = false;
+                        break;
+                    }
+                    const unsigned okm = okm_of[16 + (g & 15)];
+                    ++g;
+                    unsigned char* base = smem + L::v + x * L::VTILE;
+                    const int r0 = min(TN, max(0, c0 - k0)), r1 = min(TN, kend - k0);
+                    if (j >= j1) {
+                        // the empty tile
+                    } else if constexpr (CODES) {
+                        const unsigned char* raw = smem + L::raw + rx * L::RAW;
+                        constexpr int kRowChunks = D / 16;       // chunks of 16 codes
+                        constexpr int kStep = 32 / kRowChunks;   // rows a warp covers in a round: 4 or 8
+                        constexpr int kRounds = TN / kStep;
+                        const int ch = lane % kRowChunks, rr = lane / kRowChunks;
+                        const int cb = ch >> 2, cc = (ch & 3) * 2;
+                        // round y: rows kStep y + rr; where two rounds make an 8-row atom (D = 128), the
+                        // odd one's rows are 4 further on, which flips bit 2 of a swizzled chunk's place
+                        const unsigned char* src = raw + rr * D + ch * 16;
+                        unsigned char* dst = base + cb * L::HALF_OFF + rr * 128;
+                        const int o0 = (cc ^ rr) << 4, o1 = ((cc + 1) ^ rr) << 4;
+                        auto out_at = [&](int y, int o) {
+                            return kStep == 8 ? dst + y * L::ATOM + o
+                                              : dst + (y >> 1) * L::ATOM + (y & 1) * 512 + (o ^ ((y & 1) << 6));
+                        };
+                        auto live = [&](int y) {
+                            const int row = kStep * y + rr;
+                            return row < r1 && ((okm >> (row >> 4)) & 1u);
+                        };
+                        uint32_t nan = 0;
+                        if (okm == 0xffu && k0 + TN <= c0) {
+                            // All of it cached context: nothing to look for, every place a constant from
+                            // the warp's own, so a round is a load, eight conversions and two stores.  (These
+                            // warps are few and run in order: with the checks of the other form in it, the
+                            // call took 136 us instead of 117, batch of 64.)
+                            const unsigned char* from = src + fw * kStep * D;
+                            unsigned char* even[2] = {out_at(fw, o0), out_at(fw, o1)};
+                            unsigned char* odd[2] = {out_at(fw + kFin, o0), out_at(fw + kFin, o1)};
+                            constexpr int kMine = (kRounds + kFin - 1) / kFin;   // the last may be past the tile
+                            constexpr int kPair = kStep == 8 ? 2 * kFin * L::ATOM : kFin * L::ATOM;   // two rounds on
+                            constexpr int kBatch = (kMine + 1) / 2;
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                uint4 c[kBatch];
+#pragma unroll
+                                for (int k = 0; k < kBatch; ++k) {
+                                    const int m = b * kBatch + k;
+                                    if (m < kMine && (m + 1 < kMine || fw + m * kFin < kRounds))
+                                        c[k] = ld_shared_v4(from + m * kFin * kStep * D);
+                                }
+#pragma unroll
+                                for (int k = 0; k < kBatch; ++k) {
+                                    const int m = b * kBatch + k;
+                                    if (m < kMine && (m + 1 < kMine || fw + m * kFin < kRounds)) {
+                                        uint32_t v[8];
+                                        e4m3x16_to_f16(c[k], v);
+                                        unsigned char* const* to = (m & 1) ? odd : even;
+                                        const int at = (m >> 1) * kPair;
+                                        *reinterpret_cast<uint4*>(to[0] + at) = make_uint4(v[0], v[1], v[2], v[3]);
+                                        *reinterpret_cast<uint4*>(to[1] + at) = make_uint4(v[4], v[5], v[6], v[7]);
+                                    }
+                                }
+                            }
+                        } else {
+                        constexpr int kBatch = 2;
+#pragma unroll 1
+                        for (int y0 = fw; y0 < kRounds; y0 += kFin * kBatch) {
                             uint4 c[kBatch];
 #pragma unroll
                             for (int k = 0; k < kBatch; ++k) {
-                                const int m = b * kBatch + k;
-                                if (m < kMine && (m + 1 < kMine || fw + m * kFin < kRounds))
-                                    c[k] = ld_shared_v4(from + m * kFin * kStep * D);
+                                const int y = y0 + k * kFin;
+                                c[k] = make_uint4(0u, 0u, 0u, 0u);
+                                if (y < kRounds && live(y)) c[k] = ld_shared_v4(src + y * kStep * D);
                             }
 #pragma unroll
                             for (int k = 0; k < kBatch; ++k) {
-                                const int m = b * kBatch + k;
-                                if (m < kMine && (m + 1 < kMine || fw + m * kFin < kRounds)) {
-                                    uint32_t v[8];
-                                    e4m3x16_to_f16(c[k], v);
-                                    unsigned char* const* to = (m & 1) ? odd : even;
-                                    *reinterpret_cast<uint4*>(to[0] + (m >> 1) * kPair) = make_uint4(v[0], v[1], v[2], v[3]);
-                                    *reinterpret_cast<uint4*>(to[1] + (m >> 1) * kPair) = make_uint4(v[4], v[5], v[6], v[7]);
+                                const int y = y0 + k * kFin;
+                                if (y >= kRounds) break;
+                                uint32_t v[8];
+                                e4m3x16_to_f16(c[k], v);
+                                if (kStep * y + rr >= r0) nan |= nan_codes(c[k]);
+                                *reinterpret_cast<uint4*>(out_at(y, o0)) = make_uint4(v[0], v[1], v[2], v[3]);
+                                *reinterpret_cast<uint4*>(out_at(y, o1)) = make_uint4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
+                        }
+                        if (__any_sync(0xffffffffu, nan != 0)) {
+                            // a draft's NaN elements are set aside
+#pragma unroll 1
+                            for (int y = fw; y < kRounds; y += kFin) {
+                                if (!live(y) || kStep * y + rr < r0) continue;
+#pragma unroll 1
+                                for (int e = 0; e < 16; ++e) {
+                                    if ((src[y * kStep * D + e] & 0x7f) != 0x7f) continue;
+                                    *reinterpret_cast<unsigned short*>(out_at(y, e < 8 ? o0 : o1) + (e & 7) * 2) = 0;
+                                    wild = true;
                                 }
                             }
                         }
-                    } else {
-                    constexpr int kBatch = 2;
-#pragma unroll 1
-                    for (int y0 = fw; y0 < kRounds; y0 += kFin * kBatch) {
-                        uint4 c[kBatch];
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            const int y = y0 + k * kFin;
-                            c[k] = make_uint4(0u, 0u, 0u, 0u);
-                            if (y < kRounds && live(y)) c[k] = ld_shared_v4(src + y * kStep * D);
-                        }
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            const int y = y0 + k * kFin;
-                            if (y >= kRounds) break;
-                            uint32_t v[8];
-                            e4m3x16_to_f16(c[k], v);
-                            if (kStep * y + rr >= r0) nan |= nan_codes(c[k]);
-                            *reinterpret_cast<uint4*>(out_at(y, o0)) = make_uint4(v[0], v[1], v[2], v[3]);
-                            *reinterpret_cast<uint4*>(out_at(y, o1)) = make_uint4(v[4], v[5], v[6], v[7]);
-                        }
-                    }
-                    }
-                    if (__any_sync(0xffffffffu, nan != 0)) {
-                        // a draft's NaN elements are set aside
-#pragma unroll 1
-                        for (int y = fw; y < kRounds; y += kFin) {
-                            if (!live(y) || kStep * y + rr < r0) continue;
-#pragma unroll 1
-                            for (int e = 0; e < 16; ++e) {
-                                if ((src[y * kStep * D + e] & 0x7f) != 0x7f) continue;
-                                *reinterpret_cast<unsigned short*>(out_at(y, e < 8 ? o0 : o1) + (e & 7) * 2) = 0;
-                                wild = true;
+                        tc::fence_proxy_async_smem();
+                    } else if (okm != 0xffu || k0 + TN > c0) {
+                        // 16-byte chunk cc of row r (its place within the swizzle does not matter);
+                        // with every block id in range, the rows before the first draft stay
+                        const int first = okm == (1u << ((r1 + 15) >> 4)) - 1u ? r0 : 0;
+                        constexpr int kRowChunks = L::NC * 8;
+                        constexpr int kStep = 32 / kRowChunks;
+                        const int rr = lane / kRowChunks, cb = (lane >> 3) % L::NC, cc = lane & 7;
+                        for (int r = first + fw * kStep + rr; r < TN; r += kFin * kStep) {
+                            uint4* at = reinterpret_cast<uint4*>(base + (r >> 3) * L::ATOM + cb * L::HALF_OFF +
+                                                                 (r & 7) * 128 + cc * 16);
+                            if (r >= r1 || !((okm >> (r >> 4)) & 1u)) {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (r >= r0) {
+                                uint4 v = *at;
+                                bool w = tame(v.x);
+                                w |= tame(v.y);
+                                w |= tame(v.z);
+                                w |= tame(v.w);
+                                if (w) *at = v;
+                                wild |= w;
                             }
                         }
+                        tc::fence_proxy_async_smem();
                     }
-                    tc::fence_proxy_async_smem();
-                } else if (okm != 0xffu || k0 + TN > c0) {
-                    // 16-byte chunk cc of row r (its place within the swizzle does not matter);
-                    // with every block id in range, the rows before the first draft stay
-                    const int first = okm == (1u << ((r1 + 15) >> 4)) - 1u ? r0 : 0;
-                    constexpr int kRowChunks = L::NC * 8;
-                    constexpr int kStep = 32 / kRowChunks;
-                    const int rr = lane / kRowChunks, cb = (lane >> 3) % L::NC, cc = lane & 7;
-                    for (int r = first + fw * kStep + rr; r < TN; r += kFin * kStep) {
-                        uint4* at = reinterpret_cast<uint4*>(base + (r >> 3) * L::ATOM + cb * L::HALF_OFF +
-                                                             (r & 7) * 128 + cc * 16);
-                        if (r >= r1 || !((okm >> (r >> 4)) & 1u)) {
-                            *at = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (r >= r0) {
-                            uint4 v = *at;
-                            bool w = tame(v.x);
-                            w |= tame(v.y);
-                            w |= tame(v.z);
-                            w |= tame(v.w);
-                            if (w) *at = v;
-                            wild |= w;
-                        }
+                    wild = __any_sync(0xffffffffu, wild);
+                    if (lane == 0) {
+                        if (j + 1 == j1) wild_of[(i % kRing) * 4 + fw] = wild ? 1 : 0;
+                        mbar_arrive(&v_ready[x]);
+                        if constexpr (CODES) mbar_arrive(&raw_empty[rx]);
                     }
-                    tc::fence_proxy_async_smem();
+                    if (++x == L::VS) {
+                        x = 0;
+                        par ^= 1;
+                    }
+                    if (CODES && ++rx == L::RS) {
+                        rx = 0;
+                        rpar ^= 1;
+                    }
                 }
-                wild = __any_sync(0xffffffffu, wild);
-                if (lane == 0) {
-                    if (j + 1 == j1) wild_of[(i % kRing) * 4 + fw] = wild ? 1 : 0;
-                    mbar_arrive(&v_ready[x]);
-                    if constexpr (CODES) mbar_arrive(&raw_empty[rx]);
+                piece_done(i);
+            }
+        } else {
+            // ============================= MMA issue =====================================
+            // One warp a stream: its products run in order S(0), P(0) V, S(1), P(1) V, ...: S(u + 1)
+            // overwrites the columns P(u) lives in, and the tensor core executes one thread's
+            // products in issue order.  One issuer for both streams was the bound at 16 products a
+            // tile and stream.
+            constexpr uint32_t idS = CODES ? tc::idesc_e4m3_f32(TM, TN, 0, 0) : tc::idesc_bf16_f32(TM, TN, 0, 0);
+            constexpr uint32_t idO = CODES ? tc::idesc_f16_f32(TM, D, 0, 1) : tc::idesc_bf16_f32(TM, D, 0, 1);
+            // An MMA takes its operands from uniform registers.  The slots and parities here are the
+            // same in all lanes, and are kept so that the compiler sees it: otherwise each of a
+            // product's operands is moved over, MMA by MMA, and issuing took longer than computing.
+            const int t = uniform(warp) - kMmaW;
+            const int tq = QT == 1 ? 0 : t;
+            // K-major rows of 128 bytes, or (codes, D = 64) of 64
+            auto kmajor = [](uint32_t at, uint32_t atom) {
+                return CODES && D == 64 ? tc::sdesc_sw64(at, 16, 512) : tc::sdesc_sw128(at, 16, CODES ? 1024 : atom);
+            };
+            const uint64_t qdesc = kmajor(smem_u32(smem + L::q + tq * L::QTILE), 1024);
+            const uint64_t kdesc = kmajor(smem_u32(smem + L::k), L::ATOM);
+            const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::v), L::HALF_OFF, L::ATOM);
+            const uint32_t tm = (uint32_t)uniform((int)tmem);
+            const uint32_t dS = tm + t * L::SCOL, dO = tm + L::OCOL + t * D;
+            int kx = 0, vx = 0;                 // slots of the next tile
+            uint32_t kpar = 0, vpar = 0;        // and their parities
+            uint32_t qpar = 0, ppar = 0;
+            bool ok = true;
+            auto need = [&](uint64_t* bar, uint32_t par) {
+                // no lane may still be polling when one hands the barrier's slot on
+                if (ok && !__all_sync(0xffffffffu, bar_wait(bar, par))) {
+                    if (lane == 0) fail();
+                    ok = false;
                 }
-                if (++x == L::VS) {
+                return ok;
+            };
+            auto step = [&](int& x, uint32_t& par, int n) {
+                if (++x == n) {
                     x = 0;
                     par ^= 1;
                 }
-                if (CODES && ++rx == L::RS) {
-                    rx = 0;
-                    rpar ^= 1;
-                }
-            }
-            piece_done(i);
-        }
-    } else {
-        // ============================= MMA issue =====================================
-        // One warp a stream: its products run in order S(0), P(0) V, S(1), P(1) V, ...: S(u + 1)
-        // overwrites the columns P(u) lives in, and the tensor core executes one thread's
-        // products in issue order.  One issuer for both streams was the bound at 16 products a
-        // tile and stream.
-        constexpr uint32_t idS = CODES ? tc::idesc_e4m3_f32(TM, TN, 0, 0) : tc::idesc_bf16_f32(TM, TN, 0, 0);
-        constexpr uint32_t idO = CODES ? tc::idesc_f16_f32(TM, D, 0, 1) : tc::idesc_bf16_f32(TM, D, 0, 1);
-        // An MMA takes its operands from uniform registers.  The slots and parities here are the
-        // same in all lanes, and are kept so that the compiler sees it: otherwise each of a
-        // product's operands is moved over, MMA by MMA, and issuing took longer than computing.
-        const int t = uniform(warp) - kMmaW;
-        const int tq = QT == 1 ? 0 : t;
-        // K-major rows of 128 bytes, or (codes, D = 64) of 64
-        auto kmajor = [](uint32_t at, uint32_t atom) {
-            return CODES && D == 64 ? tc::sdesc_sw64(at, 16, 512) : tc::sdesc_sw128(at, 16, CODES ? 1024 : atom);
-        };
-        const uint64_t qdesc = kmajor(smem_u32(smem + L::q + tq * L::QTILE), 1024);
-        const uint64_t kdesc = kmajor(smem_u32(smem + L::k), L::ATOM);
-        const uint64_t vdesc = tc::sdesc_sw128(smem_u32(smem + L::v), L::HALF_OFF, L::ATOM);
-        const uint32_t tm = (uint32_t)uniform((int)tmem);
-        const uint32_t dS = tm + t * L::SCOL, dO = tm + L::OCOL + t * D;
-        int kx = 0, vx = 0;                 // slots of the next tile
-        uint32_t kpar = 0, vpar = 0;        // and their parities
-        uint32_t qpar = 0, ppar = 0;
-        bool ok = true;
-        auto need = [&](uint64_t* bar, uint32_t par) {
-            // no lane may still be polling when one hands the barrier's slot on
-            if (ok && !__all_sync(0xffffffffu, bar_wait(bar, par))) {
-                if (lane == 0) fail();
-                ok = false;
-            }
-            return ok;
-        };
-        auto step = [&](int& x, uint32_t& par, int n) {
-            if (++x == n) {
-                x = 0;
-                par ^= 1;
-            }
-        };
-        auto advance = [&]() {              // to the stream's next tile
+            };
+            auto advance = [&]() {              // to the stream's next tile
 #pragma unroll
-            for (int k = 0; k < (QT == 1 ? 2 : 1); ++k) {
+                for (int k = 0; k < (QT == 1 ? 2 : 1); ++k) {
+                    step(kx, kpar, L::KS);
+                    step(vx, vpar, L::VS);
+                }
+            };
+            if (QT == 1 && t == 1) {            // the first tile is stream 0's
                 step(kx, kpar, L::KS);
                 step(vx, vpar, L::VS);
             }
-        };
-        if (QT == 1 && t == 1) {            // the first tile is stream 0's
-            step(kx, kpar, L::KS);
-            step(vx, vpar, L::VS);
-        }
-        for (int i = 0; ok && __all_sync(0xffffffffu, piece(i)); ++i) {
-            const PieceRec& it = ring[i % kRing];
-            const int nt = uniform(steps(it, t)), all = uniform(it.j1 - it.j0);
-            if (QT == 2 && nt == 0) {       // no rows: hand the tiles on as they land
-                for (int u = 0; u < all && ok; ++u) {
+            for (int i = 0; ok && __all_sync(0xffffffffu, piece(i)); ++i) {
+                const PieceRec& it = ring[i % kRing];
+                const int nt = uniform(steps(it, t)), all = uniform(it.j1 - it.j0);
+                if (QT == 2 && nt == 0) {       // no rows: hand the tiles on as they land
+                    for (int u = 0; u < all && ok; ++u) {
+                        if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
+                        if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&v_empty[vx]);
+                        advance();
+                    }
+                    piece_done(i);
+                    continue;
+                }
+                if (!need(&q_full[tq], qpar)) break;
+                qpar ^= 1;
+                if (nt == 0 && lane == 0) mbar_arrive(&q_empty[tq]);
+#pragma unroll 1
+                for (int u = -1; u < nt && ok; ++u) {
+                    // P V of step u ...
+                    if (u >= 0) {
+                        if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
+                        ppar ^= 1;
+                        tc::fence_after_sync();
+                        const uint32_t vd = (uint32_t)vdesc + ((vx * L::VTILE) >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < TN / 16; ++kk)
+                                mma<1>(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), 0u, vd + ((kk * 2 * L::ATOM) >> 4),
+                                       (uint32_t)(vdesc >> 32), idO, (u > 0 || kk > 0) ? 1u : 0u);
+                            tc::commit(&v_empty[vx]);
+                            tc::commit(pv_done(t));
+                        }
+                        __syncwarp();
+                        advance();
+                    }
+                    // ... then S of step u + 1
+                    if (u + 1 < nt) {
+                        if (!need(&k_full[kx], kpar)) break;
+                        tc::fence_after_sync();
+                        if (elect_one()) {
+                            const uint32_t kd = (uint32_t)kdesc + ((kx * L::KTILE) >> 4), qd = (uint32_t)qdesc;
+                            const uint32_t khi = (uint32_t)(kdesc >> 32), qhi = (uint32_t)(qdesc >> 32);
+                            if constexpr (CODES) {       // the two parts of q, one after the other
+#pragma unroll
+                                for (int x = 0; x < 2 * D / 32; ++x) {
+                                    const int part = x / (D / 32), kk = x % (D / 32);
+                                    mma<2>(dS, qd + ((part * TM * D + kk * 32) >> 4), qhi, kd + ((kk * 32) >> 4), khi, idS,
+                                           x > 0 ? 1u : 0u);
+                                }
+                            } else {
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
+                                    const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
+                                    mma<0>(dS, qd + (qoff >> 4), qhi, kd + (koff >> 4), khi, idS, kk > 0 ? 1u : 0u);
+                                }
+                            }
+                            tc::commit(s_full(t));
+                            tc::commit(&k_empty[kx]);
+                            if (u + 2 == nt) tc::commit(&q_empty[tq]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (QT == 1 && ok && 2 * nt + t < ring_tiles(all)) {   // stream 1's empty tile: hand it back
                     if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
                     if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&v_empty[vx]);
                     advance();
                 }
                 piece_done(i);
-                continue;
             }
-            if (!need(&q_full[tq], qpar)) break;
-            qpar ^= 1;
-            if (nt == 0 && lane == 0) mbar_arrive(&q_empty[tq]);
-#pragma unroll 1
-            for (int u = -1; u < nt && ok; ++u) {
-                // P V of step u ...
-                if (u >= 0) {
-                    if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
-                    ppar ^= 1;
-                    tc::fence_after_sync();
-                    const uint32_t vd = (uint32_t)vdesc + ((vx * L::VTILE) >> 4);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < TN / 16; ++kk)
-                            mma<1>(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), 0u, vd + ((kk * 2 * L::ATOM) >> 4),
-                                   (uint32_t)(vdesc >> 32), idO, (u > 0 || kk > 0) ? 1u : 0u);
-                        tc::commit(&v_empty[vx]);
-                        tc::commit(pv_done(t));
-                    }
-                    __syncwarp();
-                    advance();
-                }
-                // ... then S of step u + 1
-                if (u + 1 < nt) {
-                    if (!need(&k_full[kx], kpar)) break;
-                    tc::fence_after_sync();
-                    if (elect_one()) {
-                        const uint32_t kd = (uint32_t)kdesc + ((kx * L::KTILE) >> 4), qd = (uint32_t)qdesc;
-                        const uint32_t khi = (uint32_t)(kdesc >> 32), qhi = (uint32_t)(qdesc >> 32);
-                        if constexpr (CODES) {       // the two parts of q, one after the other
-#pragma unroll
-                            for (int x = 0; x < 2 * D / 32; ++x) {
-                                const int part = x / (D / 32), kk = x % (D / 32);
-                                mma<2>(dS, qd + ((part * TM * D + kk * 32) >> 4), qhi, kd + ((kk * 32) >> 4), khi, idS,
-                                       x > 0 ? 1u : 0u);
-                            }
-                        } else {
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
-                                const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
-                                mma<0>(dS, qd + (qoff >> 4), qhi, kd + (koff >> 4), khi, idS, kk > 0 ? 1u : 0u);
-                            }
-                        }
-                        tc::commit(s_full(t));
-                        tc::commit(&k_empty[kx]);
-                        if (u + 2 == nt) tc::commit(&q_empty[tq]);
-                    }
-                    __syncwarp();
-                }
-            }
-            if (QT == 1 && ok && 2 * nt + t < ring_tiles(all)) {   // stream 1's empty tile: hand it back
-                if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
-                if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&v_empty[vx]);
-                advance();
-            }
-            piece_done(i);
         }
-    }
     } else {
         // ============================= softmax =======================================
         regs_up<kSoftRegs>();
@@ -995,7 +1003,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     x = (static_cast<const unsigned char*>(p.v_pool)[at + e] & 0x7f) == 0x7f ? NAN : 0.f;
                                 else
                                     x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pool)[at + e]);
-                                float* y = reinterpret_cast<float*>(stage + lane * 128 + (((e >> 2) ^ (lane & 7)) << 4)) + (e & 3);
+                                float* y = reinterpret_cast<float*>(stage + lane * 128 +
+                                                                    (((e >> 2) ^ (lane & 7)) << 4)) + (e & 3);
                                 if (!(fabsf(x) < INFINITY)) *y += x;
                             }
                         }
