@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
         // ---- the rows, or this piece of them ----
         const bool whole = it.j0 == 0 && it.j1 == it.nt;
         const int piece = tree_piece_slot(cta, it.j0);
-        if (!whole && it.j0 == 0) rec = tree_record(p, *st, it, cta);
+        if (!whole && it.j0 == 0) rec = make_int4(it.q_begin + i0, it.h, tree_last(*st, it, cta), R);
 #pragma unroll
         for (int a = 0; a < RPW; ++a) {
             const int r = warp + kCcWarps * a;
@@ -313,42 +313,44 @@ __global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
 // ---------------------------------------------------------------------------
 // CTA (k, y): the unit cut at the end of CTA k's stretch, rows 8 y .. 8 y + 7, a warp a
 // row: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over its pieces i in position
-// order.  Pieces are read kChunk at a time, all loads before the first use.  Launched as
-// a programmatic dependent of the kernel before it.
+// order.  Latency is all of it, so the first two pieces, which every cut unit has and whose
+// places do not depend on the record, are read beside it, and the others kChunk at a time.
+// Launched as a programmatic dependent of the kernel before it.
 template <typename A, int D>
 __global__ void __launch_bounds__(256) paged_tree_join_kernel(const TreeParams p) {
     constexpr int VPL = D / 32;
     constexpr int kChunk = 8;
     using Vec = typename std::conditional<VPL == 4, float4, float2>::type;
     const int lane = threadIdx.x & 31;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);   // below p.rows, a multiple of 8
+    const int first = blockIdx.x;
+    Vec x[kChunk];
+    float2 ml[kChunk];
+    const auto load = [&](int u, int cta, int i) {   // piece i of the unit, in `cta`
+        const int64_t at = (int64_t)tree_piece_slot(cta, i) * p.rows + r;
+        ml[u] = __ldcg(p.ws_ml + at);
+        x[u] = __ldcg(reinterpret_cast<const Vec*>(p.ws_o + at * D) + lane);
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 rec = __ldcg(p.ws_rec + blockIdx.x);
-    if (rec.w == 0) return;
-    const int q_begin = __ldg(p.cu_q_lens + rec.x), n = __ldg(p.cu_q_lens + rec.x + 1) - q_begin;
-    const int qb = rec.y / p.H_kv, h = rec.y - qb * p.H_kv;
-    const int i0 = qb * p.tokb;
-    if (r >= min(p.tokb, n - i0) * p.G) return;
-    const int first = blockIdx.x, cnt = rec.z - first + 1;
+    const int4 rec = __ldcg(p.ws_rec + first);
+    load(0, first, 0);
+    load(1, min(first + 1, (int)gridDim.x - 1), 1);
+    if (r >= rec.w) return;
+    const int cnt = rec.z - first + 1;
     float M = -INFINITY, den = 0.f;
-    float o[VPL];
+    float o[VPL] = {};
+#pragma unroll 1
+    for (int u0 = 0; u0 < cnt;) {
+        const int take = u0 == 0 ? 2 : min(kChunk, cnt - u0);
+        if (u0 > 0) {
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) o[e] = 0.f;
-    for (int u0 = 0; u0 < cnt; u0 += kChunk) {
-        Vec x[kChunk];
-        float2 ml[kChunk];
-#pragma unroll
-        for (int u = 0; u < kChunk; ++u) {
-            ml[u] = make_float2(-INFINITY, 0.f);
-            if (u0 + u < cnt) {
-                const int64_t at = (int64_t)tree_piece_slot(first + u0 + u, u0 + u) * p.rows + r;
-                ml[u] = __ldcg(p.ws_ml + at);
-                x[u] = __ldcg(reinterpret_cast<const Vec*>(p.ws_o + at * D) + lane);
-            }
+            for (int u = 0; u < kChunk; ++u)
+                if (u < take) load(u, first + u0 + u, u0 + u);
         }
         float mn = M;
 #pragma unroll
-        for (int u = 0; u < kChunk; ++u) mn = fmaxf(mn, ml[u].x);
+        for (int u = 0; u < kChunk; ++u)
+            if (u < take) mn = fmaxf(mn, ml[u].x);
         // a piece (or all before it) without a maximum has a sum of 0, or of NaN, which has to stay
         const float a = M == -INFINITY ? 1.f : exp2f(M - mn);
         den *= a;
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(256) paged_tree_join_kernel(const TreeParams p
         for (int e = 0; e < VPL; ++e) o[e] *= a;
 #pragma unroll
         for (int u = 0; u < kChunk; ++u) {
-            if (u0 + u >= cnt || ml[u].y == 0.f) continue;
+            if (u >= take || ml[u].y == 0.f) continue;
             const float w = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - mn);
             den += w * ml[u].y;
             o[0] += w * x[u].x;
@@ -367,10 +369,11 @@ __global__ void __launch_bounds__(256) paged_tree_join_kernel(const TreeParams p
             }
         }
         M = mn;
+        u0 += take;
     }
 #pragma unroll
     for (int e = 0; e < VPL; ++e) o[e] = den == 0.f ? 0.f : o[e] / den;
-    const int64_t row = (int64_t)(q_begin + i0 + r / p.G) * p.H_q + h * p.G + r % p.G;
+    const int64_t row = (int64_t)(rec.x + r / p.G) * p.H_q + rec.y * p.G + r % p.G;
     store_out<A, VPL>(static_cast<char*>(p.out) + (row * D + lane * VPL) * A::kBytes, o);
 }
 
@@ -390,10 +393,7 @@ __global__ void __launch_bounds__(256, kManyCtasPerSm) paged_tree_join_many_kern
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 rec = __ldcg(p.ws_rec + blockIdx.x);
     if (rec.w == 0) return;
-    const int q_begin = __ldg(p.cu_q_lens + rec.x), n = __ldg(p.cu_q_lens + rec.x + 1) - q_begin;
-    const int qb = rec.y / p.H_kv, h = rec.y - qb * p.H_kv;
-    const int i0 = qb * p.tokb;
-    const int rows = min(p.tokb, n - i0) * p.G;
+    const int rows = rec.w;
     const int first = blockIdx.x, cnt = rec.z - first + 1, step = 8 * gridDim.y;
 #pragma unroll 1
     for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += kManyRows * step) {
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(256, kManyCtasPerSm) paged_tree_join_many_kern
             if (rk >= rows) break;
 #pragma unroll
             for (int e = 0; e < VPL; ++e) o[k][e] = den[k] == 0.f ? 0.f : o[k][e] / den[k];
-            const int64_t row = (int64_t)(q_begin + i0 + rk / p.G) * p.H_q + h * p.G + rk % p.G;
+            const int64_t row = (int64_t)(rec.x + rk / p.G) * p.H_q + rec.y * p.G + rk % p.G;
             store_out<A, VPL>(static_cast<char*>(p.out) + (row * D + lane * VPL) * A::kBytes, o[k]);
         }
     }

@@ -31,7 +31,9 @@ struct TreeParams {
     uint32_t* dev_status;
     float* ws_o;     // [2 * CTAs][row block] rows of D
     float2* ws_ml;   // [2 * CTAs][row block]
-    int4* ws_rec;    // [CTAs]: the cut unit that starts in this CTA
+    // [CTAs]: the cut unit that starts in this CTA: {its first draft's row of q, KV head, last CTA
+    // with a piece of it, rows (0: there is no such unit)}
+    int4* ws_rec;
     int32_t M, B, total_q, max_q_len, max_seq_len, H_q, H_kv, G, N, P, W;
     int32_t rows;    // rows of a row block in the workspace
     int32_t tokb;    // drafts of a row block
@@ -87,6 +89,7 @@ struct alignas(16) TreeStart {   // 64-bit scratch follows it in shared memory
     int pos;     // its first cost position
     int off;     // that position within request b
     int b;
+    TreeReq r;   // request b
 };
 
 // All threads of the CTA; `scratch` holds blockDim.x / 32 values.  Ends with a barrier.
@@ -131,9 +134,11 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
         int at = first;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const int c = (int)tree_cost(p, tree_request(p, b, false), tile);
+            const TreeReq r = tree_request(p, b, false);
+            const int c = (int)tree_cost(p, r, tile);
             if (s < at + c) {
                 st->b = b;
+                st->r = r;
                 st->off = s - at;
                 break;
             }
@@ -161,7 +166,7 @@ struct TreeWalk {
     TreeReq r;
 
     __device__ __forceinline__ TreeWalk(const TreeStart& st)
-        : pos(st.pos), left(st.left), off(st.off), b(st.b), ready(0) {}
+        : pos(st.pos), left(st.left), off(st.off), b(st.b), ready(1), r(st.r) {}
 
     __device__ __forceinline__ bool next(const TreeParams& p, int tile, TreePiece& it) {
         const int lane = threadIdx.x & 31;
@@ -216,13 +221,12 @@ struct TreeWalk {
 // later one in the first place of its own.
 __device__ __forceinline__ int tree_piece_slot(int cta, int j0) { return 2 * cta + (j0 == 0 ? 1 : 0); }
 
-// The record of the cut unit whose first piece `it` is: {request, row block * H_kv + KV
-// head, last CTA that holds a piece, 1}.
-__device__ __forceinline__ int4 tree_record(const TreeParams& p, const TreeStart& st, const TreePiece& it, int cta) {
+// The last CTA that holds a piece of the unit whose first piece `it` is.
+__device__ __forceinline__ int tree_last(const TreeStart& st, const TreePiece& it, int cta) {
     int last = cta;
 #pragma unroll 1
     for (int64_t next = (int64_t)st.share * (cta + 1); next < it.end; next += st.share) ++last;
-    return make_int4(it.b, it.qb * p.H_kv + it.h, last, 1);
+    return last;
 }
 
 // Whether draft row i of a request sees its draft j.

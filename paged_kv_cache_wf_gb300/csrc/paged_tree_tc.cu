@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             e.kend = it.kend;
                             e.j0 = it.j0;
                             e.j1 = it.j1;
-                            e.last = it.j0 == 0 && it.j1 < it.nt ? tree_record(p, *st, it, cta).z : 0;
+                            e.last = it.j0 == 0 && it.j1 < it.nt ? tree_last(*st, it, cta) : 0;
                         }
                         mbar_arrive(&piece_full[made % kRing]);
                     }
@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int tile_row = it.q_row + t0;
             const int64_t wbase = (int64_t)slot_of_piece * p.rows + t0 * p.G;
             if (!whole) {
-                if (it.j0 == 0) rec = make_int4(it.b, it.tok0 / p.tokb * p.H_kv + it.h, it.last, 1);
+                if (it.j0 == 0) rec = make_int4(it.q_row, it.h, it.last, it.rows_tok * p.G);
                 if (row_valid && (QT == 2 || t == 0)) p.ws_ml[wbase + r] = make_float2(m_ref, l_run);
             }
             const float f = v_scale * (!whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run);
