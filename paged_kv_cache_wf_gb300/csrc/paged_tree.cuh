@@ -112,12 +112,14 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
     }
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int64_t before = 0, total = 0;
-#pragma unroll 4
-    for (int w = 0; w < nwarp; ++w) {
-        if (w < warp) before += scratch[w];
-        total += scratch[w];
-    }
+    // sums over the warps, in two parts of 20 bits and more (2^40 stands for all that is too much)
+    const int64_t v = lane < nwarp ? min(scratch[lane], (int64_t)1 << 40) : 0;
+    const uint32_t lo = (uint32_t)v & 0xfffffu, hi = (uint32_t)(v >> 20);
+    const auto sum = [](uint32_t h, uint32_t l) {
+        return ((int64_t)__reduce_add_sync(0xffffffffu, h) << 20) + __reduce_add_sync(0xffffffffu, l);
+    };
+    int64_t total = sum(hi, lo);
+    const int64_t before = sum(lane < warp ? hi : 0u, lane < warp ? lo : 0u);
     if (total > INT32_MAX) {
         if (cta == 0 && tid == 0) report(p.dev_status, WF_DEV_BAD_SEQLEN);
         total = mine = 0;
