@@ -16,10 +16,10 @@
 //           half of the columns.
 //   QT = 2  (up to 256 rows a unit): one 128-row query tile each, on the same tiles, so
 //           a loaded tile serves 256 rows.
-// Device time of a call, and of its bytes at the copy peak: 32 requests of 1-16 drafts 34.7
-// and 18.1 us, 118 of 33-61 drafts (QT = 2) 276 and 190 us, 64 of 3-13 drafts of 64-wide heads
-// 40.5 and 15.5 us, 64 of 8-24 drafts over fp8 105.5 and 37.0 us; one request of 8 drafts 11.3 us.
-// What is left: 5.5 us from launch to the first product (division of the work, first block ids,
+// Device time of a call, and of its bytes at the copy peak: 32 requests of 1-16 drafts 33.9
+// and 18.1 us, 118 of 33-61 drafts (QT = 2) 275 and 190 us, 64 of 3-13 drafts of 64-wide heads
+// 39.4 and 15.5 us, 64 of 8-24 drafts over fp8 103 and 37.0 us; one request of 8 drafts 10.9 us.
+// What is left: 5 us from launch to the first product (division of the work, first block ids,
 // first tiles, cold code); 2-5 us around every piece's end, where its streams wait for one
 // another and O is joined; 2-10 us of the join; and with long pieces the chain S -> softmax ->
 // P V of a stream, 4600 clocks a 128-wide tile of which the softmax is 2700, for two streams.
