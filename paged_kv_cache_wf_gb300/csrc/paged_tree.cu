@@ -22,8 +22,9 @@ namespace {
 // the softmax and P V of a row never leave its warp: lane l has positions l and l + 32 of S and
 // columns l D / 32 .. of O.  K and V rows of the next tile are on their way in registers
 // meanwhile; they are widened to fp32 into shared memory once for all warps.  With 4 rows a
-// warp the shared-memory reads bound it (12 cycles a step of S against 8 of FMAs): packed FMAs
-// take 177 us where these take 181 (8 requests of up to 61 drafts, 128-wide fp32).  With 1, for
+// warp it runs at half the FMA pipe's rate (8 requests of up to 61 drafts, 128-wide fp32: 181 us,
+// 92 of FMAs); packed FMAs (177 us) and tiles of 2 x 4 a lane, which read half as much shared
+// memory (184 us), leave it there.  With 1, for
 // chains and small trees, it is the start and the join: 8 requests of up to 7 drafts of 64-wide
 // fp32 heads 13.6 us, 2.0 at the copy peak; blocks of 7, 8 requests of up to 16 drafts of
 // 128-wide bf16 heads 62 us.
