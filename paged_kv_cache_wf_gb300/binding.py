@@ -166,13 +166,23 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = None   # the current stream's handle: a tenth of current_stream()'s time
+
+
+def _find_raw_stream():
+    global _raw_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and torch.cuda.is_initialized():
+        device = torch._C._cuda_getDevice
+        _raw_stream = lambda: raw(device())   # noqa: E731
+        return _raw_stream()
+    return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a tenth of current_stream()'s time
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch._C._cuda_getDevice())
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream() if _raw_stream is not None else _find_raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -232,6 +242,23 @@ def _desc(k_pool, k_scale, v_scale):
     return d
 
 
+_known_types = None
+
+
+def _types():
+    """torch's dtypes, looked up once."""
+    global _known_types
+    import torch
+    _known_types = (torch.bfloat16, torch.uint8, torch.float32, torch.int32, torch.int64)
+    return _known_types
+
+
+def _dense(*ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("libwf takes dense row-major tensors")
+
+
 def _contig(*ts):
     for t in ts:
         if t is not None and not isinstance(t, int) and not t.is_contiguous():
@@ -259,12 +286,12 @@ def wf_qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps: float, co
     """Norm (q_weight, k_weight [D] or None) and rotate q [T, H_q, D] and k [T, H_kv, D] (cos_sin [positions, rotary_dim]
     float32 or None, positions [T] int32), write q_out [T, H_q, D] and scatter the new k and v rows into the pools.
     q, k and v may be strided over tokens (views of one fused projection)."""
-    import torch
-    _contig(q_out, q_weight, k_weight, cos_sin, positions, k_pool, v_pool, slot_mapping)
+    bf16, u8, f32, i32, i64 = _known_types or _types()
+    _dense(q_out, q_weight, k_weight, cos_sin, positions, k_pool, v_pool, slot_mapping)
     T, H_q, D = q.shape
     _, _, H_kv, pool_D = k_pool.shape
     dt, pool_dt = q.dtype, k_pool.dtype
-    if D != pool_D or dt is not (torch.bfloat16 if pool_dt is torch.uint8 else pool_dt) or \
+    if D != pool_D or dt is not (bf16 if pool_dt is u8 else pool_dt) or \
             q_out.shape != q.shape or q_out.dtype is not dt or v_pool.shape != k_pool.shape or v_pool.dtype is not pool_dt:
         raise ValueError("q, k, v and q_out have the pool's dtype (bf16 for fp8 pools) and head size, q_out is like q")
     rows = (T, H_kv, D)
@@ -273,7 +300,7 @@ def wf_qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps: float, co
     (qs, qh, qe), (ks, kh, ke), (vs, vh, ve) = q.stride(), k.stride(), v.stride()
     if qe != 1 or ke != 1 or ve != 1 or (qh != D and H_q > 1) or ((kh != D or vh != D) and H_kv > 1):
         raise ValueError("q, k, v: heads and elements of a token must be dense")
-    if slot_mapping.shape[0] != T or slot_mapping.dtype is not torch.int64:
+    if slot_mapping.shape[0] != T or slot_mapping.dtype is not i64:
         raise ValueError(f"slot_mapping must be [{T}] int64")
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype is not dt or w.numel() != D):
@@ -281,13 +308,14 @@ def wf_qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps: float, co
     max_position = rotary = 0
     if cos_sin is not None:
         max_position, rotary = cos_sin.shape
-        if cos_sin.dtype is not torch.float32 or positions.dtype is not torch.int32 or positions.shape[0] != T:
+        if cos_sin.dtype is not f32 or positions.dtype is not i32 or positions.shape[0] != T:
             raise ValueError("cos_sin must be [max_position, rotary_dim] float32 and positions [T] int32")
-    rc = load().wf_qk_norm_rope_and_cache(
-        q_out.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q_weight), _ptr(k_weight), eps,
-        _ptr(cos_sin), max_position, rotary, interleaved, _ptr(positions) if rotary else None, k_pool.data_ptr(),
-        v_pool.data_ptr(), slot_mapping.data_ptr(), T, H_q, _desc(k_pool, k_scale, v_scale), _ptr(dev_status),
-        _stream(stream))
+    rc = (_lib or load()).wf_qk_norm_rope_and_cache(
+        q_out.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        q_weight.data_ptr() if q_weight is not None else None, k_weight.data_ptr() if k_weight is not None else None, eps,
+        cos_sin.data_ptr() if rotary else None, max_position, rotary, interleaved,
+        positions.data_ptr() if rotary else None, k_pool.data_ptr(), v_pool.data_ptr(), slot_mapping.data_ptr(), T, H_q,
+        _desc(k_pool, k_scale, v_scale), _ptr(dev_status), _stream(stream))
     if rc:
         raise WfError("wf_qk_norm_rope_and_cache", rc)
 
@@ -367,7 +395,7 @@ def wf_paged_tree_decode(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_le
                          v_scale=1.0):
     """out, q [T_total, H_q, D] packed drafts; cu_q_lens [B+1] int32; seq_lens [B] int32 count the drafts; tree_mask
     [T_total, words] int32 (bit j of a row: draft j of its request is seen); workspace uint8 tensor."""
-    _contig(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, tree_mask)
+    _dense(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, tree_mask)
     T, H_q, D = q.shape
     B, M = block_tables.shape
     rows, words = tree_mask.shape
@@ -377,7 +405,7 @@ def wf_paged_tree_decode(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_le
         raise ValueError("out is like q [T, H_q, D] of the pool's dtype (bf16 for fp8 pools) and head size")
     if rows != T or tree_mask.element_size() != 4 or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1:
         raise ValueError("tree_mask is [T, words] of 32-bit words, block_tables [B, M], seq_lens [B], cu_q_lens [B + 1]")
-    rc = load().wf_paged_tree_decode(
+    rc = (_lib or load()).wf_paged_tree_decode(
         out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), M,
         seq_lens.data_ptr(), cu_q_lens.data_ptr(), tree_mask.data_ptr(), words, B, T, max_q_len, max_seq_len, H_q, scale,
         _desc(k_pool, k_scale, v_scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
@@ -390,13 +418,13 @@ def wf_keep_accepted(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted
                      dev_status=None, stream=None, k_scale=1.0, v_scale=1.0):
     """Move the rows of each request's accepted drafts (accepted [B, depth] int32, num_accepted [B] int32) to the front
     of its drafts in both pools; new_seq_lens [B] int32 receives the kept lengths."""
-    _contig(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted, num_accepted, new_seq_lens)
+    _dense(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted, num_accepted, new_seq_lens)
     B, M = block_tables.shape
     paths, depth = accepted.shape
     if paths != B or num_accepted.shape[0] != B or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or \
             v_pool.shape != k_pool.shape or (new_seq_lens is not None and new_seq_lens.shape[0] != B):
         raise ValueError("accepted [B, depth], num_accepted, seq_lens and new_seq_lens [B], cu_q_lens [B + 1]")
-    rc = load().wf_keep_accepted(
+    rc = (_lib or load()).wf_keep_accepted(
         k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), M, seq_lens.data_ptr(), cu_q_lens.data_ptr(),
         accepted.data_ptr(), depth, num_accepted.data_ptr(), _ptr(new_seq_lens), B, _desc(k_pool, k_scale, v_scale),
         _ptr(dev_status), _stream(stream))

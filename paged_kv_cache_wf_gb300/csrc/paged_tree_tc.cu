@@ -553,26 +553,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 }
                             }
                         } else {
-                        constexpr int kBatch = 2;
+                            constexpr int kBatch = 2;
 #pragma unroll 1
-                        for (int y0 = fw; y0 < kRounds; y0 += kFin * kBatch) {
-                            uint4 c[kBatch];
+                            for (int y0 = fw; y0 < kRounds; y0 += kFin * kBatch) {
+                                uint4 c[kBatch];
 #pragma unroll
-                            for (int k = 0; k < kBatch; ++k) {
-                                const int y = y0 + k * kFin;
-                                c[k] = make_uint4(0u, 0u, 0u, 0u);
-                                if (y < kRounds && live(y)) c[k] = ld_shared_v4(src + y * kStep * D);
-                            }
+                                for (int k = 0; k < kBatch; ++k) {
+                                    const int y = y0 + k * kFin;
+                                    c[k] = make_uint4(0u, 0u, 0u, 0u);
+                                    if (y < kRounds && live(y)) c[k] = ld_shared_v4(src + y * kStep * D);
+                                }
 #pragma unroll
-                            for (int k = 0; k < kBatch; ++k) {
-                                const int y = y0 + k * kFin;
-                                if (y >= kRounds) break;
-                                uint32_t v[8];
-                                e4m3x16_to_f16(c[k], v);
-                                if (kStep * y + rr >= r0) nan |= nan_codes(c[k]);
-                                *reinterpret_cast<uint4*>(out_at(y, o0)) = make_uint4(v[0], v[1], v[2], v[3]);
-                                *reinterpret_cast<uint4*>(out_at(y, o1)) = make_uint4(v[4], v[5], v[6], v[7]);
-                            }
+                                for (int k = 0; k < kBatch; ++k) {
+                                    const int y = y0 + k * kFin;
+                                    if (y >= kRounds) break;
+                                    uint32_t v[8];
+                                    e4m3x16_to_f16(c[k], v);
+                                    if (kStep * y + rr >= r0) nan |= nan_codes(c[k]);
+                                    *reinterpret_cast<uint4*>(out_at(y, o0)) = make_uint4(v[0], v[1], v[2], v[3]);
+                                    *reinterpret_cast<uint4*>(out_at(y, o1)) = make_uint4(v[4], v[5], v[6], v[7]);
+                                }
                         }
                         }
                         if (__any_sync(0xffffffffu, nan != 0)) {
