@@ -225,19 +225,32 @@ def pool_desc(k_pool, k_scale=1.0, v_scale=1.0) -> wf_pool_desc:
     return d
 
 
-_descs = {}   # descriptors by pool geometry and per-tensor scales
+_descs = {}   # descriptors by pool geometry and the values of the scales
+
+
+def _scale_key(scale):
+    """A scale's value (per-head: values), None for what is not plain numbers."""
+    kind = type(scale)
+    if kind is float or kind is int:
+        return scale
+    if kind is list or kind is tuple:
+        for x in scale:
+            if type(x) is not float:
+                return None
+        return tuple(scale)
+    return None
 
 
 def _desc(k_pool, k_scale, v_scale):
-    """pool_desc, made once for each geometry and pair of per-tensor scales."""
-    try:
-        key = (k_pool.shape, k_pool.dtype, k_scale, v_scale)
-        d = _descs.get(key)
-    except TypeError:      # per-head scales (lists, arrays): made anew
+    """pool_desc, made once for each geometry and values of the scales."""
+    ks, vs = _scale_key(k_scale), _scale_key(v_scale)
+    if ks is None or vs is None:
         return pool_desc(k_pool, k_scale, v_scale)
+    key = (k_pool.shape, k_pool.dtype, ks, vs)
+    d = _descs.get(key)
     if d is None:
         d = pool_desc(k_pool, k_scale, v_scale)
-        if isinstance(k_scale, (int, float)) and isinstance(v_scale, (int, float)) and len(_descs) < 1024:
+        if len(_descs) < 1024:
             _descs[key] = d
     return d
 

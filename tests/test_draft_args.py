@@ -164,3 +164,23 @@ def test_binding_refuses_what_the_abi_cannot_see(lib):
         wf.wf_keep_accepted(pool, pool.clone(), bt, lens, cu, torch.zeros(2, 3, dtype=torch.int32), lens, stream=0)
     with pytest.raises(ValueError):
         wf.wf_keep_accepted(pool, pool.clone(), bt, lens, lens, torch.zeros(1, 3, dtype=torch.int32), lens, stream=0)
+
+
+def test_descriptors_follow_the_values_of_the_scales(lib):
+    import numpy as np
+    import torch
+    pool = torch.zeros(4, 16, 2, 64, dtype=torch.uint8)
+    scales = [0.5, 0.25]
+    d = wf._desc(pool, scales, 1.0)
+    assert wf._desc(pool, [0.5, 0.25], 1.0) is d and wf._desc(pool, (0.5, 0.25), 1.0) is d
+    scales[1] = 0.125          # the same list, other values
+    e = wf._desc(pool, scales, 1.0)
+    assert e is not d and [e.k_head_scales[h] for h in range(2)] == [0.5, 0.125]
+    assert [d.k_head_scales[h] for h in range(2)] == [0.5, 0.25]
+    assert wf._desc(pool, 1.0, scales) is not e
+    for other in (np.array([0.5, 0.25]), torch.tensor([0.5, 0.25]), [torch.tensor(0.5), torch.tensor(0.25)]):
+        x = wf._desc(pool, other, 1.0)
+        assert x is not d and [x.k_head_scales[h] for h in range(2)] == [0.5, 0.25]
+    with pytest.raises(ValueError):
+        wf._desc(pool, [0.5, 0.25, 0.5], 1.0)
+    assert wf._desc(torch.zeros(5, 16, 2, 64, dtype=torch.uint8), [0.5, 0.25], 1.0).num_blocks == 5
