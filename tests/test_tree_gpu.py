@@ -65,6 +65,11 @@ CASES = {
     "blocks of 7, 16 rows": T([64, 130], [5, 3], 6, 2, 128, 7, "bf16", seed=56),
     "fp8 blocks of 7, 8 rows": T([64, 130], [1, 1], 16, 2, 128, 7, "fp8", seed=57, **FP8),
     "fp8 blocks of 7, 16 rows": T([64, 130, 0], [2, 1, 2], 8, 1, 64, 7, "fp8", seed=58, **FP8),
+    "blocks of 24, 16 rows": T([64, 130, 3], [5, 8, 2], 8, 4, 64, 24, "bf16", seed=75),
+    "blocks of 1000, 8 rows d128": T([1400, 130], [2, 2], 8, 2, 128, 1000, "bf16", seed=76),
+    "fp8 blocks of 9, 8 rows": T([64, 130, 0], [3, 8, 1], 3, 3, 64, 9, "fp8", seed=77, **FP8),
+    "fp8 blocks of 9, 16 rows d128": T([64, 130, 0], [3, 2, 1], 10, 2, 128, 9, "fp8", seed=78, **FP8),
+    "fp8 blocks of 9, d128": T([64, 130, 0], [13, 20, 1], 14, 2, 128, 9, "fp8", seed=79, **FP8),
     # fp8
     "fp8": T([64, 300, 1], [7, 33, 5], 8, 2, 128, 16, "fp8", seed=31, **FP8),
     "fp8 d64": T([64, 300, 0], [7, 70, 30], 8, 2, 64, 16, "fp8", seed=32, **FP8),
