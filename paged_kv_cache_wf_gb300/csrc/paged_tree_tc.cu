@@ -39,7 +39,7 @@
 // the row up to 2^-10 (a 2^-17 part of its largest value).  The row's power of two and
 // the K scale go into the exponent's factor.  V codes are widened to fp16, which is exact
 // and which the hardware converts two at a time, by the finishing warps, into the ring
-// that P V reads, and the weights (at most 2^8, see kLazyMax) are rounded to fp16, whose
+// that P V reads, and the weights (2^7 of them, see kCodesUp) are rounded to fp16, whose
 // step is an eighth of bf16's; the V scale multiplies the outputs.  To bf16 there is no
 // conversion, and shifting and scaling the codes there took the call from 94 us (V not
 // widened) to 135 us, batch of 64.  Widening K too would cost twice the finishing warps'
@@ -58,6 +58,11 @@ namespace {
 constexpr int TM = 128;           // rows of a query tile (TMEM lanes)
 constexpr int TN = 128;           // positions of a tile
 constexpr float kLazyMax = 8.f;   // rescale O only when a row's maximum grows by more than 2^8
+// fp16 weights (fp8 pools) carry a factor of 2^7, which the sum has too: up to 2^15 of fp16's
+// 2^16.  A weight below 2^-21 of the row's largest loses bits, one below 2^-32 is 0 (without the
+// factor 2^-14 and 2^-25, which a long tail of small weights would feel).
+constexpr float kCodesUp = 7.f;
+static_assert(kLazyMax + kCodesUp <= 15.f, "fp16 weights overflow");
 constexpr int kSoftW = 8, kKW = 8, kVW = 9, kWalkW = 10, kMmaW = 11, kFinW = 13, kFin = 3;
 constexpr int kTcThreads = (kFinW + kFin) * 32;
 constexpr int kSoftRegs = 192, kOtherRegs = 64;
@@ -870,7 +875,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     l_run *= alpha;
                     const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
                     const float2 sc2 = make_float2(scale, scale);
-                    const float2 nm2 = make_float2(-m_use, -m_use);
+                    const float up = CODES ? kCodesUp - m_use : -m_use;
+                    const float2 nm2 = make_float2(up, up);
                     float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                     make_float2(0.f, 0.f)};
                     // the weights of positions 0-63 take columns 0-31, those of 64-127 columns 64-95

@@ -121,6 +121,9 @@ class Tree:
                     W[t, g] = w @ np.abs(v)
                     S[t, g] = (np.abs(k) @ np.abs(q[t, g])).max() * abs(self.scale)
                     if self.pool == "fp8" and self.kernel() == wf.WF_KERNEL_TENSOR_CORES:
+                        # weights go there as fp16, 2^7 of them: below fp16's smallest normal number the half
+                        # step is 2^-25, so 2^-32 of a sum that is at least 1; `bound` multiplies W by 2^-8 or more
+                        W[t, g] += np.abs(v).sum(0) * 2.0 ** -24
                         # q goes to the tensor cores as two e4m3 parts: off by at most 2^-17 of the row's largest
                         # element in each; `bound` multiplies S by (D + 4) 2^-24
                         S[t, g] += np.abs(k).sum(-1).max() * np.abs(q[t, g]).max() * abs(self.scale) * 2.0 ** 7 / (self.D + 4)

@@ -316,3 +316,20 @@ def test_negative_and_zero_scale():
             t.scale = scale
             d = t.device()
             R.check(t, t.run(d, t.workspace()))
+
+
+@pytest.mark.parametrize("pool,D,P", [("bf16", 128, 16), ("bf16", 64, 7), ("fp8", 128, 16), ("fp8", 64, 16), ("fp8", 64, 7),
+                                      ("f32", 64, 16)])
+def test_a_long_tail_of_small_weights(pool, D, P):
+    """One position of weight 1 whose values are 0 and 900 of 2^-26: the outputs are the tail's."""
+    t = R.Tree([900], [3], 8, 2, D, P, pool, seed=80, **(FP8 if pool == "fp8" else {}))
+    r = np.random.default_rng(81)
+    own = torch.from_numpy(t.table[0].astype(np.int64))
+    spike = R.to_pool(np.array([1.0 / t.ks]), pool)[0]
+    t.k[own], t.v[own] = 0, R.to_pool(2.0 / t.vs * r.random((len(own), P, 2, D)), pool)
+    t.k[own[0], 0, :, 0], t.v[own[0], 0] = spike, 0
+    t.q[:], t.scale = 0, 1.0
+    t.q[..., 0] = 18.0            # 18 log2(e) = 25.97
+    d = t.device()
+    R.check(t, t.run(d, t.workspace()))
+    assert float(d["out"].float().abs().min()) > 2.0 ** -18
