@@ -117,3 +117,39 @@ def test_the_first_call_of_a_process_is_captured(pool):
     r = subprocess.run([sys.executable, "-c", FIRST % (pool, ", k_scale=1/64, v_scale=1/64" if pool == "fp8" else "")],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("pool,D", [("bf16", 128), ("bf16", 64), ("fp8", 64)])
+def test_beside_a_prefill_and_a_decode(pool, D):
+    """Tree attention on one stream while prefills and decodes, tensor memory users too, run on two others."""
+    fp8 = dict(k_scale=1 / 64, v_scale=1 / 64) if pool == "fp8" else {}
+    r = np.random.default_rng(82)
+    t = R.Tree(r.integers(100, 900, 24), r.integers(1, 13, 24), 8, 2, D, 16, pool, seed=83, **fp8)
+    o = R.Tree([700, 0, 300, 90], [100, 64, 7, 200], 8, 2, D, 16, "bf16", seed=84)
+    d, ws, e = t.device(), t.workspace(), o.device()
+    q1 = e["q"][:4].contiguous()
+    wsd = torch.empty(max(1, wf.wf_paged_decode_workspace_size(4, 8, o.max_len, wf.pool_desc(e["k"]))), dtype=torch.uint8,
+                      device="cuda")
+    dec = torch.zeros_like(q1)
+
+    def prefill(stream=None):
+        wf.wf_paged_prefill(e["out"], e["q"], e["k"], e["v"], e["table"], e["lens"], e["cu"], o.max_q, o.max_len, o.scale,
+                            e["status"], stream=stream)
+
+    def decode(stream=None):
+        wf.wf_paged_decode(dec, q1, e["k"], e["v"], e["table"], e["lens"], o.max_len, o.scale, wsd, e["status"],
+                           stream=stream)
+
+    prefill()
+    decode()
+    first = t.run(d, ws).clone(), e["out"].clone(), dec.clone()
+    torch.cuda.synchronize()
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    for _ in range(20):
+        t.run(d, ws, stream=a)
+        prefill(b)
+        decode(c)
+    torch.cuda.synchronize()
+    for x, y in zip(first, (d["out"], e["out"], dec)):
+        assert torch.equal(x, y)
+    assert wf.wf_device_status_fetch(d["status"]) == wf.wf_device_status_fetch(e["status"]) == 0
