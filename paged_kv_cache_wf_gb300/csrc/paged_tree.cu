@@ -6,9 +6,6 @@
 // 0 .. c_b - 1 (ember, "The core idea": position p lives in block table[p / P] at
 // p % P) and the drafts c_b + j that its mask names; o = softmax(scale q K^T) V over
 // them, with the running maximum and sum of an online softmax in fp32 (exp2 domain).
-#include <cfloat>
-#include <cmath>
-
 #include "paged_tree.cuh"
 
 namespace wf {
@@ -573,10 +570,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint3
     p.tokb = s.tokb;
     p.ucost = s.ucost;
     p.q_inv = nullptr;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    // a masked score is -inf before it is scaled: a scale of 0 (equal weights) stands as the
-    // smallest normal number, which leaves every finite score a weight of 2^0
-    if (fabsf(p.scale_log2) < FLT_MIN) p.scale_log2 = copysignf(FLT_MIN, p.scale_log2);
+    p.scale_log2 = tree_factor(a.scale * 1.4426950408889634f);
     const bool d128 = pool.head_dim == 128;
     if (tree_tc_supported(pool, a.num_q_heads)) {
         void* prep = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(p.ws_rec + cap) + 127) & ~(uintptr_t)127);

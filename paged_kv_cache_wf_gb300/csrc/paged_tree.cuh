@@ -15,6 +15,9 @@
 // positions: at 64 drafts of 4 heads that is as many bytes as the K and V they read.
 #pragma once
 
+#include <cfloat>
+#include <cmath>
+
 #include "wf_internal.h"
 
 namespace wf {
@@ -41,6 +44,11 @@ struct TreeParams {
     float scale_log2;
     const float* q_inv;   // fp8 pools on the tensor cores: factors of the prepared q rows
 };
+
+// A factor of the scores, held at fp32's smallest normal number or above (its sign kept): a
+// masked score is -inf before it is scaled, and -inf * 0 is NaN.  At that factor every finite score
+// has a weight of 2^0, as it has at 0.
+__host__ __device__ __forceinline__ float tree_factor(float f) { return copysignf(fmaxf(fabsf(f), FLT_MIN), f); }
 
 // Rows of a row block, drafts in it, tile and CTAs an SM of the kernel that runs a call.
 struct TreeShape {

@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (i == 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // the q rows' factors
                 const int hs = min(it.h, kMaxScaleHeads - 1);
                 const int64_t row = ((int64_t)it.b * p.max_q_len + it.tok0 + tok) * p.H_q + it.h * p.G + r % p.G;
-                scale = p.scale_log2 * sc.k[hs] * (row_valid ? __ldcg(p.q_inv + row) : 1.f);
+                scale = tree_factor(p.scale_log2 * sc.k[hs] * (row_valid ? __ldcg(p.q_inv + row) : 1.f));
                 v_scale = sc.v[hs];
             }
             float m_ref = -INFINITY, l_run = 0.f;
