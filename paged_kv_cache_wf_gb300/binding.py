@@ -262,7 +262,7 @@ def _types():
     """torch's dtypes, looked up once."""
     global _known_types
     import torch
-    _known_types = (torch.bfloat16, torch.uint8, torch.float32, torch.int32, torch.int64)
+    _known_types = (torch.bfloat16, torch.uint8, torch.float32, torch.int32, torch.int64, torch.uint32)
     return _known_types
 
 
@@ -299,7 +299,7 @@ def wf_qk_norm_rope_and_cache(q_out, q, k, v, q_weight, k_weight, eps: float, co
     """Norm (q_weight, k_weight [D] or None) and rotate q [T, H_q, D] and k [T, H_kv, D] (cos_sin [positions, rotary_dim]
     float32 or None, positions [T] int32), write q_out [T, H_q, D] and scatter the new k and v rows into the pools.
     q, k and v may be strided over tokens (views of one fused projection)."""
-    bf16, u8, f32, i32, i64 = _known_types or _types()
+    bf16, u8, f32, i32, i64, _ = _known_types or _types()
     _dense(q_out, q_weight, k_weight, cos_sin, positions, k_pool, v_pool, slot_mapping)
     T, H_q, D = q.shape
     _, _, H_kv, pool_D = k_pool.shape
@@ -407,17 +407,21 @@ def wf_paged_tree_decode(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_le
                          max_seq_len: int, scale: float, workspace, dev_status=None, stream=None, k_scale=1.0,
                          v_scale=1.0):
     """out, q [T_total, H_q, D] packed drafts; cu_q_lens [B+1] int32; seq_lens [B] int32 count the drafts; tree_mask
-    [T_total, words] int32 (bit j of a row: draft j of its request is seen); workspace uint8 tensor."""
+    [T_total, words] int32 or uint32 (bit j of a row: draft j of its request is seen); workspace uint8 tensor."""
+    bf16, u8, _, i32, _, u32 = _known_types or _types()
     _dense(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, tree_mask)
     T, H_q, D = q.shape
     B, M = block_tables.shape
     rows, words = tree_mask.shape
-    if out.shape != q.shape or out.dtype is not q.dtype or D != k_pool.shape[3] or \
-            q.element_size() != max(2, k_pool.element_size()) or v_pool.shape != k_pool.shape or \
-            v_pool.dtype is not k_pool.dtype:
+    dt, pool_dt = q.dtype, k_pool.dtype
+    if out.shape != q.shape or out.dtype is not dt or D != k_pool.shape[3] or \
+            dt is not (bf16 if pool_dt is u8 else pool_dt) or v_pool.shape != k_pool.shape or v_pool.dtype is not pool_dt:
         raise ValueError("out is like q [T, H_q, D] of the pool's dtype (bf16 for fp8 pools) and head size")
-    if rows != T or tree_mask.element_size() != 4 or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1:
-        raise ValueError("tree_mask is [T, words] of 32-bit words, block_tables [B, M], seq_lens [B], cu_q_lens [B + 1]")
+    if rows != T or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or block_tables.dtype is not i32 or \
+            seq_lens.dtype is not i32 or cu_q_lens.dtype is not i32 or \
+            (tree_mask.dtype is not i32 and tree_mask.dtype is not u32):
+        raise ValueError("tree_mask is [T, words] of 32-bit words, block_tables [B, M], seq_lens [B] and cu_q_lens [B + 1] "
+                         "are int32")
     rc = (_lib or load()).wf_paged_tree_decode(
         out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), M,
         seq_lens.data_ptr(), cu_q_lens.data_ptr(), tree_mask.data_ptr(), words, B, T, max_q_len, max_seq_len, H_q, scale,
