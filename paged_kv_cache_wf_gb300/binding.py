@@ -435,12 +435,18 @@ def wf_keep_accepted(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted
                      dev_status=None, stream=None, k_scale=1.0, v_scale=1.0):
     """Move the rows of each request's accepted drafts (accepted [B, depth] int32, num_accepted [B] int32) to the front
     of its drafts in both pools; new_seq_lens [B] int32 receives the kept lengths."""
+    _, _, _, i32, _, _ = _known_types or _types()
     _dense(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted, num_accepted, new_seq_lens)
     B, M = block_tables.shape
     paths, depth = accepted.shape
+    if v_pool.shape != k_pool.shape or v_pool.dtype is not k_pool.dtype:
+        raise ValueError("the pools are alike")
     if paths != B or num_accepted.shape[0] != B or seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or \
-            v_pool.shape != k_pool.shape or (new_seq_lens is not None and new_seq_lens.shape[0] != B):
-        raise ValueError("accepted [B, depth], num_accepted, seq_lens and new_seq_lens [B], cu_q_lens [B + 1]")
+            block_tables.dtype is not i32 or seq_lens.dtype is not i32 or cu_q_lens.dtype is not i32 or \
+            accepted.dtype is not i32 or num_accepted.dtype is not i32 or \
+            (new_seq_lens is not None and (new_seq_lens.shape[0] != B or new_seq_lens.dtype is not i32)):
+        raise ValueError("block_tables [B, M], accepted [B, depth], num_accepted, seq_lens and new_seq_lens [B] and "
+                         "cu_q_lens [B + 1] are int32")
     rc = (_lib or load()).wf_keep_accepted(
         k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), M, seq_lens.data_ptr(), cu_q_lens.data_ptr(),
         accepted.data_ptr(), depth, num_accepted.data_ptr(), _ptr(new_seq_lens), B, _desc(k_pool, k_scale, v_scale),
