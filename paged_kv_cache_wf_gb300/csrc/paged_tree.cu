@@ -79,6 +79,7 @@ __device__ __forceinline__ void cc_row(float (&f)[VPL], const float* from) {
 
 // CTAs an SM: as many as the registers that the next tile and the rows take leave room for.
 constexpr int cc_ctas_per_sm(int bytes, int D, int rpw) { return bytes == 4 && D == 128 && rpw == 4 ? 1 : 2; }
+static_assert(cc_ctas_per_sm(2, 64, 1) * kTreeMaxSms <= kTreeRecs, "records for every CTA");
 
 // Rows of a warp: the fewest that hold all rows of a request's drafts under a KV head, 4 at most
 // (64-wide fp32 heads: 8 rows 13.6 us with 1, 14.9 with 2; 14 rows 53 us with 2, 73 with 4).
@@ -528,7 +529,7 @@ size_t tree_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, i
     if (B < 0 || max_q_len < 0 || max_seq_len < 0 || !tree_shape(pool, num_q_heads, max_q_len, &s)) return 0;
     const int64_t ctas = tree_ctas(s, B, pool.num_kv_heads, max_q_len, max_seq_len);
     const int64_t rows = 2 * ctas * s.rows;
-    const size_t bytes = (size_t)(256 + ctas * (int64_t)sizeof(int4) + rows * 8 + rows * pool.head_dim * 4);
+    const size_t bytes = (size_t)(256 + kTreeRecs * (int64_t)sizeof(int4) + rows * 8 + rows * pool.head_dim * 4);
     if (pool.dtype != WF_DTYPE_FP8_E4M3 || !tree_tc_supported(pool, num_q_heads)) return bytes;
     const size_t prep = tree_tc_prep_bytes(B, num_q_heads, max_q_len, pool);
     return prep == SIZE_MAX ? 0 : bytes + prep;
@@ -573,7 +574,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint3
     p.scale_log2 = tree_factor(a.scale * 1.4426950408889634f);
     const bool d128 = pool.head_dim == 128;
     if (tree_tc_supported(pool, a.num_q_heads)) {
-        void* prep = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(p.ws_rec + cap) + 127) & ~(uintptr_t)127);
+        void* prep = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(p.ws_rec + kTreeRecs) + 127) & ~(uintptr_t)127);
         const cudaError_t e = launch_tree_tc(p, pool, prep, ctas, stream);
         if (e != cudaSuccess || ctas == 1) return e;
         return d128 ? launch_join<BF16, 128>(p, ctas, stream) : launch_join<BF16, 64>(p, ctas, stream);

@@ -34,7 +34,7 @@ struct TreeParams {
     uint32_t* dev_status;
     float* ws_o;     // [2 * CTAs][row block] rows of D
     float2* ws_ml;   // [2 * CTAs][row block]
-    // [CTAs]: the cut unit that starts in this CTA: {its first draft's row of q, KV head, last CTA
+    // [kTreeRecs], a CTA each: the cut unit that starts in this CTA: {its first draft's row of q, KV head, last CTA
     // with a piece of it, rows (0: there is no such unit)}
     int4* ws_rec;
     int32_t M, B, total_q, max_q_len, max_seq_len, H_q, H_kv, G, N, P, W;
@@ -64,6 +64,9 @@ cudaError_t launch_tree_tc(const TreeParams& p, const wf_pool_desc& pool, void* 
 namespace {
 
 constexpr int kTreeMaxSms = 160;    // SMs a launch may use (the workspace holds their CTAs' pieces)
+// Records in the workspace: of the most CTAs any kernel uses, not of this call's, so that more
+// drafts never need less (beyond 16 rows the fp32 kernel has half the CTAs, each with twice the rows).
+constexpr int kTreeRecs = 2 * kTreeMaxSms;
 
 // A request's drafts and length, n = 0 for one that fails the checks.
 struct TreeReq {
