@@ -77,15 +77,6 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// mbar_wait in a rolled loop: unrolled, this kernel's waits take 50 KB of its instruction
-// cache.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
-#pragma unroll 1
-    for (uint32_t i = 0; i < (1u << 21); ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return false;
-}
-
 // A piece as the warps read it; nt = 0 ends the list.
 constexpr int kRing = 8;
 struct PieceRec {
@@ -332,8 +323,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile unsigned char* okm_of = smem + L::okm;
     // the record of piece i, when it is there: false ends a warp's loop
     auto piece = [&](int i) -> bool {
-        if (misc[1]) return false;
-        if (!bar_wait(&piece_full[i % kRing], (i / kRing) & 1)) {
+        if (__any_sync(0xffffffffu, misc[1] != 0)) return false;
+        if (!mbar_wait_warp(&piece_full[i % kRing], (i / kRing) & 1)) {
             if (lane == 0) fail();
             return false;
         }
@@ -371,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int blk = blk_next;
                     const bool in = lane < 8 && real > 0 && pos < kend;
                     if (real > 1 && lane < 8 && pos + TN < kend) blk_next = __ldg(trow + (pos + TN) / p.P);
-                    if (!bar_wait(&empty[x], par)) {
+                    if (!mbar_wait_warp(&empty[x], par)) {
                         if (lane == 0) fail();
                         ok = false;
                         break;
@@ -410,7 +401,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int made = 0, asked = 0, second = 0;   // records, pieces whose tiles are asked for, second tiles
             int t = 0;
             uint32_t idle = 0;
-            while (!misc[1] && (more || asked < made)) {
+            while ((more || asked < made) && !__any_sync(0xffffffffu, misc[1] != 0)) {
                 bool did = false;
                 if (more && (made < kRing || __shfl_sync(0xffffffffu, (int)mbar_test(&piece_empty[made % kRing],
                                                                                       (made / kRing - 1) & 1), 0))) {
@@ -491,8 +482,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int j = it.j0, end = j + ring_tiles(j1 - j); j < end; ++j) {
                     const int k0 = j * TN;
-                    if (CODES ? !bar_wait(&raw_full[rx], rpar) || !bar_wait(&v_empty[x], par ^ 1)
-                              : !bar_wait(&v_full[x], par)) {
+                    if (CODES ? !mbar_wait_warp(&raw_full[rx], rpar) || !mbar_wait_warp(&v_empty[x], par ^ 1)
+                              : !mbar_wait_warp(&v_full[x], par)) {
                         if (lane == 0) fail();
                         ok = false;
                         break;
@@ -662,8 +653,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t qpar = 0, ppar = 0;
             bool ok = true;
             auto need = [&](uint64_t* bar, uint32_t par) {
-                // no lane may still be polling when one hands the barrier's slot on
-                if (ok && !__all_sync(0xffffffffu, bar_wait(bar, par))) {
+                // (of all lanes: none may still be polling when one hands the barrier's slot on)
+                if (ok && !mbar_wait_warp(bar, par)) {
                     if (lane == 0) fail();
                     ok = false;
                 }
@@ -803,7 +794,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) vis[w] = row_valid ? mask_bits(mrow, p.W, k0 + 32 * w - c, n) : 0u;
                 }
-                if (!bar_wait(s_full(t), (gs + u) & 1)) {
+                if (!mbar_wait_warp(s_full(t), (gs + u) & 1)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
@@ -858,7 +849,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         m_ref = mt;
                     }
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                        if (!bar_wait(pv_done(t), (gs + u - 1) & 1)) fail();
+                        if (!mbar_wait_warp(pv_done(t), (gs + u - 1) & 1)) fail();
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
@@ -900,7 +891,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 __syncwarp();
                 // the first P of a piece lets P V overwrite O, which the last piece's join reads
-                if (QT == 1 && u == 0 && i > 0 && !bar_wait(x_done, (i - 1) & 1)) {
+                if (QT == 1 && u == 0 && i > 0 && !mbar_wait_warp(x_done, (i - 1) & 1)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
@@ -909,7 +900,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok) break;
             // ---- epilogue: the rows, or this piece of them ------------------------------
-            if (nt > 0 && !bar_wait(pv_done(t), (gs + nt - 1) & 1)) {
+            if (nt > 0 && !mbar_wait_warp(pv_done(t), (gs + nt - 1) & 1)) {
                 if (lane == 0) fail();
                 break;
             }
@@ -919,7 +910,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float w0 = 1.f, w1 = 0.f;                     // weights of the streams' O (QT = 1)
             const float2* ml = reinterpret_cast<const float2*>(smem + L::ml);
             if constexpr (QT == 1) {
-                if (nt == 0 && i > 0 && !bar_wait(x_done, (i - 1) & 1)) {
+                if (nt == 0 && i > 0 && !mbar_wait_warp(x_done, (i - 1) & 1)) {
                     if (lane == 0) fail();
                     break;
                 }
@@ -927,7 +918,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(x_ready);
-                if (!bar_wait(x_ready, i & 1)) {
+                if (!mbar_wait_warp(x_ready, i & 1)) {
                     if (lane == 0) fail();
                     break;
                 }

@@ -269,6 +269,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     return false;
 }
 
+// The same for a whole warp, in a rolled loop (unrolled, the waits of a kernel that has many
+// take 50 KB of its instruction cache).  Lanes poll by themselves, and at the limit some might
+// see the phase and others not: the warp gives up when one of its lanes does, so that it stays
+// together for what needs all of its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit = (1u << 21)) {
+    bool ok = false;
+#pragma unroll 1
+    for (uint32_t i = 0; i < limit; ++i)
+        if ((ok = mbar_try_wait(bar, parity))) break;
+    return __all_sync(0xffffffffu, ok);
+}
+
 // One contiguous global -> shared copy on the bulk-copy (TMA) engine, completing
 // `bytes` of transaction count on `bar`.  dst, src 16-byte aligned; bytes % 16 == 0.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
