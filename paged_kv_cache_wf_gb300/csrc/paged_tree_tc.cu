@@ -113,8 +113,8 @@ struct TtLayout {
     static constexpr int bars = ml + (QT == 1 ? 2 * TM * 8 : 0);
     // q_full[QT], q_empty[QT], k_full[KS], k_empty[KS], v_full[VS] (CODES: not used), v_empty[VS], v_ready[VS],
     // raw_full[RS], raw_empty[RS], per stream s_full, p_full, pv_done, then x_ready, x_done and
-    // piece_full[kRing], piece_empty[kRing]
-    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing;
+    // piece_full[kRing], piece_empty[kRing], per stream mma_end
+    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing + 2;
     static constexpr int ring = bars + nbars * 8;        // [kRing] records of pieces
     static constexpr int start = (ring + kRing * (int)sizeof(PieceRec) + 15) / 16 * 16;
     static constexpr int scratch = start + (int)sizeof(TreeStart);
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t* x_done = x_ready + 1;
     uint64_t* piece_full = x_done + 1;
     uint64_t* piece_empty = piece_full + kRing;
+    uint64_t* mma_end = piece_empty + kRing;
     PieceRec* ring = reinterpret_cast<PieceRec*>(smem + L::ring);
     TreeStart* st = reinterpret_cast<TreeStart*>(smem + L::start);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::misc);
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(s_full(t), 1);
             mbar_init(p_full(t), 4);
             mbar_init(pv_done(t), 1);
+            mbar_init(&mma_end[t], 1);
         }
         mbar_init(x_ready, kSoftW);
         mbar_init(x_done, kSoftW);
@@ -391,6 +393,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 piece_done(i);
             }
+            if (!mbar_drain_ring(full, nslots, g) && lane == 0) fail();   // see the end of the kernel
         } else if (warp == kWalkW) {
             // ============================= walk, query tiles =============================
             // publishes records as far ahead as the ring allows and loads each piece's query
@@ -468,6 +471,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __nanosleep(64);
                 }
             }
+            bool landed = mbar_drain_warp(&q_full[0], asked + t);
+            if constexpr (QT == 2) landed &= mbar_drain_warp(&q_full[1], second);
+            if (!landed && lane == 0) fail();
         } else if (warp >= kFinW) {
             // ============================= V finish ======================================
             // a third of a tile's rows each, dealt in turn
@@ -747,6 +753,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 piece_done(i);
             }
+            if (elect_one()) tc::commit(&mma_end[t]);
+            if (!mbar_drain_warp(&mma_end[t], 1) && lane == 0) fail();
         }
     } else {
         // ============================= softmax =======================================
@@ -1046,6 +1054,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (threadIdx.x == 0) p.ws_rec[cta] = rec;
     }
 
+    // Every role has waited (within a limit) for the copies and products it issued, also where it
+    // gave up on another's: none reaches this CTA's shared or tensor memory after it is gone.
     tc::fence_before_sync();
     __syncthreads();
     if (threadIdx.x == 0 && misc[1]) report(p.dev_status, WF_DEV_TIMEOUT);

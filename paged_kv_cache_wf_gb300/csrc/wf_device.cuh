@@ -281,6 +281,19 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
     return __all_sync(0xffffffffu, ok);
 }
 
+// Bounded wait, of a whole warp, until a barrier that was given `uses` phases has completed the last.
+__device__ __forceinline__ bool mbar_drain_warp(uint64_t* bar, int uses, uint32_t limit = (1u << 21)) {
+    return uses == 0 || mbar_wait_warp(bar, (uint32_t)(uses - 1) & 1u, limit);
+}
+
+// The same for a ring of `slots` barriers of which `uses` phases were given out in turn.
+__device__ __forceinline__ bool mbar_drain_ring(uint64_t* bars, int slots, int uses, uint32_t limit = (1u << 21)) {
+    bool ok = true;
+#pragma unroll 1
+    for (int s = 0; s < slots; ++s) ok &= mbar_drain_warp(bars + s, (uses + slots - 1 - s) / slots, limit);
+    return ok;
+}
+
 // One contiguous global -> shared copy on the bulk-copy (TMA) engine, completing
 // `bytes` of transaction count on `bar`.  dst, src 16-byte aligned; bytes % 16 == 0.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar,

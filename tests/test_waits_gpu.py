@@ -27,3 +27,13 @@ def test_a_warp_gives_up_together(waits, split):
     assert waits.part_ways(split, ctypes.c_void_p(out.data_ptr())) == 0
     torch.cuda.synchronize()
     assert out.tolist() == [1 if split == 32 else 0] * 32
+
+
+@pytest.mark.parametrize("slots", [1, 2, 5, 6])
+@pytest.mark.parametrize("uses", [0, 1, 2, 3, 4, 6, 7, 11, 12, 13])
+def test_a_drain_waits_for_the_last_phases(waits, slots, uses):
+    out = torch.full((32,), -1, dtype=torch.int32, device="cuda")
+    for missing in range(min(uses, slots) + 1):
+        assert waits.drain(slots, uses, missing, ctypes.c_void_p(out.data_ptr())) == 0
+        torch.cuda.synchronize()
+        assert out.tolist() == [1 if missing == 0 else 0] * 32
