@@ -316,6 +316,7 @@ size_t wf_paged_tree_decode_workspace_size(int32_t B, int32_t num_q_heads, int32
  *              j / 32 is set.  Bits of j >= n_b are ignored; a row's own bit is not
  *              implied.  mask_words >= ceil(max_q_len / 32).
  *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b], below 2^31 - 1024
+ *   scale      softmax scale; scale * log2(e) must be finite in float32
  *   workspace  device scratch of >= wf_paged_tree_decode_workspace_size(B, H_q,
  *              max_q_len, max_seq_len, pool) bytes, 16-byte aligned; needs no
  *              initialisation.  Calls that overlap in time must not share one.

@@ -377,7 +377,8 @@ wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, con
     // positions are 32-bit and looked at a tile past the end
     if (max_seq_len >= INT32_MAX - 1023) return WF_ERR_INVALID_ARG;
     if (mask_words < 0 || (int64_t)mask_words * 32 < max_q_len) return WF_ERR_INVALID_ARG;
-    if (!std::isfinite(scale)) return WF_ERR_INVALID_ARG;
+    // the kernels take scores to powers of two: an infinite factor would make a score of 0 NaN
+    if (!std::isfinite(scale * 1.4426950408889634f)) return WF_ERR_INVALID_ARG;
     if (B == 0 || total_q == 0 || max_q_len == 0) return WF_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !cu_q_lens || !tree_mask)
         return WF_ERR_INVALID_ARG;
