@@ -157,10 +157,13 @@ wf_status wf_reshape_and_cache(const void* k, const void* v, void* k_pool, void*
  * q, k, v and q_out have the pool's dtype (bfloat16 for fp8 pools).  Norm and rotation
  * are float32 and each result is rounded once, K straight to the pool's type: an fp8
  * code is e4m3(y * (1.0f / scale_h)) of the float32 y, which is not always the code
- * that wf_reshape_and_cache stores for a y rounded to bfloat16 first.
+ * that wf_reshape_and_cache stores for a y rounded to bfloat16 first.  The sum of squares
+ * is float32 too: head rows whose sum leaves its range (elements of 1e18 and more, or
+ * an eps of 0 beside elements of 1e-20 and less) are not normed rightly.
  * A token with a negative slot is padding: nothing is written for it, its q_out row
- * included, and its position is not looked at.  A token with a slot >= N*P (WF_DEV_BAD_SLOT) or a position out
- * of range (WF_DEV_BAD_POSITION) is skipped and flagged the same way.
+ * included, and its position is not looked at.  A token with a slot >= N*P
+ * (WF_DEV_BAD_SLOT) or a position out of range (WF_DEV_BAD_POSITION) is skipped and
+ * flagged the same way.
  * Any rotary_dim is taken; multiples of 16 read the table in 16-byte chunks.
  */
 wf_status wf_qk_norm_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -315,7 +318,11 @@ size_t wf_paged_tree_decode_workspace_size(int32_t B, int32_t num_q_heads, int32
  *              0 .. c_b - 1 and to every c_b + j, j < n_b, whose bit j % 32 of word
  *              j / 32 is set.  Bits of j >= n_b are ignored; a row's own bit is not
  *              implied.  mask_words >= ceil(max_q_len / 32).
- *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b], below 2^31 - 1024
+ *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b], below 2^31 - 1024.
+ *              max_q_len also decides how the rows of all requests are laid over the
+ *              GPU: the result is the same to rounding, but a max_q_len far above the
+ *              batch's drafts costs time (up to 16 drafts of 4 query heads a KV head:
+ *              34 us with 16, 38 with 64).
  *   scale      softmax scale; scale * log2(e) must be finite in float32
  *   workspace  device scratch of >= wf_paged_tree_decode_workspace_size(B, H_q,
  *              max_q_len, max_seq_len, pool) bytes, 16-byte aligned; needs no
@@ -354,7 +361,10 @@ wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, con
  * Row c_b + accepted[b][j] is copied to c_b + j, byte for byte, as if all rows were read
  * before any is written; rows behind the kept ones are left as they are.  K rows carry
  * the rotation of their position in the text (context + depth), which is the position
- * they move to.  The drafts' blocks must belong to one request each.
+ * they move to.  The drafts' blocks must belong to one request each.  (The block manager
+ * of wf_blocks.h has no call that shortens a sequence: it goes on counting all drafts
+ * that were appended.  A caller that verifies drafts keeps the lengths and the blocks of
+ * its drafts itself.)
  * A request whose lengths are out of range (WF_DEV_BAD_SEQLEN) or whose path is
  * (WF_DEV_BAD_NODE) is skipped whole, its new_seq_lens entry left unwritten; a row whose
  * source or target block id is out of range (WF_DEV_BAD_BLOCK) is not moved.

@@ -24,6 +24,9 @@
  *     last sequence holding it is freed.  Free blocks are handed out last-freed
  *     first.
  *   - A call that fails changes nothing.
+ *   - A sequence grows or is freed, it is never shortened: drafts that a verification
+ *     step rejects (wf_keep_accepted) would stay counted, so their slots and lengths
+ *     are kept by the caller.
  */
 #ifndef WF_BLOCKS_H
 #define WF_BLOCKS_H

@@ -16,9 +16,11 @@
 //           half of the columns.
 //   QT = 2  (up to 256 rows a unit): one 128-row query tile each, on the same tiles, so
 //           a loaded tile serves 256 rows.
-// Device time of a call, and of its bytes at the copy peak: 32 requests of 1-16 drafts 33.9
-// and 18.1 us, 118 of 33-61 drafts (QT = 2) 275 and 190 us, 64 of 3-13 drafts of 64-wide heads
-// 39.4 and 15.5 us, 64 of 8-24 drafts over fp8 103 and 37.0 us; one request of 8 drafts 10.9 us.
+// Device time of a call in a graph of many (issued one by one a call takes 1-2 us more, the widest
+// 10-15), and of its bytes at the copy peak: 32 requests of 1-16 drafts 34.2
+// and 18.1 us, 118 of 33-61 drafts (QT = 2) 272-280 and 190 us, 64 of 3-13 drafts of 64-wide heads
+// 40.4 and 15.5 us, 64 of 8-24 drafts over fp8 96.3 and 37.0 us (64-wide 73 and 18.5 us), 118 of
+// 33-61 drafts over fp8 409 and 118 us (64-wide 291 and 59 us); one request of 8 drafts 11.0 us.
 // What is left: 5 us from launch to the first product (division of the work, first block ids,
 // first tiles, cold code); 2-5 us around every piece's end, where its streams wait for one
 // another and O is joined; 2-10 us of the join; and with long pieces the chain S -> softmax ->
@@ -32,7 +34,7 @@
 // element of a draft's row that is not finite is zeroed too, and the epilogue adds it
 // to the rows that see the draft.  Only tiles that reach the drafts are looked at.
 //
-// fp8 pools (CODES; always QT = 1).  S takes the K codes as they are (e4m3 x e4m3 ->
+// fp8 pools (CODES; QT = 1, see tree_tc_shape).  S takes the K codes as they are (e4m3 x e4m3 ->
 // fp32): a small grid before this one splits every q row, scaled by a power of two so
 // that its largest magnitude lies in [128, 256), into hi = e4m3(q) and lo = e4m3(q - hi).
 // hi keeps four of a bf16 value's eight significant bits and lo the rest, so their sum is
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     *reinterpret_cast<uint4*>(out_at(y, o0)) = make_uint4(v[0], v[1], v[2], v[3]);
                                     *reinterpret_cast<uint4*>(out_at(y, o1)) = make_uint4(v[4], v[5], v[6], v[7]);
                                 }
-                        }
+                            }
                         }
                         if (__any_sync(0xffffffffu, nan != 0)) {
                             // a draft's NaN elements are set aside
@@ -1237,10 +1239,13 @@ bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads) {
     return (int64_t)pool.num_blocks * pool.block_size <= INT32_MAX && num_q_heads / pool.num_kv_heads <= 8;
 }
 
-// Units of at most 128 rows: two streams over the same rows (32 requests of up to 64 rows 33.9 us,
-// with two query tiles 38.9); else two query tiles (118 of up to 244 rows 277 us, with row
-// blocks of 128, each of which reads K and V, 397).  fp8 pools stay with 128 rows: the widened
-// V leaves no room for a second query tile.
+// Units of at most 128 rows: two streams over the same rows (32 requests of up to 64 rows 34.2 us,
+// with two query tiles 38.4); else two query tiles (118 of up to 244 rows 277 us, with row
+// blocks of 128, each of which reads K and V, 397).  The choice is the batch's, by max_q_len: in a
+// batch with two query tiles a request of at most 128 rows runs on one of the two streams (118
+// requests of 4-244 rows 267 us, 184 at the copy peak).  fp8 pools stay with row blocks of 128,
+// each of which reads K and V and widens V again (118 of up to 244 rows 409 us).  A second query
+// tile would leave room for two K slots instead of four; that form has not been built.
 TreeShape tree_tc_shape(int G, int max_q_len, bool codes) {
     const int tok = TM / G;
     const int qt = codes || max_q_len <= tok ? 1 : 2;

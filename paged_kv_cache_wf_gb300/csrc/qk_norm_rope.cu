@@ -20,6 +20,9 @@
 // of the warp; arithmetic is on pairs (two fp32 operations an instruction); an instance
 // without weights has no norm in it.  The sum of squares is a shuffle reduction over the
 // row's lanes.  A lane reads its cos and sin once for IT rows.
+// With norm weights the same 8193 tokens take 33.5 us (fp8 pools; without 30.5) and 34.5 us (bf16
+// pools, whose bytes take 30.3).  Rotation widths that are no multiple of 16 read each pair's other
+// half, cos and sin element by element: 75.7 us at a width of 120 for the 30.5.
 #include "wf_internal.h"
 
 namespace wf {
