@@ -153,7 +153,8 @@ wf_status wf_reshape_and_cache(const void* k, const void* v, void* k_pool, void*
  *                (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i), i < rotary_dim / 2.
  *                0: no rotation; cos_sin and positions are not read and may be NULL.
  *   interleaved  0: a, b are elements i and i + rotary_dim / 2; else 2i and 2i + 1
- *   k_pool, v_pool, slot_mapping, num_tokens: as for wf_reshape_and_cache
+ *   k_pool, v_pool, slot_mapping, num_tokens: as for wf_reshape_and_cache.  Two tokens
+ *                with the same slot: each 16 bytes there are one's or the other's.
  * q, k, v and q_out have the pool's dtype (bfloat16 for fp8 pools).  Norm and rotation
  * are float32 and each result is rounded once, K straight to the pool's type: an fp8
  * code is e4m3(y * (1.0f / scale_h)) of the float32 y, which is not always the code
