@@ -13,7 +13,13 @@
  *
  *   wf_qk_norm_rope_and_cache  per-head norms and rotation of q and k, and the scatter
  *   wf_paged_tree_decode       attention of every draft over the context and its ancestors
+ *   wf_verify_drafts           the accepted path, from the target's probabilities
  *   wf_keep_accepted           the accepted path's rows moved to the front of the drafts
+ *
+ * And a step's tables need not come from the host:
+ *
+ *   wf_build_step         block tables, slots, positions and offsets from the requests' lengths
+ *   wf_trim_blocks        the blocks of shortened or finished requests back to the free list
  *
  * Sources (page title, section):
  *   weft, "Shapes and symbols": B, H_q, H_kv (H_q / H_kv = GQA group), D, N, P, T_total.
@@ -84,6 +90,9 @@ typedef enum wf_dtype {
                                     skipped                                                 */
 #define WF_DEV_BAD_NODE    0x40u /* accepted path out of range or not increasing: request
                                     skipped                                                 */
+#define WF_DEV_NO_BLOCKS   0x80u /* building a step: fewer free blocks than it needs        */
+#define WF_DEV_BAD_PROBS   0x100u /* verification: a row whose probabilities have no positive,
+                                    finite sum, or a pick outside [0, 1)                    */
 
 /* One layer's pool geometry.  k_pool and v_pool are each [N, P, H_kv, D]. */
 typedef struct wf_pool_desc {
@@ -354,8 +363,9 @@ wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, con
  *
  *   block_tables, seq_lens, cu_q_lens: as for wf_paged_tree_decode (seq_lens still
  *              counts the drafts)
- *   accepted   [B, max_accepted] int32: the accepted drafts of request b, strictly
- *              increasing node numbers below n_b; entries past num_accepted[b] are not read
+ *   accepted   [B, max_accepted] int32: the accepted drafts of request b (as wf_verify_drafts
+ *              gives them), strictly increasing node numbers below n_b; entries past
+ *              num_accepted[b] are not read
  *   num_accepted [B] int32, 0 <= num_accepted[b] <= min(max_accepted, n_b)
  *   new_seq_lens [B] int32, may be NULL: receives c_b + num_accepted[b] (must not overlap
  *              another argument)
@@ -365,7 +375,7 @@ wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, con
  * they move to.  The drafts' blocks must belong to one request each.  (The block manager
  * of wf_blocks.h has no call that shortens a sequence: it goes on counting all drafts
  * that were appended.  A caller that verifies drafts keeps the lengths and the blocks of
- * its drafts itself.)
+ * its drafts itself, or on the GPU by wf_build_step and wf_trim_blocks.)
  * A request whose lengths are out of range (WF_DEV_BAD_SEQLEN) or whose path is
  * (WF_DEV_BAD_NODE) is skipped whole, its new_seq_lens entry left unwritten; a row whose
  * source or target block id is out of range (WF_DEV_BAD_BLOCK) is not moved.
@@ -374,6 +384,110 @@ wf_status wf_keep_accepted(void* k_pool, void* v_pool, const int32_t* block_tabl
                            const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* accepted,
                            int32_t max_accepted, const int32_t* num_accepted, int32_t* new_seq_lens, int32_t B,
                            wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * wf_verify_drafts -- which drafted tokens are kept, and the token after them.
+ * (the step between wf_paged_tree_decode's layers and wf_keep_accepted; the pages have no
+ *  drafts)
+ *
+ *   target       [total_q, vocab] probabilities, row stride target_stride elements: row
+ *                cu_q_lens[b] + u is the target's distribution p_u of the token after node u
+ *                of request b
+ *   draft        [total_q, vocab], row stride draft_stride, or NULL: the distribution q_u that
+ *                the children of node u were drawn from, each by itself (with replacement).
+ *                NULL: the children are fixed candidates.
+ *   vocab        1 .. 2^28; probs_dtype: WF_DTYPE_F32 or WF_DTYPE_BF16, of both
+ *   tokens       [total_q] int32: token of each node (node 0's is not looked at)
+ *   parents      [total_q] int32: node i's parent within its request, 0 <= parents < i; node
+ *                0, the request's newest token, has none (its entry is not looked at).
+ *                NULL: chains, node i hangs on node i - 1.
+ *   cu_q_lens    [B+1] int32: request b has the n_b rows cu_q_lens[b] .. cu_q_lens[b+1]-1
+ *   max_q_len    >= every n_b, at most 4096
+ *   coins        [total_q] float32 in [0, 1): a node's random number (node 0's is not used)
+ *   picks        [B] float32 in [0, 1): the next token's
+ *   accepted     [B, max_accepted] int32 receives the path's nodes, 0 first, each the parent
+ *                of the next, then -1: what wf_keep_accepted takes
+ *   num_accepted [B] int32 receives their number, 1 .. min(max_accepted, n_b)
+ *   next_tokens  [B] int32 receives the token after the path
+ * From node u = 0 on, u's children are tried in order: with w_0 = p_u and N_0 = 1, child i of
+ * token x is kept if coins[i] q_u(x) N_k < w_k(x), and u = i; else
+ * w_{k+1} = max(w_k - N_k q_u, 0) and N_{k+1} = sum w_{k+1}.  Fixed candidates: kept if
+ * coins[i] N_k < w_k(x), else w_{k+1} is w_k without token x and N_{k+1} = N_k - p_u(x).  The
+ * path ends where no child is kept, or at max_accepted nodes (whose last has no children
+ * tried).  The next token is the first x with w(0) + .. + w(x) > picks[b] sum w (w = p_u where
+ * sum w is 0).  So the tokens are distributed as the target's own if the coins and picks are
+ * independent and uniform, p and q sum to 1, and drawn children come from q.  Sums and
+ * comparisons are exact to about 2^-46, so that a seed gives the same tokens anywhere.
+ * Negative probabilities and NaN count as 0.
+ * A request with n_b = 0 gets num_accepted 0 and next token -1.  One whose rows
+ * (WF_DEV_BAD_SEQLEN), parents or tokens (WF_DEV_BAD_NODE), or pick (WF_DEV_BAD_PROBS) are out of
+ * range is skipped and its outputs are left unwritten; where p_u has no positive finite sum its
+ * next token is -1 (WF_DEV_BAD_PROBS).
+ * Pointers are aligned to their elements; 16-byte aligned fp32 (8-byte bf16) rows are read
+ * faster.  No workspace.
+ */
+wf_status wf_verify_drafts(int32_t* accepted, int32_t max_accepted, int32_t* num_accepted, int32_t* next_tokens,
+                           const void* target, int64_t target_stride, const void* draft, int64_t draft_stride,
+                           int32_t vocab, int32_t probs_dtype, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* cu_q_lens, const float* coins, const float* picks, int32_t B, int32_t total_q,
+                           int32_t max_q_len, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * wf_build_step -- a step's block tables, slots, positions and offsets from the requests'
+ * lengths, on the GPU: what wf_blocks.h's wf_bm_append and wf_bm_tables give on the host, for
+ * requests that share no blocks.
+ * (tiny-vllm-py, "Mental Model": a request grows block by block; weft, "Cache layouts":
+ *  blocks are handed out to requests from a shared pool)
+ *
+ *   block_tables  [B, max_blocks_per_seq] int32, updated in place: the entries of the blocks
+ *                 that a request grows by are written, no others
+ *   seq_lens      [B] int32: tokens that request b holds, in ceil(seq_lens[b] / P) blocks
+ *   new_lens      [B] int32: tokens n_b >= 0 that it gets this step
+ *   free_blocks   [num_blocks] int32: the ids of the free blocks, num_free[0] of them in use,
+ *                 taken from the end (the last freed first), request by request
+ *   num_free      [1] int32
+ *   depths        [max_tokens] int32 or NULL: a row's position behind its request's tokens where
+ *                 that is not its place there (drafts of a tree)
+ *   new_seq_lens  [B] int32 receives seq_lens[b] + n_b; may be seq_lens itself
+ *   new_num_free  [1] int32 receives what is left; may be num_free itself
+ *   cu_q_lens     [B+1] int32 receives the offsets of the requests' rows
+ *   slot_mapping  [max_tokens] int64 receives each row's slot; rows past the last are padding: -1
+ *   positions     [max_tokens] int32 receives seq_lens[b] + i of row i of request b, or
+ *                 seq_lens[b] + depths[row]; padding rows get 0
+ *   B             0 .. 16384; block_size P 1 .. 1024
+ * A step is built whole or not at all: lengths out of range (negative, past
+ * max_blocks_per_seq * P or 2^31 - 1), more than max_tokens rows (WF_DEV_BAD_SEQLEN), too few
+ * free blocks (WF_DEV_NO_BLOCKS), a free block's id or a request's partly filled block out of
+ * range (WF_DEV_BAD_BLOCK) leave the tables as they are, new_seq_lens = seq_lens,
+ * new_num_free = num_free, all offsets 0 and all slots -1, so that the calls that follow have
+ * no rows.  Apart from the two pairs named, outputs must not overlap inputs.
+ */
+wf_status wf_build_step(int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* new_lens, const int32_t* free_blocks, const int32_t* num_free,
+                        const int32_t* depths, int32_t* new_seq_lens, int32_t* new_num_free, int32_t* cu_q_lens,
+                        int64_t* slot_mapping, int32_t* positions, int32_t B, int32_t max_tokens, int32_t num_blocks,
+                        int32_t block_size, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * wf_trim_blocks -- the blocks that requests no longer need go back to the free list: those of
+ * rejected drafts, or (kept_lens 0) of finished requests.
+ *
+ *   block_tables, seq_lens, free_blocks, num_free: as for wf_build_step; the tables are only read
+ *   kept_lens     [B] int32: tokens that request b keeps, 0 <= kept_lens[b] <= seq_lens[b] (what
+ *                 wf_keep_accepted gives as new_seq_lens).  Its blocks ceil(kept_lens[b] / P) ..
+ *                 ceil(seq_lens[b] / P) - 1 go back.
+ *   free_blocks   receives them behind the num_free[0] that are there, the last request's last
+ *                 block first, so that the next wf_build_step hands them out in the order they
+ *                 had
+ *   new_num_free  [1] int32 receives the number of free blocks; may be num_free itself
+ *   B             0 .. 16384
+ * Blocks that several tables hold must not be among those that go back.  All or nothing, as for
+ * wf_build_step: lengths out of range (WF_DEV_BAD_SEQLEN), block ids out of range or more blocks
+ * than num_blocks (WF_DEV_BAD_BLOCK) leave the list as it is and new_num_free = num_free.
+ */
+wf_status wf_trim_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         const int32_t* kept_lens, int32_t* free_blocks, const int32_t* num_free, int32_t* new_num_free,
+                         int32_t B, int32_t num_blocks, int32_t block_size, uint32_t* dev_status, cudaStream_t stream);
 
 /*
  * Size of the fixed device array wf_paged_decode_static_scratch uses as its

@@ -26,7 +26,7 @@
  *   - A call that fails changes nothing.
  *   - A sequence grows or is freed, it is never shortened: drafts that a verification
  *     step rejects (wf_keep_accepted) would stay counted, so their slots and lengths
- *     are kept by the caller.
+ *     are kept by the caller, or on the GPU (wf_build_step, wf_trim_blocks).
  */
 #ifndef WF_BLOCKS_H
 #define WF_BLOCKS_H

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(PKG, "libwf.so")
 WF_OK, WF_ERR_INVALID_ARG, WF_ERR_UNSUPPORTED, WF_ERR_WORKSPACE, WF_ERR_CUDA, WF_ERR_NO_BLOCKS = range(6)
 WF_DTYPE_F32, WF_DTYPE_BF16, WF_DTYPE_FP8_E4M3 = 0, 1, 2
 WF_DEV_BAD_SLOT, WF_DEV_BAD_BLOCK, WF_DEV_BAD_SEQLEN, WF_DEV_TIMEOUT, WF_DEV_BAD_TASK = 0x1, 0x2, 0x4, 0x8, 0x10
-WF_DEV_BAD_POSITION, WF_DEV_BAD_NODE = 0x20, 0x40
+WF_DEV_BAD_POSITION, WF_DEV_BAD_NODE, WF_DEV_NO_BLOCKS, WF_DEV_BAD_PROBS = 0x20, 0x40, 0x80, 0x100
 WF_KERNEL_NONE, WF_KERNEL_CUDA_CORES, WF_KERNEL_TENSOR_CORES, WF_KERNEL_TENSOR_CORES_SIMPLE = range(4)
 
 # every entry point include/*.h declares
@@ -32,7 +32,10 @@ EXPORTS = (
     "wf_paged_prefill_decode_fused",
     "wf_paged_tree_decode_workspace_size",
     "wf_paged_tree_decode",
+    "wf_verify_drafts",
     "wf_keep_accepted",
+    "wf_build_step",
+    "wf_trim_blocks",
     "wf_paged_decode_static_scratch",
     "wf_decode_worker",
     "wf_paged_decode_kernel",
@@ -110,6 +113,13 @@ def load(path: str = LIB_PATH):
         lib.wf_paged_tree_decode_kernel.restype = ctypes.c_int
         lib.wf_keep_accepted.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, i32, wf_pool_desc, vp, vp]
         lib.wf_keep_accepted.restype = ctypes.c_int
+        lib.wf_verify_drafts.argtypes = [vp, i32, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp,
+                                         vp]
+        lib.wf_verify_drafts.restype = ctypes.c_int
+        lib.wf_build_step.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+        lib.wf_build_step.restype = ctypes.c_int
+        lib.wf_trim_blocks.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp]
+        lib.wf_trim_blocks.restype = ctypes.c_int
         lib.wf_paged_decode_static_scratch.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, f32,
                                                        wf_pool_desc, vp, vp]
         lib.wf_paged_decode_static_scratch.restype = ctypes.c_int
@@ -453,6 +463,91 @@ def wf_keep_accepted(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted
         _ptr(dev_status), _stream(stream))
     if rc:
         raise WfError("wf_keep_accepted", rc)
+
+
+def wf_verify_drafts(accepted, num_accepted, next_tokens, target, draft, tokens, parents, cu_q_lens, max_q_len: int,
+                     coins, picks, dev_status=None, stream=None):
+    """The accepted path and the next token of each request's drafts.  target [T, V] and draft [T, V] (or None: fixed
+    candidates) probabilities in float32 or bfloat16, rows may be strided; tokens [T] and parents [T] (or None: chains)
+    int32; cu_q_lens [B + 1] int32; coins [T] and picks [B] float32.  accepted [B, depth], num_accepted and next_tokens [B]
+    int32 receive them."""
+    bf16, _, f32, i32, _, _ = _known_types or _types()
+    _dense(accepted, num_accepted, next_tokens, tokens, parents, cu_q_lens, coins, picks)
+    T, V = target.shape
+    B, depth = accepted.shape
+    dt = target.dtype
+    if (dt is not f32 and dt is not bf16) or (V > 1 and target.stride(1) != 1):
+        raise ValueError("target must be [T, V] float32 or bfloat16 with dense rows")
+    if draft is not None and (draft.shape != target.shape or draft.dtype is not dt or (V > 1 and draft.stride(1) != 1)):
+        raise ValueError("draft must be like target")
+    if tokens.shape != (T,) or coins.shape != (T,) or (parents is not None and parents.shape != (T,)) or \
+            picks.shape != (B,) or cu_q_lens.shape != (B + 1,) or num_accepted.shape != (B,) or next_tokens.shape != (B,):
+        raise ValueError("tokens, parents and coins are [T], picks, num_accepted and next_tokens [B], cu_q_lens [B + 1]")
+    if coins.dtype is not f32 or picks.dtype is not f32:
+        raise ValueError("coins and picks are float32")
+    for t in (accepted, num_accepted, next_tokens, tokens, parents, cu_q_lens):
+        if t is not None and t.dtype is not i32:
+            raise ValueError("paths, tokens, parents and offsets are int32")
+    # the stride of a single row does not matter, and torch may give any
+    rows = lambda t: t.stride(0) if T > 1 else V   # noqa: E731
+    rc = (_lib or load()).wf_verify_drafts(
+        accepted.data_ptr(), depth, num_accepted.data_ptr(), next_tokens.data_ptr(), target.data_ptr(), rows(target),
+        draft.data_ptr() if draft is not None else None, rows(draft) if draft is not None else 0, V,
+        WF_DTYPE_F32 if dt is f32 else WF_DTYPE_BF16, tokens.data_ptr(), parents.data_ptr() if parents is not None else None,
+        cu_q_lens.data_ptr(), coins.data_ptr(), picks.data_ptr(), B, T, max_q_len, _ptr(dev_status), _stream(stream))
+    if rc:
+        raise WfError("wf_verify_drafts", rc)
+
+
+def wf_build_step(block_tables, seq_lens, new_lens, free_blocks, num_free, new_seq_lens, new_num_free, cu_q_lens,
+                  slot_mapping, positions, block_size: int, depths=None, dev_status=None, stream=None):
+    """A step's tables from the requests' lengths: block_tables [B, M] gets the blocks that seq_lens [B] + new_lens [B]
+    tokens need beyond seq_lens, taken from the end of free_blocks [N] (num_free [1] of them); new_seq_lens [B] (may be
+    seq_lens), new_num_free [1] (may be num_free), cu_q_lens [B + 1], slot_mapping [max_tokens] int64 and positions
+    [max_tokens] receive the rest.  depths [max_tokens] or None.  All int32 but the slots."""
+    _, _, _, i32, i64, _ = _known_types or _types()
+    ints = (block_tables, seq_lens, new_lens, free_blocks, num_free, new_seq_lens, new_num_free, cu_q_lens, positions,
+            depths)
+    _dense(slot_mapping, *ints)
+    for t in ints:
+        if t is not None and t.dtype is not i32:
+            raise ValueError("tables, lengths, lists, offsets and positions are int32")
+    B, M = block_tables.shape
+    rows = slot_mapping.shape[0]
+    if slot_mapping.dtype is not i64 or positions.shape != (rows,) or (depths is not None and depths.shape != (rows,)):
+        raise ValueError("slot_mapping [max_tokens] is int64, positions and depths are [max_tokens]")
+    if seq_lens.shape != (B,) or new_lens.shape != (B,) or new_seq_lens.shape != (B,) or cu_q_lens.shape != (B + 1,) or \
+            num_free.numel() != 1 or new_num_free.numel() != 1 or free_blocks.dim() != 1:
+        raise ValueError("seq_lens, new_lens and new_seq_lens are [B], cu_q_lens [B + 1], free_blocks [N], num_free and "
+                         "new_num_free [1]")
+    rc = (_lib or load()).wf_build_step(
+        block_tables.data_ptr(), M, seq_lens.data_ptr(), new_lens.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
+        depths.data_ptr() if depths is not None else None, new_seq_lens.data_ptr(), new_num_free.data_ptr(),
+        cu_q_lens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), B, rows, free_blocks.shape[0], block_size,
+        _ptr(dev_status), _stream(stream))
+    if rc:
+        raise WfError("wf_build_step", rc)
+
+
+def wf_trim_blocks(block_tables, seq_lens, kept_lens, free_blocks, num_free, new_num_free, block_size: int,
+                   dev_status=None, stream=None):
+    """The blocks of block_tables [B, M] between kept_lens [B] and seq_lens [B] tokens go back behind the num_free [1]
+    that free_blocks [N] holds; new_num_free [1] (may be num_free) receives their number.  All int32."""
+    _, _, _, i32, _, _ = _known_types or _types()
+    ints = (block_tables, seq_lens, kept_lens, free_blocks, num_free, new_num_free)
+    _dense(*ints)
+    for t in ints:
+        if t.dtype is not i32:
+            raise ValueError("tables, lengths and lists are int32")
+    B, M = block_tables.shape
+    if seq_lens.shape != (B,) or kept_lens.shape != (B,) or free_blocks.dim() != 1 or num_free.numel() != 1 or \
+            new_num_free.numel() != 1:
+        raise ValueError("seq_lens and kept_lens are [B], free_blocks [N], num_free and new_num_free [1]")
+    rc = (_lib or load()).wf_trim_blocks(
+        block_tables.data_ptr(), M, seq_lens.data_ptr(), kept_lens.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
+        new_num_free.data_ptr(), B, free_blocks.shape[0], block_size, _ptr(dev_status), _stream(stream))
+    if rc:
+        raise WfError("wf_trim_blocks", rc)
 
 
 WF_STATIC_SCRATCH_BYTES = 32 * 1024 * 1024

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <mutex>
 #include <unordered_map>
+#include <utility>
 
 #include "wf_internal.h"
 
@@ -216,6 +217,96 @@ wf_status wf_keep_accepted(void* k_pool, void* v_pool, const int32_t* block_tabl
     return from_cuda(wf::launch_keep_accepted(k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
                                               accepted, max_accepted, num_accepted, new_seq_lens, B, pool, dev_status,
                                               stream));
+}
+
+wf_status wf_verify_drafts(int32_t* accepted, int32_t max_accepted, int32_t* num_accepted, int32_t* next_tokens,
+                           const void* target, int64_t target_stride, const void* draft, int64_t draft_stride,
+                           int32_t vocab, int32_t probs_dtype, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* cu_q_lens, const float* coins, const float* picks, int32_t B, int32_t total_q,
+                           int32_t max_q_len, uint32_t* dev_status, cudaStream_t stream) {
+    if (B < 0 || total_q < 0 || max_q_len < 0 || max_accepted < 1 || vocab < 1) return WF_ERR_INVALID_ARG;
+    if (probs_dtype != WF_DTYPE_F32 && probs_dtype != WF_DTYPE_BF16) return WF_ERR_UNSUPPORTED;
+    if (max_q_len > wf::kMaxVerifyNodes || vocab > wf::kMaxVocab || B > (1 << 24)) return WF_ERR_UNSUPPORTED;
+    if (B == 0) return WF_OK;
+    if (!accepted || !num_accepted || !next_tokens || !cu_q_lens || !picks) return WF_ERR_INVALID_ARG;
+    const int64_t elt = probs_dtype == WF_DTYPE_F32 ? 4 : 2, cap = (int64_t)1 << 40;
+    if (total_q > 0) {
+        if (!target || !tokens || !coins) return WF_ERR_INVALID_ARG;
+        if (target_stride < vocab || target_stride > cap) return WF_ERR_INVALID_ARG;
+        if (draft && (draft_stride < vocab || draft_stride > cap)) return WF_ERR_INVALID_ARG;
+    }
+    if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) & (uintptr_t)(elt - 1))
+        return WF_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)accepted, (const void*)num_accepted, (const void*)next_tokens,
+                          (const void*)tokens, (const void*)parents, (const void*)cu_q_lens, (const void*)coins,
+                          (const void*)picks})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return WF_ERR_INVALID_ARG;
+    const wf::VerifyArgs a{accepted, num_accepted, next_tokens, max_accepted, target, draft, target_stride, draft_stride,
+                           vocab, probs_dtype, tokens, parents, cu_q_lens, coins, picks, B, total_q, max_q_len};
+    return from_cuda(wf::launch_verify_drafts(a, dev_status, stream));
+}
+
+wf_status wf_build_step(int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* new_lens, const int32_t* free_blocks, const int32_t* num_free,
+                        const int32_t* depths, int32_t* new_seq_lens, int32_t* new_num_free, int32_t* cu_q_lens,
+                        int64_t* slot_mapping, int32_t* positions, int32_t B, int32_t max_tokens, int32_t num_blocks,
+                        int32_t block_size, uint32_t* dev_status, cudaStream_t stream) {
+    if (B < 0 || max_tokens < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1 || block_size > 1024)
+        return WF_ERR_INVALID_ARG;
+    if (B > wf::kMaxStepRequests) return WF_ERR_UNSUPPORTED;
+    if (!free_blocks || !num_free || !new_num_free || !cu_q_lens) return WF_ERR_INVALID_ARG;
+    if (B > 0 && (!block_tables || !seq_lens || !new_lens || !new_seq_lens)) return WF_ERR_INVALID_ARG;
+    if (max_tokens > 0 && (!slot_mapping || !positions)) return WF_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)block_tables, (const void*)seq_lens, (const void*)new_lens,
+                          (const void*)free_blocks, (const void*)num_free, (const void*)depths,
+                          (const void*)new_seq_lens, (const void*)new_num_free, (const void*)cu_q_lens,
+                          (const void*)positions})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return WF_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) return WF_ERR_INVALID_ARG;
+    // written while others are read; seq_lens and num_free may be updated in place, from their first element on
+    const int64_t lens = 4 * (int64_t)B, rows = 4 * (int64_t)max_tokens;
+    const struct {
+        const void* p;
+        int64_t bytes;
+    } in[] = {{seq_lens, lens}, {new_lens, lens}, {free_blocks, 4 * (int64_t)num_blocks}, {num_free, 4}, {depths, depths ? rows : 0}},
+      out[] = {{block_tables, 4 * (int64_t)B * max_blocks_per_seq}, {new_seq_lens, lens}, {new_num_free, 4},
+               {cu_q_lens, lens + 4}, {slot_mapping, 2 * rows}, {positions, rows}};
+    constexpr int kOut = sizeof(out) / sizeof(out[0]);
+    for (int o = 0; o < kOut; ++o) {
+        if (out[o].bytes == 0) continue;
+        for (const auto& i : in) {
+            const bool in_place = (out[o].p == new_seq_lens && i.p == seq_lens && new_seq_lens == seq_lens) ||
+                                  (out[o].p == new_num_free && i.p == num_free && new_num_free == num_free);
+            if (i.bytes > 0 && !in_place && overlap(out[o].p, out[o].bytes, i.p, i.bytes)) return WF_ERR_INVALID_ARG;
+        }
+        for (int x = o + 1; x < kOut; ++x)
+            if (out[x].bytes > 0 && overlap(out[o].p, out[o].bytes, out[x].p, out[x].bytes)) return WF_ERR_INVALID_ARG;
+    }
+    const wf::BuildArgs a{block_tables, max_blocks_per_seq, seq_lens, new_lens, free_blocks, num_free, depths,
+                          new_seq_lens, new_num_free, cu_q_lens, slot_mapping, positions, B, max_tokens, num_blocks,
+                          block_size};
+    return from_cuda(wf::launch_build_step(a, dev_status, stream));
+}
+
+wf_status wf_trim_blocks(const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         const int32_t* kept_lens, int32_t* free_blocks, const int32_t* num_free, int32_t* new_num_free,
+                         int32_t B, int32_t num_blocks, int32_t block_size, uint32_t* dev_status, cudaStream_t stream) {
+    if (B < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || block_size < 1 || block_size > 1024)
+        return WF_ERR_INVALID_ARG;
+    if (B > wf::kMaxStepRequests) return WF_ERR_UNSUPPORTED;
+    if (!free_blocks || !num_free || !new_num_free) return WF_ERR_INVALID_ARG;
+    if (B > 0 && (!block_tables || !seq_lens || !kept_lens)) return WF_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)block_tables, (const void*)seq_lens, (const void*)kept_lens,
+                          (const void*)free_blocks, (const void*)num_free, (const void*)new_num_free})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return WF_ERR_INVALID_ARG;
+    const int64_t lens = 4 * (int64_t)B, list = 4 * (int64_t)num_blocks, table = lens * max_blocks_per_seq;
+    if (overlap(free_blocks, list, num_free, 4) || overlap(free_blocks, list, new_num_free, 4)) return WF_ERR_INVALID_ARG;
+    if (B > 0)
+        for (const auto& [p, bytes] : {std::pair<const void*, int64_t>{block_tables, table}, {seq_lens, lens}, {kept_lens, lens}})
+            if (overlap(free_blocks, list, p, bytes) || overlap(new_num_free, 4, p, bytes)) return WF_ERR_INVALID_ARG;
+    const wf::TrimArgs a{block_tables, max_blocks_per_seq, seq_lens, kept_lens, free_blocks, num_free, new_num_free, B,
+                         num_blocks, block_size};
+    return from_cuda(wf::launch_trim_blocks(a, dev_status, stream));
 }
 
 wf_status wf_copy_blocks(void* k_pool, void* v_pool, const int32_t* block_pairs, int32_t num_pairs,

@@ -168,6 +168,43 @@ cudaError_t launch_keep_accepted(void* k_pool, void* v_pool, const int32_t* bloc
                                  int32_t max_accepted, const int32_t* num_accepted, int32_t* new_seq_lens, int32_t B,
                                  const wf_pool_desc& pool, uint32_t* dev_status, cudaStream_t stream);
 
+// Drafts against the target's probabilities (verify_drafts.cu).
+constexpr int kMaxVerifyNodes = 4096, kMaxVocab = 1 << 28;   // nodes of a request in shared memory; 32-bit token numbers
+struct VerifyArgs {
+    int32_t *accepted, *num_accepted, *next_tokens;
+    int32_t max_accepted;
+    const void *target, *draft;                  // row strides in elements
+    int64_t target_stride, draft_stride;
+    int32_t vocab, probs_dtype;
+    const int32_t *tokens, *parents, *cu_q_lens;
+    const float *coins, *picks;
+    int32_t B, total, max_q_len;
+};
+cudaError_t launch_verify_drafts(const VerifyArgs& a, uint32_t* dev_status, cudaStream_t stream);
+
+// A step's tables and the blocks given back (step_tables.cu).
+constexpr int kMaxStepRequests = 16384;          // their sums stand in shared memory
+struct BuildArgs {
+    int32_t* block_tables;
+    int32_t max_blocks_per_seq;
+    const int32_t *seq_lens, *new_lens, *free_blocks, *num_free, *depths;
+    int32_t *new_seq_lens, *new_num_free, *cu_q_lens;
+    int64_t* slot_mapping;
+    int32_t* positions;
+    int32_t B, max_tokens, num_blocks, block_size;
+};
+cudaError_t launch_build_step(const BuildArgs& a, uint32_t* dev_status, cudaStream_t stream);
+struct TrimArgs {
+    const int32_t* block_tables;
+    int32_t max_blocks_per_seq;
+    const int32_t *seq_lens, *kept_lens;
+    int32_t* free_blocks;
+    const int32_t* num_free;
+    int32_t* new_num_free;
+    int32_t B, num_blocks, block_size;
+};
+cudaError_t launch_trim_blocks(const TrimArgs& a, uint32_t* dev_status, cudaStream_t stream);
+
 // Tree attention (paged_tree.cu: CUDA cores, the joining kernel and the dispatch).
 struct TreeArgs {
     void* out;
