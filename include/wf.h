@@ -16,6 +16,11 @@
  *   wf_verify_drafts           the accepted path, from the target's probabilities
  *   wf_keep_accepted           the accepted path's rows moved to the front of the drafts
  *
+ * Models whose scores are capped by a tanh or biased by distance, windows, packed documents and
+ * prefixes seen in both directions have
+ *
+ *   wf_paged_scored_attention  for single tokens and prompts alike
+ *
  * And a step's tables need not come from the host:
  *
  *   wf_build_step         block tables, slots, positions and offsets from the requests' lengths
@@ -384,6 +389,61 @@ wf_status wf_keep_accepted(void* k_pool, void* v_pool, const int32_t* block_tabl
                            const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* accepted,
                            int32_t max_accepted, const int32_t* num_accepted, int32_t* new_seq_lens, int32_t B,
                            wf_pool_desc pool, uint32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Bytes of caller-allocated device workspace wf_paged_scored_attention needs for at most B
+ * requests of at most max_q_len new tokens each, total_q in all, and max_seq_len tokens.  Depends
+ * only on its arguments, and larger ones never need less; 0 if they are invalid.
+ */
+size_t wf_paged_scored_attention_workspace_size(int32_t B, int32_t num_q_heads, int32_t total_q, int32_t max_q_len,
+                                                int32_t max_seq_len, wf_pool_desc pool);
+
+/*
+ * wf_paged_scored_attention -- attention of new tokens (one a request, a few, or whole
+ * prompts, mixed as they come) over the pool, with capped scores, a bias by distance, and a
+ * window or a range of positions for each row.
+ * (the reads of wf_paged_decode and the packed rows of wf_paged_prefill; the pages' models
+ *  have plain causal scores)
+ *
+ *   out, q     [T_total, H_q, D]: request b owns rows cu_q_lens[b] .. cu_q_lens[b+1]-1, its n_b
+ *              new tokens.  Rows past cu_q_lens[B] are not written.  out must not overlap q.
+ *   cu_q_lens  [B+1] int32, cu_q_lens[0] = 0, non-decreasing, cu_q_lens[B] <= T_total
+ *   seq_lens   [B] int32: tokens of request b in the pool INCLUDING its n_b new ones, already
+ *              written.  Row i is the token at position t = seq_lens[b] - n_b + i.
+ *   scale      softmax scale; scale * log2(e) must be finite in float32
+ *   cap        > 0: a score x = scale q.K_p becomes cap tanh(x / cap); 0: it stays
+ *   slopes     [H_q] float32 or NULL: then slopes[g] |t - p| is taken off it (any sign)
+ *   window     > 0: position p is seen only if p > t - window; 0: no window
+ *   row_ranges [T_total, 2] int32, 8-byte aligned, or NULL: row r sees the positions p with
+ *              row_ranges[r][0] <= p < row_ranges[r][1] (cut to the request's tokens); NULL: p <= t.
+ *              So a document packed with others starts its rows' ranges at its first position, a
+ *              prefix seen in both directions ends them at its last one, and an empty range is a
+ *              row of padding.  The window cuts a range too.
+ *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b], below 2^31 - 1024.  max_q_len also
+ *              decides how the rows of all requests are laid over the GPU.
+ *   workspace  device scratch of >= wf_paged_scored_attention_workspace_size(B, H_q, T_total,
+ *              max_q_len, max_seq_len, pool) bytes, 16-byte aligned; needs no initialisation.
+ *              Calls that overlap in time must not share one.
+ * A row that sees nothing gives zeros.  Positions that a row does not see have no effect on it,
+ * whatever their K and V rows hold (NaN and infinities included), and table entries of blocks before
+ * the first position and behind the last one that any row of a request sees are not read: a window's
+ * past may be given back.  Requests
+ * with n_b = 0 are no-ops.  A request whose n_b or length is out of range (WF_DEV_BAD_SEQLEN) is
+ * skipped and its rows are left unwritten; positions of a block id out of range
+ * (WF_DEV_BAD_BLOCK) are left out of the softmax.
+ * float32, bfloat16 and fp8 e4m3 pools (q and out bfloat16 for fp8), H_q / H_kv <= 8.  bf16 and fp8
+ * pools of block sizes that are multiples of 16 run on the tensor cores (the kernel is
+ * wf_paged_tree_decode_kernel's), others on the CUDA cores.  Scores, cap, bias and softmax are
+ * float32; the weights that multiply V are rounded as in wf_paged_tree_decode.
+ * As there, where a request's softmax is cut and joined depends on the whole batch: two calls with the
+ * same inputs give the same bytes, one request in two batches need not.
+ */
+wf_status wf_paged_scored_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                    const int32_t* cu_q_lens, int32_t B, int32_t total_q, int32_t max_q_len,
+                                    int32_t max_seq_len, int32_t num_q_heads, float scale, float cap, int32_t window,
+                                    const float* slopes, const int32_t* row_ranges, wf_pool_desc pool, void* workspace,
+                                    size_t workspace_bytes, uint32_t* dev_status, cudaStream_t stream);
 
 /*
  * wf_verify_drafts -- which drafted tokens are kept, and the token after them.

@@ -32,6 +32,8 @@ EXPORTS = (
     "wf_paged_prefill_decode_fused",
     "wf_paged_tree_decode_workspace_size",
     "wf_paged_tree_decode",
+    "wf_paged_scored_attention_workspace_size",
+    "wf_paged_scored_attention",
     "wf_verify_drafts",
     "wf_keep_accepted",
     "wf_build_step",
@@ -113,6 +115,11 @@ def load(path: str = LIB_PATH):
         lib.wf_paged_tree_decode_kernel.restype = ctypes.c_int
         lib.wf_keep_accepted.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, vp, vp, i32, wf_pool_desc, vp, vp]
         lib.wf_keep_accepted.restype = ctypes.c_int
+        lib.wf_paged_scored_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32, wf_pool_desc]
+        lib.wf_paged_scored_attention_workspace_size.restype = sz
+        lib.wf_paged_scored_attention.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, f32, f32, i32, vp,
+                                                  vp, wf_pool_desc, vp, sz, vp, vp]
+        lib.wf_paged_scored_attention.restype = ctypes.c_int
         lib.wf_verify_drafts.argtypes = [vp, i32, vp, vp, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp,
                                          vp]
         lib.wf_verify_drafts.restype = ctypes.c_int
@@ -463,6 +470,42 @@ def wf_keep_accepted(k_pool, v_pool, block_tables, seq_lens, cu_q_lens, accepted
         _ptr(dev_status), _stream(stream))
     if rc:
         raise WfError("wf_keep_accepted", rc)
+
+
+def wf_paged_scored_attention_workspace_size(B: int, num_q_heads: int, total_q: int, max_q_len: int, max_seq_len: int,
+                                             desc: wf_pool_desc) -> int:
+    return int(load().wf_paged_scored_attention_workspace_size(B, num_q_heads, total_q, max_q_len, max_seq_len, desc))
+
+
+def wf_paged_scored_attention(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, max_q_len: int, max_seq_len: int,
+                              scale: float, workspace, cap: float = 0.0, window: int = 0, slopes=None, row_ranges=None,
+                              dev_status=None, stream=None, k_scale=1.0, v_scale=1.0):
+    """out, q [T_total, H_q, D] packed new tokens; cu_q_lens [B+1] int32; seq_lens [B] int32 count them; cap > 0: scores are
+    capped by a tanh; window > 0; slopes [H_q] float32: bias by distance; row_ranges [T_total, 2] int32: positions that a row
+    sees, instead of all up to its own; workspace uint8 tensor."""
+    bf16, u8, f32, i32, _, _ = _known_types or _types()
+    _dense(out, q, k_pool, v_pool, block_tables, seq_lens, cu_q_lens, slopes, row_ranges)
+    T, H_q, D = q.shape
+    B, M = block_tables.shape
+    dt, pool_dt = q.dtype, k_pool.dtype
+    if out.shape != q.shape or out.dtype is not dt or D != k_pool.shape[3] or \
+            dt is not (bf16 if pool_dt is u8 else pool_dt) or v_pool.shape != k_pool.shape or v_pool.dtype is not pool_dt:
+        raise ValueError("out is like q [T, H_q, D] of the pool's dtype (bf16 for fp8 pools) and head size")
+    if seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or block_tables.dtype is not i32 or \
+            seq_lens.dtype is not i32 or cu_q_lens.dtype is not i32:
+        raise ValueError("block_tables [B, M], seq_lens [B] and cu_q_lens [B + 1] are int32")
+    if slopes is not None and (slopes.dtype is not f32 or slopes.numel() != H_q):
+        raise ValueError("slopes are [H_q] float32")
+    if row_ranges is not None and (row_ranges.dtype is not i32 or row_ranges.shape != (T, 2)):
+        raise ValueError("row_ranges are [T, 2] int32")
+    rc = (_lib or load()).wf_paged_scored_attention(
+        out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), M,
+        seq_lens.data_ptr(), cu_q_lens.data_ptr(), B, T, max_q_len, max_seq_len, H_q, scale, cap, window,
+        slopes.data_ptr() if slopes is not None else None, row_ranges.data_ptr() if row_ranges is not None else None,
+        _desc(k_pool, k_scale, v_scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status), _stream(stream))
+    if rc:
+        raise WfError("wf_paged_scored_attention", rc)
 
 
 def wf_verify_drafts(accepted, num_accepted, next_tokens, target, draft, tokens, parents, cu_q_lens, max_q_len: int,

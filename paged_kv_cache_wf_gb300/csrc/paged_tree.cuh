@@ -45,6 +45,51 @@ struct TreeParams {
     const float* q_inv;   // fp8 pools on the tensor cores: factors of the prepared q rows
 };
 
+// Scored attention (wf_paged_scored_attention) runs the same kernels over another list of units.
+// A row block there has the tiles [tile0, tile0 + nt) that some of its rows see, which a small
+// grid before the kernel works out (scored_blocks_kernel): with windows, documents and causal rows
+// they differ from block to block, and with ranges they stand in device memory.
+struct ScoredBlock {
+    int b, q_row, rows_tok, at;     // request, first row of q, rows (tokens), position of the first row
+    int tile0, nt;                  // at least one tile, so that rows that see nothing are written too
+    int lo, hi;                     // positions [lo, hi) are all that any row sees
+    int full_lo, full_hi;           // [full_lo, full_hi) are seen by every row
+    int len, h;                     // tokens of the request; KV head (of a piece)
+};
+
+struct ScoredParams : TreeParams {
+    const int2* ranges;             // [total_q] {begin, end}, or null: a row sees what is not behind it
+    const float* slopes;            // [H_q] or null
+    int32_t window;                 // 0: none
+    float cap_in, cap_out;          // capped: y = cap_out - 2 cap_out / (1 + 2^(cap_in s)) of a raw score s
+    const ScoredBlock* blocks;
+    const int32_t* before;          // cost of the blocks before each, under one KV head; then of all
+    const int32_t* num_blocks;
+};
+
+// What a kernel's rows see, and what becomes of their scores.
+struct TreeView {
+    using Params = TreeParams;
+    static constexpr bool kScored = false;
+    static constexpr int kRule = 0;
+};
+enum ScoreRule { kRulePlain, kRuleBias, kRuleCap };   // kRuleCap: capped, and biased where there are slopes
+template <int RULE>
+struct ScoredView {
+    using Params = ScoredParams;
+    static constexpr bool kScored = true;
+    static constexpr int kRule = RULE;
+};
+
+// Row `row` of q at position `at` of its request of `len` tokens sees positions [x, y).
+__device__ __forceinline__ int2 scored_range(const ScoredParams& p, int row, int at, int len) {
+    int2 r = p.ranges != nullptr ? __ldg(p.ranges + row) : make_int2(0, at + 1);
+    if (p.window > 0) r.x = max(r.x, at - p.window + 1);
+    r.x = min(max(r.x, 0), len);
+    r.y = max(min(r.y, len), r.x);
+    return r;
+}
+
 // A factor of the scores, held at fp32's smallest normal number or above (its sign kept): a
 // masked score is -inf before it is scaled, and -inf * 0 is NaN.  At that factor every finite score
 // has a weight of 2^0, as it has at 0.
@@ -54,6 +99,12 @@ __host__ __device__ __forceinline__ float tree_factor(float f) { return copysign
 struct TreeShape {
     int rows, tokb, tile, ctas_per_sm, ucost;
 };
+
+// The shape for a geometry and longest request, and the CTAs a launch may use (paged_tree.cu).
+bool tree_shape(const wf_pool_desc& pool, int32_t num_q_heads, int32_t max_q_len, TreeShape* s);
+int64_t tree_ctas(const TreeShape& s, int32_t B, int32_t H_kv, int32_t max_q_len, int32_t max_seq_len);
+// Joins the pieces of units that the tensor-core kernel cut (bf16 outputs).
+cudaError_t tree_join(const TreeParams& p, const wf_pool_desc& pool, int ctas, cudaStream_t stream);
 
 // The tensor-core kernel (paged_tree_tc.cu).
 bool tree_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads);
@@ -161,6 +212,43 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
     __syncthreads();
 }
 
+// The same over the blocks of a scored call: the block that a CTA's stretch begins in.  Waits for
+// the grid that made the list.  All threads of the CTA; ends with a barrier.
+struct alignas(16) ScoredStart {
+    int share, left, pos, off;   // as in TreeStart; `off` within block `block`
+    int block;
+};
+
+__device__ __forceinline__ void scored_begin(const ScoredParams& p, int cta, int ncta, ScoredStart* st) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int nb = __ldcg(p.num_blocks);
+        const int64_t total = nb > 0 ? (int64_t)__ldcg(p.before + nb) * p.H_kv : 0;   // fits 31 bits
+        const int share = (int)((total + ncta - 1) / ncta);
+        const int s = (int)min((int64_t)share * cta, total), e = (int)min((int64_t)s + share, total);
+        // the last block whose cost before it is at most s / H_kv, 32 looked at a round
+        int lo = 0, hi = nb;
+        const int key = s / p.H_kv;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int at = lo + lane * step;
+            const bool le = at < hi && __ldcg(p.before + at) <= key;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+            lo += k * step;
+            hi = min(lo + step, hi);
+        }
+        if (lane == 0) {
+            st->share = share;
+            st->left = e - s;
+            st->pos = s;
+            st->block = lo;
+            st->off = s < e ? s - __ldcg(p.before + lo) * p.H_kv : 0;
+        }
+    }
+    __syncthreads();
+}
+
 // One piece of work: tiles [j0, j1) of a unit of `nt`.
 struct TreePiece {
     int b, h, qb;
@@ -230,12 +318,60 @@ struct TreeWalk {
     }
 };
 
+// A piece of a scored call.
+struct ScoredPiece {
+    int h, end;
+    int j0, j1, nt;      // tiles of the unit, from the block's tile0 on
+    ScoredBlock k;
+};
+
+struct ScoredWalk {
+    int pos, left, off, block, ready;
+    ScoredBlock k;
+
+    __device__ __forceinline__ ScoredWalk(const ScoredStart& st)
+        : pos(st.pos), left(st.left), off(st.off), block(st.block), ready(0) {}
+
+    __device__ __forceinline__ bool next(const ScoredParams& p, int tile, ScoredPiece& it) {
+        while (left > 0) {
+            if (!ready) {
+                const int4* from = reinterpret_cast<const int4*>(p.blocks + block);
+                const int4 x = __ldcg(from), y = __ldcg(from + 1), z = __ldcg(from + 2);
+                k = ScoredBlock{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, 0};
+                ready = 1;
+            }
+            const int w = k.nt + p.ucost;
+            if (off >= p.H_kv * w) {
+                off = 0;
+                ready = 0;
+                ++block;     // the stretches end at the last block's end
+                continue;
+            }
+            const int unit = off / w, x0 = off - unit * w;
+            const int x1 = left < w - x0 ? x0 + left : w;
+            it.end = pos - x0 + w;
+            off += x1 - x0;
+            pos += x1 - x0;
+            left -= x1 - x0;
+            it.j0 = max(0, x0 - p.ucost);
+            it.j1 = max(0, x1 - p.ucost);
+            if (it.j0 >= it.j1) continue;
+            it.nt = k.nt;
+            it.h = unit;
+            it.k = k;
+            return true;
+        }
+        return false;
+    }
+};
+
 // Workspace piece of a cut unit: its first piece in the second place of its CTA, every
 // later one in the first place of its own.
 __device__ __forceinline__ int tree_piece_slot(int cta, int j0) { return 2 * cta + (j0 == 0 ? 1 : 0); }
 
 // The last CTA that holds a piece of the unit whose first piece `it` is.
-__device__ __forceinline__ int tree_last(const TreeStart& st, const TreePiece& it, int cta) {
+template <typename Start, typename Piece>
+__device__ __forceinline__ int tree_last(const Start& st, const Piece& it, int cta) {
     int last = cta;
 #pragma unroll 1
     for (int64_t next = (int64_t)st.share * (cta + 1); next < it.end; next += st.share) ++last;

@@ -487,6 +487,48 @@ wf_status wf_paged_tree_decode(void* out, const void* q, const void* k_pool, con
     return from_cuda(wf::launch_paged_tree(a, pool, dev_status, stream));
 }
 
+size_t wf_paged_scored_attention_workspace_size(int32_t B, int32_t num_q_heads, int32_t total_q, int32_t max_q_len,
+                                                int32_t max_seq_len, wf_pool_desc pool) {
+    if (check_pool(pool) != WF_OK || num_q_heads < 1) return 0;
+    return wf::scored_workspace_bytes(B, num_q_heads, total_q, max_q_len, max_seq_len, pool);
+}
+
+wf_status wf_paged_scored_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                    const int32_t* cu_q_lens, int32_t B, int32_t total_q, int32_t max_q_len,
+                                    int32_t max_seq_len, int32_t num_q_heads, float scale, float cap, int32_t window,
+                                    const float* slopes, const int32_t* row_ranges, wf_pool_desc pool, void* workspace,
+                                    size_t workspace_bytes, uint32_t* dev_status, cudaStream_t stream) {
+    wf_status s = check_pool(pool);
+    if (s != WF_OK) return s;
+    if (B < 0 || total_q < 0 || max_q_len < 0 || max_seq_len < 0 || num_q_heads < 1 || max_blocks_per_seq < 1 || window < 0)
+        return WF_ERR_INVALID_ARG;
+    if (num_q_heads % pool.num_kv_heads != 0) return WF_ERR_INVALID_ARG;
+    if (num_q_heads / pool.num_kv_heads > 8) return WF_ERR_UNSUPPORTED;
+    if ((int64_t)max_seq_len > (int64_t)max_blocks_per_seq * pool.block_size || max_q_len > max_seq_len)
+        return WF_ERR_INVALID_ARG;
+    // positions are 32-bit and looked at a tile past the end
+    if (max_seq_len >= INT32_MAX - 1023) return WF_ERR_INVALID_ARG;
+    // the kernels take scores to powers of two: an infinite factor would make a score of 0 NaN
+    constexpr float kLog2e = 1.4426950408889634f;
+    if (!std::isfinite(scale * kLog2e) || !(cap >= 0.f) || !std::isfinite(cap * kLog2e)) return WF_ERR_INVALID_ARG;
+    if (cap > 0.f && !std::isfinite((float)(2.0 * kLog2e * (double)scale / (double)cap))) return WF_ERR_INVALID_ARG;
+    if (B == 0 || total_q == 0 || max_q_len == 0) return WF_OK;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !cu_q_lens) return WF_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool)) return WF_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)block_tables, (const void*)seq_lens, (const void*)cu_q_lens, (const void*)slopes})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return WF_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(row_ranges) & 7u) return WF_ERR_INVALID_ARG;
+    const size_t need = wf::scored_workspace_bytes(B, num_q_heads, total_q, max_q_len, max_seq_len, pool);
+    if (need == 0) return WF_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return WF_ERR_WORKSPACE;
+    const int64_t rows_bytes = (int64_t)total_q * num_q_heads * pool.head_dim * (pool.dtype == WF_DTYPE_F32 ? 4 : 2);
+    if (overlap(out, rows_bytes, q, rows_bytes)) return WF_ERR_INVALID_ARG;
+    const wf::ScoredArgs a{out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, row_ranges, slopes,
+                           cap, window, B, total_q, max_q_len, max_seq_len, num_q_heads, scale, workspace};
+    return from_cuda(wf::launch_paged_scored(a, pool, dev_status, stream));
+}
+
 wf_status wf_decode_worker(void* out, const void* q, int32_t num_rows, const void* k_pool, const void* v_pool,
                            const int32_t* block_tables, int32_t num_table_rows, int32_t max_blocks_per_seq,
                            int32_t num_q_heads, float scale, wf_pool_desc pool, const wf_decode_task* tasks,

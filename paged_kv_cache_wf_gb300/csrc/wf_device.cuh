@@ -71,6 +71,12 @@ __device__ __forceinline__ void widen_chunk<BF16>(const uint4& c, float* f) {
 }
 
 // 2^x on the SFU (approximate, flushes denormals); 2^-inf = +0.
+// 1 / x (to the last bit or so; 1 / infinity is 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

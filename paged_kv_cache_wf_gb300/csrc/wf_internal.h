@@ -222,6 +222,23 @@ size_t tree_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t max_q_len, i
 int tree_kernel_kind(const wf_pool_desc& pool, int32_t num_q_heads);
 cudaError_t launch_paged_tree(const TreeArgs& a, const wf_pool_desc& pool, uint32_t* dev_status, cudaStream_t stream);
 
+// Scored attention (paged_scored.cu).
+struct ScoredArgs {
+    void* out;
+    const void *q, *k_pool, *v_pool;
+    const int32_t* block_tables;
+    int32_t max_blocks_per_seq;
+    const int32_t *seq_lens, *cu_q_lens, *row_ranges;
+    const float* slopes;
+    float cap;
+    int32_t window, B, total_q, max_q_len, max_seq_len, num_q_heads;
+    float scale;
+    void* workspace;
+};
+size_t scored_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t total_q, int32_t max_q_len, int32_t max_seq_len,
+                              const wf_pool_desc& pool);
+cudaError_t launch_paged_scored(const ScoredArgs& a, const wf_pool_desc& pool, uint32_t* dev_status, cudaStream_t stream);
+
 // ---- prefill ------------------------------------------------------------------
 // Pipelined tcgen05 prefill (bf16, P % 16 == 0, G in {1, 2, 4, 8}, D in {64, 128}).
 bool prefill_tc_supported(const wf_pool_desc& pool, int32_t num_q_heads);
