@@ -44,6 +44,20 @@ cudaError_t allow_dynamic_smem(const void* kernel, int bytes) {
     return cudaSuccess;
 }
 
+cudaError_t allow_large_cluster(const void* kernel) {
+    static std::mutex mu;
+    static std::unordered_map<uint64_t, bool> done;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t key = (reinterpret_cast<uint64_t>(kernel) << 8) ^ (uint64_t)dev;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count(key)) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err == cudaSuccess) done[key] = true;
+    return err;
+}
+
 cudaError_t encode_tiled_bf16(CUtensorMap* map, void* base, int rank, const uint64_t* dims,
                               const uint64_t* strides, const uint32_t* box, CUtensorMapL2promotion promotion) {
     return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box,

@@ -20,6 +20,9 @@ int num_sms();
 // Opt a kernel into `bytes` of dynamic shared memory (idempotent, cached).
 cudaError_t allow_dynamic_smem(const void* kernel, int bytes);
 
+// Lets a kernel run in clusters of more than 8 CTAs (idempotent, cached).
+cudaError_t allow_large_cluster(const void* kernel);
+
 // Encode a tiled TMA descriptor for a bf16 tensor (128-byte swizzle, no OOB fill).
 // dims[0] is the contiguous dimension; strides[] are bytes for dims 1..rank-1.
 // `promotion`: the bytes an L2 miss fetches.

@@ -181,6 +181,7 @@ def test_values_that_are_no_probabilities():
     assert single([[nan, -1.0, 0.5, 0.0]], None, [0], [-1], [0], 0.0) == ([0], 2, 0)
     assert single([[0.5, nan, 0.5]] * 2, [[0.5, 0.5, 0.0]] * 2, [0, 1], [-1, 0], [0, 0.0], 0.0) == ([0], 2, 0)
     assert single([[0.5, 0.0, 0.5]] * 2, [[nan, 1.0, 0.0]] * 2, [0, 1], [-1, 0], [0, 0.0], 0.0) == ([0], 0, 0)
+    assert single([[0.25, inf, 0.5]] * 2, [[0.5, 0.25, 0.25]] * 2, [0, 0], [-1, 0], [0, 0.9], 0.5) == ([0], -1, bad)
     for row in ([0.0] * 3, [nan] * 3, [0.5, inf, 0.0], [-1.0, -2.0, 0.0]):
         assert single([row], None, [0], [-1], [0], 0.5) == ([0], -1, bad)
         assert single([row] * 3, [row] * 3, [0, 1, 1], [-1, 0, 0], [0, 1.0, 1.0], 0.5) == ([0], -1, bad)
