@@ -195,13 +195,26 @@ __global__ void __launch_bounds__(kListThreads) scored_list_kernel(const ListPar
     }
 }
 
+// Blocks of at most 32 rows (tensor cores): a row stands in all four quarters of the query tile, each of
+// which takes a quarter of a tile's positions, so that all eight softmax warps work on it.  (Of one token of 4
+// query heads the other way has 4 lanes of one warp a stream, which was the bound: 231 capped decodes 393 us.)
+bool scored_shape(const wf_pool_desc& pool, int32_t num_q_heads, int32_t max_q_len, TreeShape* s) {
+    if (!tree_shape(pool, num_q_heads, max_q_len, s)) return false;
+    const int G = num_q_heads / pool.num_kv_heads;
+    if (tree_tc_supported(pool, num_q_heads) && max_q_len <= 32 / G) {
+        s->rows = 32;
+        s->tokb = 32 / G;
+    }
+    return true;
+}
+
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 // Blocks that a batch can have.  Counted with the fewest rows that any kernel's block holds, so that
 // a longer max_q_len, which may go over to larger blocks, never needs less room.
 int64_t list_capacity(const wf_pool_desc& pool, int32_t num_q_heads, int32_t B, int32_t total_q, int32_t max_q_len) {
     TreeShape s;
-    if (!tree_shape(pool, num_q_heads, 1, &s)) return 0;
+    if (!scored_shape(pool, num_q_heads, 1, &s)) return 0;
     const int64_t by_rows = (int64_t)total_q / s.tokb + B, by_request = ((int64_t)max_q_len + s.tokb - 1) / s.tokb;
     const int64_t all = by_request == 0 ? 0 : B > by_rows / by_request ? by_rows : (int64_t)B * by_request;
     return all < by_rows ? all : by_rows;
@@ -214,7 +227,7 @@ struct Layout {
 
 bool scored_layout(const wf_pool_desc& pool, int32_t num_q_heads, int32_t B, int32_t total_q, int32_t max_q_len,
                    int32_t max_seq_len, TreeShape* s, int64_t* ctas, Layout* l) {
-    if (B < 0 || total_q < 0 || max_q_len < 0 || max_seq_len < 0 || !tree_shape(pool, num_q_heads, max_q_len, s)) return false;
+    if (B < 0 || total_q < 0 || max_q_len < 0 || max_seq_len < 0 || !scored_shape(pool, num_q_heads, max_q_len, s)) return false;
     *ctas = tree_ctas(*s, B, pool.num_kv_heads, max_q_len, max_seq_len);
     l->rows = 2 * *ctas * s->rows;
     const int64_t cap = list_capacity(pool, num_q_heads, B, total_q, max_q_len);
@@ -311,7 +324,7 @@ cudaError_t launch_paged_scored(const ScoredArgs& a, const wf_pool_desc& pool, u
     p.window = a.window;
     p.cap_in = p.cap_out = 0.f;
     if (a.cap > 0.f) {
-        p.cap_in = tree_factor((float)(2.0 * 1.4426950408889634 * (double)a.scale / (double)a.cap));
+        p.cap_in = tree_factor((float)((double)a.scale / (double)a.cap));
         p.cap_out = a.cap * kLog2e;
     }
     const bool tc = tree_tc_supported(pool, a.num_q_heads), codes = tc && pool.dtype == WF_DTYPE_FP8_E4M3;
@@ -332,14 +345,16 @@ cudaError_t launch_paged_scored(const ScoredArgs& a, const wf_pool_desc& pool, u
     const bool d128 = pool.head_dim == 128;
     cudaError_t e = launch_list(list, d128, stream);
     if (e != cudaSuccess) return e;
-    const int rule = a.cap > 0.f ? kRuleCap : a.slopes != nullptr ? kRuleBias : kRulePlain;
+    const bool capped = a.cap > 0.f, bias = a.slopes != nullptr;
     if (!tc)
-        return rule == kRuleCap ? launch_scored_cc<kRuleCap>(p, pool, ctas, stream)
-               : rule == kRuleBias ? launch_scored_cc<kRuleBias>(p, pool, ctas, stream)
-                                   : launch_scored_cc<kRulePlain>(p, pool, ctas, stream);
-    e = rule == kRuleCap ? launch_scored_tc<kRuleCap>(p, pool, list.parts, ctas, stream)
-        : rule == kRuleBias ? launch_scored_tc<kRuleBias>(p, pool, list.parts, ctas, stream)
-                            : launch_scored_tc<kRulePlain>(p, pool, list.parts, ctas, stream);
+        return capped ? bias ? launch_scored_cc<kRuleCapBias>(p, pool, ctas, stream)
+                             : launch_scored_cc<kRuleCap>(p, pool, ctas, stream)
+               : bias ? launch_scored_cc<kRuleBias>(p, pool, ctas, stream)
+                      : launch_scored_cc<kRulePlain>(p, pool, ctas, stream);
+    e = capped ? bias ? launch_scored_tc<kRuleCapBias>(p, pool, list.parts, ctas, stream)
+                      : launch_scored_tc<kRuleCap>(p, pool, list.parts, ctas, stream)
+        : bias ? launch_scored_tc<kRuleBias>(p, pool, list.parts, ctas, stream)
+               : launch_scored_tc<kRulePlain>(p, pool, list.parts, ctas, stream);
     if (e != cudaSuccess || ctas == 1) return e;
     return tree_join(p, pool, ctas, stream);
 }

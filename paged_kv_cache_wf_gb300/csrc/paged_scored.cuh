@@ -6,6 +6,7 @@
 
 namespace wf {
 
+// Spread: blocks of at most 32 rows (p.rows == 32).
 template <int RULE>
 cudaError_t launch_scored_tc(const ScoredParams& p, const wf_pool_desc& pool, void* prep, int ctas, cudaStream_t stream);
 template <int RULE>

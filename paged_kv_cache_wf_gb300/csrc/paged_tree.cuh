@@ -61,7 +61,7 @@ struct ScoredParams : TreeParams {
     const int2* ranges;             // [total_q] {begin, end}, or null: a row sees what is not behind it
     const float* slopes;            // [H_q] or null
     int32_t window;                 // 0: none
-    float cap_in, cap_out;          // capped: y = cap_out - 2 cap_out / (1 + 2^(cap_in s)) of a raw score s
+    float cap_in, cap_out;          // capped: a raw score s becomes cap_out tanh(cap_in s), in powers of two
     const ScoredBlock* blocks;
     const int32_t* before;          // cost of the blocks before each, under one KV head; then of all
     const int32_t* num_blocks;
@@ -72,13 +72,16 @@ struct TreeView {
     using Params = TreeParams;
     static constexpr bool kScored = false;
     static constexpr int kRule = 0;
+    static constexpr bool kSpread = false;
 };
-enum ScoreRule { kRulePlain, kRuleBias, kRuleCap };   // kRuleCap: capped, and biased where there are slopes
-template <int RULE>
+enum ScoreRule { kRulePlain, kRuleBias, kRuleCap, kRuleCapBias };
+// SPREAD: blocks of at most 32 rows (one or a few tokens a request), on the tensor cores.
+template <int RULE, bool SPREAD = false>
 struct ScoredView {
     using Params = ScoredParams;
     static constexpr bool kScored = true;
     static constexpr int kRule = RULE;
+    static constexpr bool kSpread = SPREAD;
 };
 
 // Row `row` of q at position `at` of its request of `len` tokens sees positions [x, y).

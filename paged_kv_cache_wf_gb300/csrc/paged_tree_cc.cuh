@@ -141,7 +141,9 @@ __global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
             b = it.b;
         }
         float factor = p.scale_log2;
-        if constexpr (V::kRule == kRuleCap) factor = p.cap_in * 0.34657359027997264f;   // scale / cap: tanh's argument
+        constexpr bool kCap = V::kRule == kRuleCap || V::kRule == kRuleCapBias;
+        constexpr bool kBias = V::kRule == kRuleBias || V::kRule == kRuleCapBias;
+        if constexpr (kCap) factor = p.cap_in;
         const float qscale = E::kBytes == 1 ? factor * sc.k[min(it.h, kMaxScaleHeads - 1)] : factor;
         const float vscale = E::kBytes == 1 ? sc.v[min(it.h, kMaxScaleHeads - 1)] : 1.f;
         const int32_t* trow = p.block_tables + (int64_t)b * p.M;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
             for (int a = 0; a < RPW; ++a) {
                 const int r = warp + kCcWarps * a, at = it.k.at + r / p.G;
                 sees_of[a] = r < R ? scored_range(p, q_row + r / p.G, at, it.k.len) : make_int2(0, 0);
-                slope[a] = p.slopes != nullptr && r < R ? -1.4426950408889634f * __ldg(p.slopes + it.h * p.G + r % p.G) : 0.f;
+                slope[a] = kBias && r < R ? -1.4426950408889634f * __ldg(p.slopes + it.h * p.G + r % p.G) : 0.f;
                 ref[a] = min(at, sees_of[a].y - 1);
             }
         }
@@ -270,8 +272,8 @@ __global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
                         float y = s[a][u] * qscale;
                         if constexpr (V::kScored) {
                             // (here the cap is tanhf's, whose error is a few last bits)
-                            if constexpr (V::kRule == kRuleCap) y = p.cap_out * tanhf(y);
-                            if constexpr (V::kRule != kRulePlain) y = fmaf(slope[a], fabsf((float)(pos - ref[a])), y);
+                            if constexpr (kCap) y = p.cap_out * tanhf(y);
+                            if constexpr (kBias) y = fmaf(slope[a], fabsf((float)(pos - ref[a])), y);
                         }
                         s[a][u] = there ? y : -INFINITY;
                         mx = fmaxf(mx, s[a][u]);

@@ -129,7 +129,9 @@ struct TtLayout {
     // q_full[QT], q_empty[QT], k_full[KS], k_empty[KS], v_full[VS] (CODES: not used), v_empty[VS], v_ready[VS],
     // raw_full[RS], raw_empty[RS], per stream s_full, p_full, pv_done, then x_ready, x_done and
     // piece_full[kRing], piece_empty[kRing], per stream mma_end
-    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing + 2;
+    // and (spread) a meeting per stream
+    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing + 2 + (V::kSpread ? 2 : 0);
+    static_assert(!V::kSpread || QT == 1, "spread rows have one query tile");
     static constexpr int ring = bars + nbars * 8;        // [kRing] records of pieces
     static constexpr int start = (ring + kRing * (int)sizeof(RecOf<V>) + 15) / 16 * 16;
     static constexpr int scratch = start + (int)sizeof(StartOf<V>);
@@ -249,46 +251,77 @@ __device__ __forceinline__ float cap_out_of(const P& p) {
     else return 0.f;
 }
 
-// A tile of raw scores of a row into powers of two: capped, cap_out tanh(s ..) =
-// cap_out - 2 cap_out / (1 + 2^(scale s)), or scaled; and biased by slope |d + position|.
-// (tanh is off by 2^-22 or so of the cap: the exponentials' and the reciprocal's last bits.)
-template <int RULE>
-__device__ __forceinline__ void score_rule(float (&s)[4][32], float scale, float cap_out, float slope, float d, bool ahead) {
+// ---- scored calls: the scores of 32 positions of a row ----
+
+// tanh(t) / t of |t| <= kTanhNear as a polynomial of t^2, fitted here (minimax, relative error 6e-7, and
+// 2^-21 of tanh with its roundings).  Most scores lie well inside their cap, and then a tile needs no
+// other special function than its weights' exponentials: with tanh = 1 - 2 / (1 + 2^z) everywhere, two more a
+// score, eight prompts took 364 us (a reciprocal shared by four scores: 442, as the products' chains are long).
+constexpr float kTanhNear = 0.75f;
+
+// cap_out tanh(k s) + add of two scores.
+struct Cap {
+    float k, z, out, c0, c1, c2, c3, c4;         // z = 2 log2(e) k
+    float hidden;      // a score whose polynomial is so far below all others (its t is -16) that its weight is 0
+    bool plain;        // factors for which that holds
+    __device__ __forceinline__ Cap(float k_, float out_)
+        : k(k_), z(2.f * 1.4426950408889634f * k_), out(out_), c0(out_ * 0.99999946f), c1(out_ * -0.3332825f),
+          c2(out_ * 0.13258983f), c3(out_ * -0.0500563f), c4(out_ * 0.012929631f), hidden(-16.f / k_),
+          plain(k_ > 1e-30f && out_ > 1e-4f && out_ < 1e25f) {}
+    __device__ __forceinline__ float2 near(float2 s, float2 add) const {
+        const float2 t = __fmul2_rn(s, make_float2(k, k)), w = __fmul2_rn(t, t);
+        float2 y = __ffma2_rn(make_float2(c4, c4), w, make_float2(c3, c3));
+        y = __ffma2_rn(y, w, make_float2(c2, c2));
+        y = __ffma2_rn(y, w, make_float2(c1, c1));
+        y = __ffma2_rn(y, w, make_float2(c0, c0));
+        return __ffma2_rn(t, y, add);
+    }
+    // off by 2^-20 of the cap or so: the exponential by 2^-22, the sum by 2^-24, the reciprocal by 2^-23, times 2
+    __device__ __forceinline__ float2 far(float2 s, float2 add) const {
+        const float2 e = __fmul2_rn(s, make_float2(z, z));
+        const float2 u = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.f, 1.f));
+        const float2 v = make_float2(rcp_approx(u.x), rcp_approx(u.y));
+        return __ffma2_rn(v, make_float2(-2.f * out, -2.f * out), __fadd2_rn(add, make_float2(out, out)));
+    }
+};
+
+// The largest and (WIDE) the smallest of 32 scores.
+template <bool WIDE>
+__device__ __forceinline__ void extremes(const float (&s)[32], float& top, float& low) {
+    float a = fmax3(s[0], s[1], s[2]), b = fmax3(s[3], s[4], s[5]);
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int e = 6; e < 30; e += 4) {
+        a = fmax3(a, s[e], s[e + 1]);
+        b = fmax3(b, s[e + 2], s[e + 3]);
+    }
+    top = fmaxf(top, fmax3(a, fmaxf(s[30], s[31]), b));
+    if constexpr (WIDE) {
+        a = fmin3(s[0], s[1], s[2]), b = fmin3(s[3], s[4], s[5]);
+#pragma unroll
+        for (int e = 6; e < 30; e += 4) {
+            a = fmin3(a, s[e], s[e + 1]);
+            b = fmin3(b, s[e + 2], s[e + 3]);
+        }
+        low = fminf(low, fmin3(a, fminf(s[30], s[31]), b));
+    }
+}
+
+// scale s + slope |p - ref| of positions first .. first + 31, d = first - ref: up to ref it is a line, of which
+// eight positions' steps are kept (`step`, -slope times 0 .. 7).
+__device__ __forceinline__ void bias_word(float (&s)[32], float scale, float slope, const float2 (&step)[4], float d,
+                                          bool ahead) {
+    if (!ahead) {
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-            float2 y;
-            if constexpr (RULE == kRuleCap) {
-                const float2 z = __fmul2_rn(make_float2(s[w][e], s[w][e + 1]), make_float2(scale, scale));
-                const float2 u = __fadd2_rn(make_float2(ex2(z.x), ex2(z.y)), make_float2(1.f, 1.f));
-                const float2 v = make_float2(rcp_approx(u.x), rcp_approx(u.y));
-                y = __ffma2_rn(v, make_float2(-2.f * cap_out, -2.f * cap_out), make_float2(cap_out, cap_out));
-            } else {
-                y = __fmul2_rn(make_float2(s[w][e], s[w][e + 1]), make_float2(scale, scale));
-            }
-            s[w][e] = y.x;
-            s[w][e + 1] = y.y;
+            const float base = -slope * (d + (float)(e & ~7));
+            const float2 b = __fadd2_rn(make_float2(base, base), step[(e & 7) >> 1]);
+            const float2 y = __ffma2_rn(make_float2(s[e], s[e + 1]), make_float2(scale, scale), b);
+            s[e] = y.x;
+            s[e + 1] = y.y;
         }
-    if (RULE == kRuleBias || slope != 0.f) {
-        if (!ahead) {
-            // no position lies past the row's own: |x| = -x
-            const float2 sl = make_float2(-slope, -slope);
+    } else {
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float at = (float)(w * 32 + e);
-                    const float2 y = __ffma2_rn(sl, make_float2(d + at, d + at + 1.f), make_float2(s[w][e], s[w][e + 1]));
-                    s[w][e] = y.x;
-                    s[w][e + 1] = y.y;
-                }
-        } else {
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) s[w][e] = fmaf(slope, fabsf(d + (float)(w * 32 + e)), s[w][e]);
-        }
+        for (int e = 0; e < 32; ++e) s[e] = fmaf(slope, fabsf(d + (float)e), s[e] * scale);
     }
 }
 
@@ -336,6 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t* piece_full = x_done + 1;
     uint64_t* piece_empty = piece_full + kRing;
     uint64_t* mma_end = piece_empty + kRing;
+    uint64_t* meet = mma_end + 2;                        // spread: the warps of a stream
     Rec* ring = reinterpret_cast<Rec*>(smem + L::ring);
     StartOf<V>* st = reinterpret_cast<StartOf<V>*>(smem + L::start);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::misc);
@@ -368,6 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(p_full(t), 4);
             mbar_init(pv_done(t), 1);
             mbar_init(&mma_end[t], 1);
+            if constexpr (V::kSpread) mbar_init(&meet[t], 4);
         }
         mbar_init(x_ready, kSoftW);
         mbar_init(x_done, kSoftW);
@@ -388,7 +423,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tree_begin(p, TN, cta, gridDim.x, st, reinterpret_cast<int64_t*>(smem + L::scratch));
     tc::fence_after_sync();
     const uint32_t tmem = (uint32_t)misc[0];
-    const int tok_tile = TM / p.G;                       // drafts of a query tile
+    const int tok_tile = (V::kSpread ? 32 : TM) / p.G;   // drafts of a query tile
     auto rows_tok_of = [](const Rec& it) {
         if constexpr (V::kScored) return it.k.rows_tok;
         else return it.rows_tok;
@@ -561,7 +596,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int prev = t == 0 ? asked : second;
                     if (prev == 0 || __shfl_sync(0xffffffffu, (int)mbar_test(&q_empty[t], (prev - 1) & 1), 0)) {
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(&q_full[t], (uint32_t)(2 * D * box_tok * p.G));
+                            constexpr int kCopies = V::kSpread ? 4 : 1;   // spread: in every quarter of the tile's rows
+                            mbar_arrive_expect_tx(&q_full[t], (uint32_t)(kCopies * 2 * D * box_tok * p.G));
+#pragma unroll
+                            for (int x = 0; x < kCopies; ++x)
                             if constexpr (CODES) {
 #pragma unroll
                                 for (int part = 0; part < 2; ++part) {   // hi rows, then lo rows
@@ -570,12 +608,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                         row = part * p.total_q + e.k.q_row;
                                     else
                                         row = (part * p.B + e.b) * p.max_q_len + e.tok0;
-                                    tma_load_3d_nohint(smem + L::q + part * (TM * D), &tm_q, 0, h_of(e) * p.G, row, &q_full[t]);
+                                    tma_load_3d_nohint(smem + L::q + part * (TM * D) + x * 32 * D, &tm_q, 0, h_of(e) * p.G, row, &q_full[t]);
                                 }
                             } else {
 #pragma unroll
                                 for (int cb = 0; cb < L::NC; ++cb)
-                                    tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128), &tm_q, cb * 64,
+                                    tma_load_3d_nohint(smem + L::q + t * L::QTILE + cb * (TM * 128) + x * 32 * 128, &tm_q, cb * 64,
                                                        h_of(e) * p.G, q_row_of(e) + t * tok_tile, &q_full[t]);
                             }
                         }
@@ -901,10 +939,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t sbase = tmem + lane_addr + t * L::SCOL;
         const uint32_t obase = tmem + lane_addr + L::OCOL + t * D;
         unsigned char* stage = smem + L::stage + warp * 4096;
-        const int tok = (QT == 2 ? t * tok_tile : 0) + r / p.G;
-        const bool row_fits = r < tok_tile * p.G;
+        const int tr = V::kSpread ? lane : r;            // row of the query tile
+        const int tok = (QT == 2 ? t * tok_tile : 0) + tr / p.G;
+        const bool row_fits = tr < tok_tile * p.G;
+        constexpr int kWords = V::kSpread ? 1 : 4;       // runs of 32 positions of a tile that a thread takes
+        auto word = [&](int w) { return V::kSpread ? quad : w; };
+        int met = 0;                                     // spread: meetings of the stream's warps
+        auto meeting = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&meet[t]);
+            const bool came = mbar_wait_warp(&meet[t], met & 1);
+            ++met;
+            if (!came && lane == 0) fail();
+            return came;
+        };
         const int g_inv = (65536 + p.G - 1) / p.G;       // row / G for rows below 128
-        float scale = V::kRule == kRuleCap ? cap_in_of(p) : p.scale_log2;
+        constexpr bool kCap = V::kRule == kRuleCap || V::kRule == kRuleCapBias;
+        constexpr bool kBias = V::kRule == kRuleBias || V::kRule == kRuleCapBias;
+        float scale = kCap ? cap_in_of(p) : p.scale_log2;
         const bool negate = V::kRule == kRulePlain && p.scale_log2 < 0.f;
         int4 rec = make_int4(0, 0, 0, 0);
         const float fill = negate ? INFINITY : -INFINITY;   // of a masked score: a weight of 0
@@ -923,17 +975,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int2 sees = make_int2(0, 0);                              // scored: the row's positions
             float slope = 0.f;                                        // and its bias, slope |p - ref|
             int ref = 0;
+            float2 step[4] = {};
             bool ahead = false;                                       // some row sees past its own position
             if constexpr (V::kScored) {
                 const int at = it.k.at + tok;
-                if (row_valid) sees = scored_range(p, q_row, at, it.k.len);
-                if constexpr (V::kRule != kRulePlain) {
-                    if (p.slopes != nullptr && row_valid) {
-                        slope = -1.4426950408889634f * __ldg(p.slopes + h_of(it) * p.G + r % p.G);
+                // (a row that is not there sees what the others do, so that it holds nobody up)
+                sees = row_valid ? scored_range(p, q_row, at, it.k.len) : make_int2(0, INT32_MAX);
+                if constexpr (kBias) {
+                    if (row_valid) {
+                        slope = -1.4426950408889634f * __ldg(p.slopes + h_of(it) * p.G + tr % p.G);
                         // distances from the nearest position that the row sees on its own side: a shift of
                         // all its scores, which keeps far rows' distances exact
                         ref = min(at, sees.y - 1);
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) step[e] = make_float2(-slope * (float)(2 * e), -slope * (float)(2 * e + 1));
                     ahead = __any_sync(0xffffffffu, row_valid && sees.y > at + 1);
                 }
             } else {
@@ -947,10 +1003,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int hs = min(h_of(it), kMaxScaleHeads - 1);
                 int64_t row;
                 if constexpr (V::kScored)
-                    row = (int64_t)q_row * p.H_q + h_of(it) * p.G + r % p.G;
+                    row = (int64_t)q_row * p.H_q + h_of(it) * p.G + tr % p.G;
                 else
-                    row = ((int64_t)it.b * p.max_q_len + it.tok0 + tok) * p.H_q + h_of(it) * p.G + r % p.G;
-                const float factor = V::kRule == kRuleCap ? cap_in_of(p) : p.scale_log2;
+                    row = ((int64_t)it.b * p.max_q_len + it.tok0 + tok) * p.H_q + h_of(it) * p.G + tr % p.G;
+                const float factor = kCap ? cap_in_of(p) : p.scale_log2;
                 scale = tree_factor(factor * sc.k[hs] * (row_valid ? __ldcg(p.q_inv + row) : 1.f));
                 v_scale = sc.v[hs];
             }
@@ -961,11 +1017,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 bool masked;
                 uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                 if constexpr (V::kScored) {
-                    masked = __any_sync(0xffffffffu, sees.x > k0 || sees.y < k0 + TN);
-                    if (masked) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) vis[w] = range_bits(sees.x, sees.y, k0 + 32 * w);
-                    }
+                    masked = __any_sync(0xffffffffu, sees.x > k0 + 32 * word(0) || sees.y < k0 + 32 * word(kWords - 1) + 32);
                 } else {
                     masked = k0 + TN > c;
                     if (warp_live && masked) {
@@ -978,7 +1030,140 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = false;
                     break;
                 }
-                if (warp_live) {
+                if constexpr (V::kScored) {
+                    if (warp_live) {
+                        tc::fence_after_sync();
+                        const uint32_t okm = okm_of[(g + tile_at(t, u)) & 15];
+                        masked |= okm != 0xffu;
+                        // the row in registers, or (spread) its quarter of a row
+                        float s[kWords][32];
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w) tc::ld_32cols(sbase + word(w) * 32, s[w]);
+                        tc::wait_ld();
+                        const Cap cap(scale, cap_out_of(p));
+                        bool near = false;
+                        float top = -INFINITY, low = INFINITY;
+                        if constexpr (kCap) {
+                            // (also over what is not seen, which costs at most the shorter way)
+#pragma unroll
+                            for (int w = 0; w < kWords; ++w) extremes<true>(s[w], top, low);
+                            near = cap.plain && __all_sync(0xffffffffu, fmaxf(top, -low) * scale <= kTanhNear);
+                        }
+                        // Scores that are final before the weights: biased ones, and capped ones of the longer way.
+                        const bool made = kBias || (kCap && !near);
+                        if constexpr (kCap) {
+                            if (made) {
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) {
+                                        const float2 x = make_float2(s[w][e], s[w][e + 1]), none = make_float2(0.f, 0.f);
+                                        const float2 y = kBias && near ? cap.near(x, none) : cap.far(x, none);
+                                        s[w][e] = y.x;
+                                        s[w][e + 1] = y.y;
+                                    }
+                            }
+                        }
+                        if constexpr (kBias) {
+#pragma unroll
+                            for (int w = 0; w < kWords; ++w)
+                                bias_word(s[w], kCap ? 1.f : scale, slope, step, (float)(k0 + 32 * word(w) - ref), ahead);
+                        }
+                        const float hide = V::kRule == kRuleCap && near ? cap.hidden : fill;
+                        if (masked) {
+#pragma unroll
+                            for (int w = 0; w < kWords; ++w) {
+                                const uint32_t v = range_bits(sees.x, sees.y, k0 + 32 * word(w)) &
+                                                   (((okm >> (2 * word(w))) & 1u ? 0xffffu : 0u) |
+                                                    ((okm >> (2 * word(w) + 1)) & 1u ? 0xffff0000u : 0u));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) s[w][e] = (v >> e) & 1u ? s[w][e] : hide;
+                            }
+                        }
+                        if (V::kRule != kRuleCap || made || masked) {
+                            top = -INFINITY;
+                            if (negate) {   // the largest scaled score is the smallest score's
+                                float no = 0.f;
+                                low = INFINITY;
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w) extremes<true>(s[w], no, low);
+                            } else {
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w) extremes<false>(s[w], top, low);
+                            }
+                        }
+                        float mt = V::kRule != kRulePlain ? top : negate ? low * scale : top * scale;
+                        if constexpr (V::kRule == kRuleCap) {
+                            // tanh keeps their order
+                            if (near)
+                                mt = masked && top == hide ? -INFINITY
+                                                           : cap.far(make_float2(top, top), make_float2(0.f, 0.f)).x;
+                        }
+                        float alpha = 1.f;
+                        if (m_ref == -INFINITY) {
+                            m_ref = mt;
+                        } else if (row_valid && mt > m_ref + kLazyMax) {
+                            alpha = ex2(m_ref - mt);
+                            m_ref = mt;
+                        }
+                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                            if (!mbar_wait_warp(pv_done(t), (gs + u - 1) & 1)) fail();
+                            tc::fence_after_sync();
+    #pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                float o[16];
+                                uint32_t w[16];
+                                tc::ld_16cols(obase + c, o);
+                                tc::wait_ld();
+    #pragma unroll
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                                st_16words(obase + c, w);
+                            }
+                            tc::wait_st();
+                        }
+                        l_run *= alpha;
+                        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+                        const float up = CODES ? kCodesUp - m_use : -m_use;
+                        const float2 nm2 = make_float2(up, up), sc2 = make_float2(scale, scale);
+                        float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                        make_float2(0.f, 0.f)};
+                        // the weights of positions 0-63 take columns 0-31, those of 64-127 columns 64-95
+                        const auto weigh = [&](auto score) {
+#pragma unroll
+                            for (int w = 0; w < kWords; ++w) {
+                                uint32_t pw[16];
+#pragma unroll
+                                for (int v = 0; v < 16; ++v) {
+                                    const float2 x = score(make_float2(s[w][2 * v], s[w][2 * v + 1]));
+                                    const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
+                                    ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
+                                    pw[v] = CODES ? pack_f16x2(e2.x, e2.y) : pack_bf16x2(e2.x, e2.y);
+                                }
+                                st_16words(sbase + (word(w) >> 1) * 64 + (word(w) & 1) * 16, pw);
+                            }
+                        };
+                        if constexpr (V::kRule == kRulePlain) {
+                            weigh([&](float2 x) { return __ffma2_rn(x, sc2, nm2); });
+                        } else if (V::kRule == kRuleCap && near) {
+                            weigh([&](float2 x) { return cap.near(x, nm2); });
+                        } else {
+                            weigh([&](float2 x) { return __fadd2_rn(x, nm2); });
+                        }
+                        if constexpr (V::kSpread) {          // the other positions are other quarters'
+                            const uint32_t zeros[16] = {};
+#pragma unroll
+                            for (int w = 1; w < 4; ++w) {
+                                const int x = (quad + w) & 3;
+                                st_16words(sbase + (x >> 1) * 64 + (x & 1) * 16, zeros);
+                            }
+                        }
+                        tc::wait_st();
+                        const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
+                        const float2 pst = __fadd2_rn(ps01, ps23);
+                        l_run += pst.x + pst.y;
+                        tc::fence_before_sync();
+                    }
+                } else if (warp_live) {
                     tc::fence_after_sync();
                     const uint32_t okm = okm_of[(g + tile_at(t, u)) & 15];
                     if (!masked && okm != 0xffu) masked = true;
@@ -993,9 +1178,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) tc::ld_32cols(sbase + w * 32, s[w]);
                     tc::wait_ld();
-                    if constexpr (V::kRule != kRulePlain) {
-                        score_rule<V::kRule>(s, scale, cap_out_of(p), slope, (float)(k0 - ref), ahead);
-                    }
                     if (masked) {
 #pragma unroll
                         for (int w = 0; w < 4; ++w)
@@ -1013,7 +1195,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             m8[e] = fmax3(m8[e], s[w][e + 8], s[w][e + 16]);
                         }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[3][e + 24]);
+                    for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[4 - 1][e + 24]);
                     float top = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
                     if (negate) {   // the largest scaled score is the smallest score's
                         top = INFINITY;
@@ -1022,7 +1204,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) top = fminf(top, s[w][e]);
                     }
-                    const float mt = V::kRule == kRulePlain ? top * scale : top;
+                    const float mt = top * scale;
                     float alpha = 1.f;
                     if (m_ref == -INFINITY) {
                         m_ref = mt;
@@ -1047,8 +1229,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     l_run *= alpha;
                     const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-                    const float rate = V::kRule == kRulePlain ? scale : 1.f;   // (scores that a rule made are in powers of two)
-                    const float2 sc2 = make_float2(rate, rate);
+                    const float2 sc2 = make_float2(scale, scale);
                     const float up = CODES ? kCodesUp - m_use : -m_use;
                     const float2 nm2 = make_float2(up, up);
                     float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
@@ -1059,8 +1240,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         uint32_t pw[16];
 #pragma unroll
                         for (int v = 0; v < 16; ++v) {
-                            const float2 sv = make_float2(s[w][2 * v], s[w][2 * v + 1]);
-                            const float2 x = V::kRule == kRulePlain ? __ffma2_rn(sv, sc2, nm2) : __fadd2_rn(sv, nm2);
+                            const float2 x = __ffma2_rn(make_float2(s[w][2 * v], s[w][2 * v + 1]), sc2, nm2);
                             const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
                             ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
                             pw[v] = CODES ? pack_f16x2(e2.x, e2.y) : pack_bf16x2(e2.x, e2.y);
@@ -1107,12 +1287,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     break;
                 }
                 const float2 a = ml[r], b = ml[TM + r];
-                const float mm = fmaxf(a.x, b.x);
+                float mm = fmaxf(a.x, b.x);
+                if constexpr (V::kSpread) {
+#pragma unroll
+                    for (int x = 1; x < 4; ++x) {
+                        const int at = ((quad + x) & 3) * 32 + lane;
+                        mm = fmax3(mm, ml[at].x, ml[TM + at].x);
+                    }
+                }
                 // a stream without a maximum has a sum and an O of 0, or of NaN, which has to stay
                 w0 = a.x == -INFINITY ? 1.f : ex2(a.x - mm);
                 w1 = b.x == -INFINITY ? 1.f : ex2(b.x - mm);
                 m_ref = mm;
                 l_run = w0 * a.y + w1 * b.y;
+                if constexpr (V::kSpread) {              // in one order in all quarters
+                    l_run = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float2 e = ml[y * TM + x * 32 + lane];
+                            l_run += (e.x == -INFINITY ? 1.f : ex2(e.x - mm)) * e.y;
+                        }
+                    }
+                }
             }
             tc::fence_after_sync();
             const bool both = QT == 1 && it.j1 - it.j0 > 1;    // stream 1 has an O
@@ -1125,7 +1323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int64_t wbase = (int64_t)slot_of_piece * p.rows + t0 * p.G;
             if (!whole) {
                 if (it.j0 == 0) rec = make_int4(q_row_of(it), h_of(it), it.last, rows_tok_of(it) * p.G);
-                if (row_valid && (QT == 2 || t == 0)) p.ws_ml[wbase + r] = make_float2(m_ref, l_run);
+                if (row_valid && (QT == 2 || t == 0) && (!V::kSpread || quad == 0)) p.ws_ml[wbase + tr] = make_float2(m_ref, l_run);
             }
             const float f = v_scale * (!whole ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run);
             w0 *= f;
@@ -1166,7 +1364,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int e4 = 0; e4 < 8; ++e4)
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((e4 ^ (lane & 7)) << 4)) =
                             make_float4(o[e4 * 4], o[e4 * 4 + 1], o[e4 * 4 + 2], o[e4 * 4 + 3]);
-                    if (wild && row_valid) {
+                    if (wild && row_valid && (!V::kSpread || quad == 0)) {
                         // drafts whose V row is not finite: what was zeroed for P V, added to the
                         // rows that see them
                         int pos0, pos1;
@@ -1205,6 +1403,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     }
+                    if constexpr (V::kSpread) {
+                        // the quarters' parts of a row, added up: 8 rows a warp
+                        if (!meeting()) {
+                            ok = false;
+                            break;
+                        }
+                        const unsigned char* from = smem + L::stage + t * 4 * 4096;
+                        const auto sum_at = [&](int rr, int cc) {
+                            const int at = rr * 128 + ((cc ^ (rr & 7)) << 4);
+                            float4 a = ld_shared_f4(from + at);
+#pragma unroll
+                            for (int x = 1; x < 4; ++x) {
+                                const float4 b = ld_shared_f4(from + x * 4096 + at);
+                                a.x += b.x;
+                                a.y += b.y;
+                                a.z += b.z;
+                                a.w += b.w;
+                            }
+                            return a;
+                        };
+                        if (whole) {
+                            const int row = quad * 8 + (lane >> 2), cc = (lane & 3) * 2;
+                            const float4 a = sum_at(row, cc), b = sum_at(row, cc + 1);
+                            if (row < live_rows) {
+                                const int dr = (row * g_inv) >> 16;
+                                const int64_t at = (int64_t)(tile_row + dr) * p.H_q + h_of(it) * p.G + row - dr * p.G;
+                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at * D + col + cc * 4) =
+                                    make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                                               pack_bf16x2(b.z, b.w));
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int row = quad * 8 + k * 4 + (lane >> 3), cc = lane & 7;
+                                const float4 a = sum_at(row, cc);
+                                if (row < live_rows)
+                                    *reinterpret_cast<float4*>(p.ws_o + (wbase + row) * D + col + cc * 4) = a;
+                            }
+                        }
+                        if (!meeting()) {
+                            ok = false;
+                            break;
+                        }
+                        continue;
+                    }
                     __syncwarp();
                     if (whole) {
 #pragma unroll 2
@@ -1234,6 +1477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                 }
             }
+            if (!ok) break;
             // O (and the streams' sums) are read: the next piece may overwrite them
             tc::fence_before_sync();
             if constexpr (QT == 1) {
@@ -1364,7 +1608,7 @@ cudaError_t launch_after(Kern kern, int ctas, int smem, cudaStream_t stream, con
 
 template <typename V, int D, int QT>
 cudaError_t launch_bf16(const typename V::Params& p, int ctas, cudaStream_t stream) {
-    const int tok = TM / p.G;
+    const int tok = (V::kSpread ? 32 : TM) / p.G;
     const int box_tok = p.max_q_len < tok ? p.max_q_len : tok;   // drafts of a query tile's box
     CUtensorMap tq, tk, tv;
     const uint64_t slots = (uint64_t)p.N * p.P;
@@ -1407,7 +1651,7 @@ cudaError_t launch_bf16(const typename V::Params& p, int ctas, cudaStream_t stre
 
 template <typename V, int D>
 cudaError_t launch_codes(typename V::Params p, const HeadScales& sc, void* prep, int ctas, cudaStream_t stream) {
-    const int tok = TM / p.G;
+    const int tok = (V::kSpread ? 32 : TM) / p.G;
     const int box_tok = p.max_q_len < tok ? p.max_q_len : tok;
     const uint64_t drafts = V::kScored ? (uint64_t)p.total_q : (uint64_t)p.B * p.max_q_len;
     const uint64_t slots = (uint64_t)p.N * p.P, row = (uint64_t)p.H_kv * D;
@@ -1450,9 +1694,11 @@ cudaError_t launch_tc(const typename V::Params& p, const wf_pool_desc& pool, voi
         const HeadScales sc = head_scales(pool);
         return d128 ? launch_codes<V, 128>(p, sc, prep, ctas, stream) : launch_codes<V, 64>(p, sc, prep, ctas, stream);
     }
-    if (p.rows == TM)
-        return d128 ? launch_bf16<V, 128, 1>(p, ctas, stream) : launch_bf16<V, 64, 1>(p, ctas, stream);
-    return d128 ? launch_bf16<V, 128, 2>(p, ctas, stream) : launch_bf16<V, 64, 2>(p, ctas, stream);
+    if constexpr (!V::kSpread) {
+        if (p.rows != TM)
+            return d128 ? launch_bf16<V, 128, 2>(p, ctas, stream) : launch_bf16<V, 64, 2>(p, ctas, stream);
+    }
+    return d128 ? launch_bf16<V, 128, 1>(p, ctas, stream) : launch_bf16<V, 64, 1>(p, ctas, stream);
 }
 
 }  // namespace

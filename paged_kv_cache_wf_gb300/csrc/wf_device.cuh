@@ -172,10 +172,16 @@ __device__ __forceinline__ bool item_walk_find(ItemWalk& w, int64_t item, const 
     }
 }
 
-// max(a, b, c) in one instruction.
+// max(a, b, c) and min(a, b, c) in one instruction.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+    float y;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
