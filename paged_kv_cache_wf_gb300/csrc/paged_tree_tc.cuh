@@ -67,6 +67,9 @@ constexpr float kLazyMax = 8.f;   // rescale O only when a row's maximum grows b
 // factor 2^-14 and 2^-25, which a long tail of small weights would feel).
 constexpr float kCodesUp = 7.f;
 static_assert(kLazyMax + kCodesUp <= 15.f, "fp16 weights overflow");
+// Scored calls over bf16 pools: bf16 weights and fp32 sums have the range for more, and then hardly any tile
+// after a row's first rescales (with 8 some row of a warp did every few tiles, a sixth of the time).
+constexpr float kLazyFar = 40.f;
 constexpr int kSoftW = 8, kKW = 8, kVW = 9, kWalkW = 10, kMmaW = 11, kFinW = 13, kFin = 3;
 constexpr int kTcThreads = (kFinW + kFin) * 32;
 constexpr int kSoftRegs = 192, kOtherRegs = 64;
@@ -129,8 +132,9 @@ struct TtLayout {
     // q_full[QT], q_empty[QT], k_full[KS], k_empty[KS], v_full[VS] (CODES: not used), v_empty[VS], v_ready[VS],
     // raw_full[RS], raw_empty[RS], per stream s_full, p_full, pv_done, then x_ready, x_done and
     // piece_full[kRing], piece_empty[kRing], per stream mma_end
-    // and (spread) a meeting per stream
-    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing + 2 + (V::kSpread ? 2 : 0);
+    // and (spread) a meeting per stream, or (half tiles) s_full, p_full and pv_done of each stream's second half
+    static constexpr bool kHalf = V::kScored && !V::kSpread;
+    static constexpr int nbars = 2 * QT + 2 * NSLOT + VS + 2 * RS + 6 + 2 + 2 * kRing + 2 + (V::kSpread ? 2 : kHalf ? 6 : 0);
     static_assert(!V::kSpread || QT == 1, "spread rows have one query tile");
     static constexpr int ring = bars + nbars * 8;        // [kRing] records of pieces
     static constexpr int start = (ring + kRing * (int)sizeof(RecOf<V>) + 15) / 16 * 16;
@@ -288,22 +292,21 @@ struct Cap {
 // The largest and (WIDE) the smallest of 32 scores.
 template <bool WIDE>
 __device__ __forceinline__ void extremes(const float (&s)[32], float& top, float& low) {
-    float a = fmax3(s[0], s[1], s[2]), b = fmax3(s[3], s[4], s[5]);
+    float a[4], b[4];
 #pragma unroll
-    for (int e = 6; e < 30; e += 4) {
-        a = fmax3(a, s[e], s[e + 1]);
-        b = fmax3(b, s[e + 2], s[e + 3]);
+    for (int x = 0; x < 4; ++x) {
+        a[x] = fmaxf(s[x], s[x + 4]);
+        if constexpr (WIDE) b[x] = fminf(s[x], s[x + 4]);
     }
-    top = fmaxf(top, fmax3(a, fmaxf(s[30], s[31]), b));
-    if constexpr (WIDE) {
-        a = fmin3(s[0], s[1], s[2]), b = fmin3(s[3], s[4], s[5]);
 #pragma unroll
-        for (int e = 6; e < 30; e += 4) {
-            a = fmin3(a, s[e], s[e + 1]);
-            b = fmin3(b, s[e + 2], s[e + 3]);
+    for (int e = 8; e < 32; e += 8)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            a[x] = fmax3(a[x], s[e + x], s[e + x + 4]);
+            if constexpr (WIDE) b[x] = fmin3(b[x], s[e + x], s[e + x + 4]);
         }
-        low = fminf(low, fmin3(a, fminf(s[30], s[31]), b));
-    }
+    top = fmaxf(top, fmax3(a[0], a[1], fmaxf(a[2], a[3])));
+    if constexpr (WIDE) low = fminf(low, fmin3(b[0], b[1], fminf(b[2], b[3])));
 }
 
 // scale s + slope |p - ref| of positions first .. first + 31, d = first - ref: up to ref it is a line, of which
@@ -370,6 +373,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t* piece_empty = piece_full + kRing;
     uint64_t* mma_end = piece_empty + kRing;
     uint64_t* meet = mma_end + 2;                        // spread: the warps of a stream
+    // A scored call's softmax takes a tile in halves of 64 positions, a half's S product being issued while
+    // the other's softmax runs: its columns of S are free once P V of the tile before has them read.
+    constexpr bool kHalf = L::kHalf;
+    // Each half has barriers of its own: a wait tells no phase from the one two before it, and both halves'
+    // products may be under way.
+    auto s_full_of = [&](int t, int h) { return h == 0 ? s_full(t) : meet + 3 * t; };
+    auto p_full_of = [&](int t, int h) { return h == 0 ? p_full(t) : meet + 3 * t + 1; };
+    auto pv_done_of = [&](int t, int h) { return h == 0 ? pv_done(t) : meet + 3 * t + 2; };
     Rec* ring = reinterpret_cast<Rec*>(smem + L::ring);
     StartOf<V>* st = reinterpret_cast<StartOf<V>*>(smem + L::start);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::misc);
@@ -403,6 +414,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(pv_done(t), 1);
             mbar_init(&mma_end[t], 1);
             if constexpr (V::kSpread) mbar_init(&meet[t], 4);
+            if constexpr (kHalf) {
+                mbar_init(s_full_of(t, 1), 1);
+                mbar_init(p_full_of(t, 1), 4);
+                mbar_init(pv_done_of(t, 1), 1);
+            }
         }
         mbar_init(x_ready, kSoftW);
         mbar_init(x_done, kSoftW);
@@ -506,15 +522,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int32_t* trow = p.block_tables + (int64_t)b_of(it) * p.M;
                 const int h = h_of(it), kend = end_of(it);
                 const int kbegin = V::kScored ? begin_of(it) - 15 : 0;   // of a box that a row sees some of
-                int pos = at_of(it) + it.j0 * TN + lane * 16;
+                // a scored piece's tiles from the last one down (see the softmax)
+                constexpr int kOn = V::kScored ? -TN : TN;
+                int pos = at_of(it) + (V::kScored ? it.j1 - 1 : it.j0) * TN + lane * 16;
                 int real = it.j1 - it.j0;        // what is left of the piece, and of its tiles in the ring
                 int left = ring_tiles(real);
                 int blk_next = lane < 8 && pos < kend && pos >= kbegin ? __ldg(trow + pos / p.P) : 0;
 #pragma unroll 1
-                for (; left > 0; --left, --real, pos += TN, ++g) {
+                for (; left > 0; --left, --real, pos += kOn, ++g) {
                     const int blk = blk_next;
                     const bool in = lane < 8 && real > 0 && pos < kend && pos >= kbegin;
-                    if (real > 1 && lane < 8 && pos + TN < kend && pos + TN >= kbegin) blk_next = __ldg(trow + (pos + TN) / p.P);
+                    if (real > 1 && lane < 8 && pos + kOn < kend && pos + kOn >= kbegin) blk_next = __ldg(trow + (pos + kOn) / p.P);
                     if (!mbar_wait_warp(&empty[x], par)) {
                         if (lane == 0) fail();
                         ok = false;
@@ -657,7 +675,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int kbegin = begin_of(it), at0 = at_of(it);
 #pragma unroll 1
                 for (int j = it.j0, end = j + ring_tiles(j1 - j); j < end; ++j) {
-                    const int k0 = at0 + j * TN;
+                    const int k0 = at0 + (V::kScored ? it.j0 + j1 - 1 - j : j) * TN;
                     if (CODES ? !mbar_wait_warp(&raw_full[rx], rpar) || !mbar_wait_warp(&v_empty[x], par ^ 1)
                               : !mbar_wait_warp(&v_full[x], par)) {
                         if (lane == 0) fail();
@@ -811,7 +829,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // overwrites the columns P(u) lives in, and the tensor core executes one thread's
             // products in issue order.  One issuer for both streams was the bound at 16 products a
             // tile and stream.
-            constexpr uint32_t idS = CODES ? tc::idesc_e4m3_f32(TM, TN, 0, 0) : tc::idesc_bf16_f32(TM, TN, 0, 0);
+            constexpr int kSN = kHalf ? TN / 2 : TN;
+            constexpr uint32_t idS = CODES ? tc::idesc_e4m3_f32(TM, kSN, 0, 0) : tc::idesc_bf16_f32(TM, kSN, 0, 0);
             constexpr uint32_t idO = CODES ? tc::idesc_f16_f32(TM, D, 0, 1) : tc::idesc_bf16_f32(TM, D, 0, 1);
             // An MMA takes its operands from uniform registers.  The slots and parities here are the
             // same in all lanes, and are kept so that the compiler sees it: otherwise each of a
@@ -871,6 +890,75 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!need(&q_full[tq], qpar)) break;
                 qpar ^= 1;
                 if (nt == 0 && lane == 0) mbar_arrive(&q_empty[tq]);
+                if constexpr (kHalf) {
+                    // S(0) in both halves, then P(u) V and S(u + 1) half by half
+                    const auto issue_s = [&](int h, bool last) {
+                        if (elect_one()) {
+                            const uint32_t kd = (uint32_t)kdesc + ((kx * L::KTILE + h * (L::KTILE / 2)) >> 4), qd = (uint32_t)qdesc;
+                            const uint32_t khi = (uint32_t)(kdesc >> 32), qhi = (uint32_t)(qdesc >> 32);
+                            if constexpr (CODES) {       // the two parts of q, one after the other
+#pragma unroll
+                                for (int x = 0; x < 2 * D / 32; ++x) {
+                                    const int part = x / (D / 32), kk = x % (D / 32);
+                                    mma<2>(dS + h * 64, qd + ((part * TM * D + kk * 32) >> 4), qhi, kd + ((kk * 32) >> 4), khi,
+                                           idS, x > 0 ? 1u : 0u);
+                                }
+                            } else {
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
+                                    const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
+                                    mma<0>(dS + h * 64, qd + (qoff >> 4), qhi, kd + (koff >> 4), khi, idS, kk > 0 ? 1u : 0u);
+                                }
+                            }
+                            tc::commit(s_full_of(t, h));
+                            if (h == 1) {
+                                tc::commit(&k_empty[kx]);
+                                if (last) tc::commit(&q_empty[tq]);
+                            }
+                        }
+                        __syncwarp();
+                    };
+                    const auto next_k = [&]() {
+#pragma unroll
+                        for (int k = 0; k < (QT == 1 ? 2 : 1); ++k) step(kx, kpar, L::KS);
+                    };
+                    if (nt > 0 && need(&k_full[kx], kpar)) {
+                        tc::fence_after_sync();
+                        issue_s(0, false);
+                        issue_s(1, nt == 1);
+                        next_k();
+                    }
+#pragma unroll 1
+                    for (int u = 0; u < nt && ok; ++u) {
+                        if (!need(&v_ready[vx], vpar)) break;
+                        const uint32_t vd = (uint32_t)vdesc + ((vx * L::VTILE) >> 4);
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            if (!need(p_full_of(t, h), ppar)) break;
+                            tc::fence_after_sync();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int kk = 0; kk < TN / 32; ++kk)
+                                    mma<1>(dO, dS + h * 64 + kk * 8, 0u, vd + (((h * (TN / 32) + kk) * 2 * L::ATOM) >> 4),
+                                           (uint32_t)(vdesc >> 32), idO, (u > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                                if (h == 1) tc::commit(&v_empty[vx]);
+                                tc::commit(pv_done_of(t, h));
+                            }
+                            __syncwarp();
+                            if (u + 1 < nt) {
+                                if (h == 0 && !need(&k_full[kx], kpar)) break;
+                                tc::fence_after_sync();
+                                issue_s(h, u + 2 == nt);
+                            }
+                        }
+                        if (!ok) break;
+                        ppar ^= 1;
+                        if (u + 1 < nt) next_k();
+#pragma unroll
+                        for (int k = 0; k < (QT == 1 ? 2 : 1); ++k) step(vx, vpar, L::VS);
+                    }
+                } else {
 #pragma unroll 1
                 for (int u = -1; u < nt && ok; ++u) {
                     // P V of step u ...
@@ -919,6 +1007,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         __syncwarp();
                     }
                 }
+                }
                 if (QT == 1 && ok && 2 * nt + t < ring_tiles(all)) {   // stream 1's empty tile: hand it back
                     if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
                     if (need(&v_ready[vx], vpar) && lane == 0) mbar_arrive(&v_empty[vx]);
@@ -942,8 +1031,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tr = V::kSpread ? lane : r;            // row of the query tile
         const int tok = (QT == 2 ? t * tok_tile : 0) + tr / p.G;
         const bool row_fits = tr < tok_tile * p.G;
-        constexpr int kWords = V::kSpread ? 1 : 4;       // runs of 32 positions of a tile that a thread takes
-        auto word = [&](int w) { return V::kSpread ? quad : w; };
+        constexpr int kWords = V::kSpread ? 1 : kHalf ? 2 : 4;   // runs of 32 positions that a thread takes at once
+        constexpr int kSteps = kHalf ? 2 : 1;            // and how often in a tile
+        int hf = 0;                                      // half tiles: which
+        auto word = [&](int w) { return V::kSpread ? quad : kHalf ? 2 * hf + w : w; };
         int met = 0;                                     // spread: meetings of the stream's warps
         auto meeting = [&]() {
             __syncwarp();
@@ -976,6 +1067,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float slope = 0.f;                                        // and its bias, slope |p - ref|
             int ref = 0;
             float2 step[4] = {};
+            int all_lo = 0, all_hi = 0;                               // positions that all of the warp's rows see
             bool ahead = false;                                       // some row sees past its own position
             if constexpr (V::kScored) {
                 const int at = it.k.at + tok;
@@ -992,6 +1084,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int e = 0; e < 4; ++e) step[e] = make_float2(-slope * (float)(2 * e), -slope * (float)(2 * e + 1));
                     ahead = __any_sync(0xffffffffu, row_valid && sees.y > at + 1);
                 }
+                all_lo = __reduce_max_sync(0xffffffffu, sees.x);
+                all_hi = __reduce_min_sync(0xffffffffu, sees.y);
             } else {
                 c = it.c;
                 n = it.n;
@@ -1011,13 +1105,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 v_scale = sc.v[hs];
             }
             float m_ref = -INFINITY, l_run = 0.f;
-            for (int u = 0; u < nt; ++u) {
-                const int k0 = at0 + (j0 + tile_at(t, u)) * TN;
+#pragma unroll 1
+            for (int su = 0; su < nt * kSteps; ++su) {
+                const int u = su / kSteps;
+                hf = su % kSteps;
+                // Scored: the last tile first.  Where a bias grows towards a row's own position its maximum is there, and
+                // later tiles do not move it (from the first on they did almost each time: prompts with slopes 294 us).
+                const int k0 = at0 + (V::kScored ? it.j1 - 1 - tile_at(t, u) : j0 + tile_at(t, u)) * TN;
                 // positions of this tile that the row sees, when it is not all of them
                 bool masked;
                 uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                 if constexpr (V::kScored) {
-                    masked = __any_sync(0xffffffffu, sees.x > k0 + 32 * word(0) || sees.y < k0 + 32 * word(kWords - 1) + 32);
+                    masked = all_lo > k0 + 32 * word(0) || all_hi < k0 + 32 * word(kWords - 1) + 32;
                 } else {
                     masked = k0 + TN > c;
                     if (warp_live && masked) {
@@ -1025,7 +1124,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int w = 0; w < 4; ++w) vis[w] = row_valid ? mask_bits(mrow, p.W, k0 + 32 * w - c, n) : 0u;
                     }
                 }
-                if (!mbar_wait_warp(s_full(t), (gs + u) & 1)) {
+                if (!mbar_wait_warp(kHalf ? s_full_of(t, hf) : s_full(t), (gs + u) & 1)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
@@ -1035,7 +1134,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc::fence_after_sync();
                         const uint32_t okm = okm_of[(g + tile_at(t, u)) & 15];
                         masked |= okm != 0xffu;
-                        // the row in registers, or (spread) its quarter of a row
+                        uint32_t seen[kWords];
+                        bool idle = false;              // none of it is seen by the warp's rows
+                        if (masked) {
+                            uint32_t some = 0;
+#pragma unroll
+                            for (int w = 0; w < kWords; ++w) {
+                                seen[w] = range_bits(sees.x, sees.y, k0 + 32 * word(w)) &
+                                          (((okm >> (2 * word(w))) & 1u ? 0xffffu : 0u) |
+                                           ((okm >> (2 * word(w) + 1)) & 1u ? 0xffff0000u : 0u));
+                                some |= seen[w];
+                            }
+                            idle = __all_sync(0xffffffffu, some == 0);
+                        }
+                        if (idle) {
+                            const uint32_t zeros[16] = {};
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                if (!kHalf || w / 2 == hf) st_16words(sbase + (w >> 1) * 64 + (w & 1) * 16, zeros);
+                            tc::wait_st();
+                            tc::fence_before_sync();
+                        } else {
+                        // the row's positions in registers
                         float s[kWords][32];
 #pragma unroll
                         for (int w = 0; w < kWords; ++w) tc::ld_32cols(sbase + word(w) * 32, s[w]);
@@ -1052,17 +1172,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // Scores that are final before the weights: biased ones, and capped ones of the longer way.
                         const bool made = kBias || (kCap && !near);
                         if constexpr (kCap) {
-                            if (made) {
+                            const auto capped = [&](auto f) {
 #pragma unroll
                                 for (int w = 0; w < kWords; ++w)
 #pragma unroll
                                     for (int e = 0; e < 32; e += 2) {
-                                        const float2 x = make_float2(s[w][e], s[w][e + 1]), none = make_float2(0.f, 0.f);
-                                        const float2 y = kBias && near ? cap.near(x, none) : cap.far(x, none);
+                                        const float2 y = f(make_float2(s[w][e], s[w][e + 1]), make_float2(0.f, 0.f));
                                         s[w][e] = y.x;
                                         s[w][e + 1] = y.y;
                                     }
-                            }
+                            };
+                            if (!near)
+                                capped([&](float2 x, float2 none) { return cap.far(x, none); });
+                            else if (kBias)
+                                capped([&](float2 x, float2 none) { return cap.near(x, none); });
                         }
                         if constexpr (kBias) {
 #pragma unroll
@@ -1073,11 +1196,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (masked) {
 #pragma unroll
                             for (int w = 0; w < kWords; ++w) {
-                                const uint32_t v = range_bits(sees.x, sees.y, k0 + 32 * word(w)) &
-                                                   (((okm >> (2 * word(w))) & 1u ? 0xffffu : 0u) |
-                                                    ((okm >> (2 * word(w) + 1)) & 1u ? 0xffff0000u : 0u));
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) s[w][e] = (v >> e) & 1u ? s[w][e] : hide;
+                                for (int e = 0; e < 32; ++e) s[w][e] = (seen[w] >> e) & 1u ? s[w][e] : hide;
                             }
                         }
                         if (V::kRule != kRuleCap || made || masked) {
@@ -1097,17 +1216,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             // tanh keeps their order
                             if (near)
                                 mt = masked && top == hide ? -INFINITY
-                                                           : cap.far(make_float2(top, top), make_float2(0.f, 0.f)).x;
+                                                           : cap.near(make_float2(top, top), make_float2(0.f, 0.f)).x;
                         }
                         float alpha = 1.f;
                         if (m_ref == -INFINITY) {
                             m_ref = mt;
-                        } else if (row_valid && mt > m_ref + kLazyMax) {
+                        } else if (row_valid && mt > m_ref + (CODES ? kLazyMax : kLazyFar)) {
                             alpha = ex2(m_ref - mt);
                             m_ref = mt;
                         }
                         if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                            if (!mbar_wait_warp(pv_done(t), (gs + u - 1) & 1)) fail();
+                            if (!mbar_wait_warp(kHalf ? pv_done_of(t, hf ^ 1) : pv_done(t),
+                                                (kHalf && hf == 1 ? gs + u : gs + u - 1) & 1))
+                                fail();
                             tc::fence_after_sync();
     #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
@@ -1162,6 +1283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const float2 pst = __fadd2_rn(ps01, ps23);
                         l_run += pst.x + pst.y;
                         tc::fence_before_sync();
+                        }
                     }
                 } else if (warp_live) {
                     tc::fence_after_sync();
@@ -1255,16 +1377,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 __syncwarp();
                 // the first P of a piece lets P V overwrite O, which the last piece's join reads
-                if (QT == 1 && u == 0 && i > 0 && !mbar_wait_warp(x_done, (i - 1) & 1)) {
+                if (QT == 1 && su == 0 && i > 0 && !mbar_wait_warp(x_done, (i - 1) & 1)) {
                     if (lane == 0) fail();
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive(p_full(t));
+                if (lane == 0) mbar_arrive(kHalf ? p_full_of(t, hf) : p_full(t));
             }
             if (!ok) break;
             // ---- epilogue: the rows, or this piece of them ------------------------------
-            if (nt > 0 && !mbar_wait_warp(pv_done(t), (gs + nt - 1) & 1)) {
+            if (nt > 0 && !mbar_wait_warp(kHalf ? pv_done_of(t, 1) : pv_done(t), (gs + nt - 1) & 1)) {
                 if (lane == 0) fail();
                 break;
             }
