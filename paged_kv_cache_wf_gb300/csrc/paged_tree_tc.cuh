@@ -257,26 +257,22 @@ __device__ __forceinline__ float cap_out_of(const P& p) {
 
 // ---- scored calls: the scores of 32 positions of a row ----
 
-// tanh(t) / t of |t| <= kTanhNear as a polynomial of t^2, fitted here (minimax, relative error 6e-7, and
-// 2^-21 of tanh with its roundings).  Most scores lie well inside their cap, and then a tile needs no
-// other special function than its weights' exponentials: with tanh = 1 - 2 / (1 + 2^z) everywhere, two more a
-// score, eight prompts took 364 us (a reciprocal shared by four scores: 442, as the products' chains are long).
-constexpr float kTanhNear = 0.75f;
+// tanh(t) of |t| <= kTanhNear as t times a polynomial of t^2, fitted here for the least largest error, 2^-20.1.
+// Most scores lie well inside their cap, and then a tile needs no other special function than its weights'
+// exponentials (eight prompts: 303 us with two more coefficients and a limit of 0.75, 343 with tanh =
+// 1 - 2 / (1 + 2^z) for all scores, and a reciprocal shared by four of them was slower still).
+constexpr float kTanhNear = 0.38f;
 
 // cap_out tanh(k s) + add of two scores.
 struct Cap {
-    float k, z, out, c0, c1, c2, c3, c4;         // z = 2 log2(e) k
-    float hidden;      // a score whose polynomial is so far below all others (its t is -16) that its weight is 0
-    bool plain;        // factors for which that holds
+    float k, z, out, c0, c1, c2;                 // z = 2 log2(e) k
     __device__ __forceinline__ Cap(float k_, float out_)
-        : k(k_), z(2.f * 1.4426950408889634f * k_), out(out_), c0(out_ * 0.99999946f), c1(out_ * -0.3332825f),
-          c2(out_ * 0.13258983f), c3(out_ * -0.0500563f), c4(out_ * 0.012929631f), hidden(-16.f / k_),
-          plain(k_ > 1e-30f && out_ > 1e-4f && out_ < 1e25f) {}
+        : k(k_), z(2.f * 1.4426950408889634f * k_), out(out_), c0(out_ * 0.99998426f), c1(out_ * -0.33244488f),
+          c2(out_ * 0.12068124f) {}
+    // (of -infinity, for k > 0: -infinity, as the last coefficient is positive)
     __device__ __forceinline__ float2 near(float2 s, float2 add) const {
         const float2 t = __fmul2_rn(s, make_float2(k, k)), w = __fmul2_rn(t, t);
-        float2 y = __ffma2_rn(make_float2(c4, c4), w, make_float2(c3, c3));
-        y = __ffma2_rn(y, w, make_float2(c2, c2));
-        y = __ffma2_rn(y, w, make_float2(c1, c1));
+        float2 y = __ffma2_rn(make_float2(c2, c2), w, make_float2(c1, c1));
         y = __ffma2_rn(y, w, make_float2(c0, c0));
         return __ffma2_rn(t, y, add);
     }
@@ -1167,7 +1163,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             // (also over what is not seen, which costs at most the shorter way)
 #pragma unroll
                             for (int w = 0; w < kWords; ++w) extremes<true>(s[w], top, low);
-                            near = cap.plain && __all_sync(0xffffffffu, fmaxf(top, -low) * scale <= kTanhNear);
+                            near = scale > 0.f && __all_sync(0xffffffffu, fmaxf(top, -low) * scale <= kTanhNear);
                         }
                         // Scores that are final before the weights: biased ones, and capped ones of the longer way.
                         const bool made = kBias || (kCap && !near);
@@ -1192,11 +1188,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             for (int w = 0; w < kWords; ++w)
                                 bias_word(s[w], kCap ? 1.f : scale, slope, step, (float)(k0 + 32 * word(w) - ref), ahead);
                         }
-                        const float hide = V::kRule == kRuleCap && near ? cap.hidden : fill;
                         if (masked) {
 #pragma unroll
                             for (int w = 0; w < kWords; ++w) {
-                                for (int e = 0; e < 32; ++e) s[w][e] = (seen[w] >> e) & 1u ? s[w][e] : hide;
+                                for (int e = 0; e < 32; ++e) s[w][e] = (seen[w] >> e) & 1u ? s[w][e] : fill;
                             }
                         }
                         if (V::kRule != kRuleCap || made || masked) {
@@ -1214,9 +1209,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         float mt = V::kRule != kRulePlain ? top : negate ? low * scale : top * scale;
                         if constexpr (V::kRule == kRuleCap) {
                             // tanh keeps their order
-                            if (near)
-                                mt = masked && top == hide ? -INFINITY
-                                                           : cap.near(make_float2(top, top), make_float2(0.f, 0.f)).x;
+                            if (near) mt = cap.near(make_float2(top, top), make_float2(0.f, 0.f)).x;
                         }
                         float alpha = 1.f;
                         if (m_ref == -INFINITY) {

@@ -97,9 +97,9 @@ class Scored(R.Tree):
                 more = np.zeros(self.H_q)
                 if self.cap:
                     # tanh does not grow errors.  The tensor cores' 1 - 2 / (1 + 2^z): 2^z is off by 2^-22 and z's own
-                    # rounding (0.45 2^-24 of a tanh at most), the sum by 2^-24, the reciprocal by 2^-23 and five roundings
-                    # of the products that share it, so 12 2^-24 of a number below 1, times 2 cap, and the result is
-                    # rounded: below cap 2^-19.  tanhf: 2^-22, and two roundings.
+                    # rounding (0.45 2^-24 of a tanh at most), the sum by 2^-24, the reciprocal by 2^-23, of a number below 1
+                    # and times 2 cap, and the result is rounded: below cap 2^-20.  Their polynomial of small arguments:
+                    # 2^-20.1 and six roundings of at most 0.4 2^-24, below cap 2^-19.  tanhf: 2^-22, and two roundings.
                     s = self.cap * np.tanh(s / self.cap)
                     more += self.cap * 2.0 ** (-19 if tc else -21)
                 if self.slopes is not None:
