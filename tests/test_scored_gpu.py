@@ -312,6 +312,20 @@ def test_pool_rows_past_32_bits_of_offset():
         del kp, vp, d
 
 
+@pytest.mark.parametrize("shape", ["decode", "few", "prompts", "fp8 prompts", "fp32 prompts"])
+def test_buffers_aligned_to_16_bytes(shape):
+    t = make(shape, "all", seed=22)
+    d = t.device()
+    for name in ("q", "out"):
+        x = torch.empty(d[name].numel() + 16 // d[name].element_size(), dtype=d[name].dtype, device="cuda")
+        x = x[16 // x.element_size():].view(d[name].shape)
+        d[name] = x.copy_(d[name])
+    ws = torch.cat([t.workspace(), torch.zeros(16, dtype=torch.uint8, device="cuda")])[16:]
+    assert d["out"].data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    t.run(d, ws)
+    check(t, d)
+
+
 def test_in_a_graph_beside_other_streams():
     """Two captured calls with workspaces of their own, replayed at once on two streams beside an eager one."""
     a, b, c = make("decode", "cap", seed=19), make("prompts", "all", seed=20), make("fp8 prompts", "window", seed=21)
