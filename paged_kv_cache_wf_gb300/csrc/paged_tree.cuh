@@ -157,18 +157,21 @@ struct alignas(16) TreeStart {   // 64-bit scratch follows it in shared memory
     TreeReq r;   // request b
 };
 
-// All threads of the CTA; `scratch` holds blockDim.x / 32 values.  Ends with a barrier.
+// The requests' costs dealt to the CTAs.  All threads of the CTA; `scratch` holds blockDim.x / 32 values.  Ends
+// with a barrier.  cost(b, tell) is a request's, found(b, off) is called by the thread that comes upon
+// the one that this CTA's stretch begins in.
 // Cost positions are 32-bit from here on: a batch of 2^31 tiles, which no memory holds but
 // shared blocks could make, is reported and not worked on.
-__device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int cta, int ncta, TreeStart* st,
-                                           int64_t* scratch) {
+template <typename Start, typename Cost, typename Found>
+__device__ __forceinline__ void deal_requests(const TreeParams& p, int cta, int ncta, Start* st, int64_t* scratch, Cost cost,
+                                              Found found) {
     const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nwarp = nthr >> 5;
     const int per = (p.B + nthr - 1) / nthr;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     int64_t mine = 0;
     // rolled: this runs once, and what it takes of the instruction cache is missed later
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += tree_cost(p, tree_request(p, b, cta == 0), tile);
+    for (int b = b0; b < b1; ++b) mine += cost(b, cta == 0);
     int64_t incl = mine;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
@@ -201,12 +204,9 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
         int at = first;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const TreeReq r = tree_request(p, b, false);
-            const int c = (int)tree_cost(p, r, tile);
+            const int c = (int)cost(b, false);
             if (s < at + c) {
-                st->b = b;
-                st->r = r;
-                st->off = s - at;
+                found(b, s - at);
                 break;
             }
             at += c;
@@ -215,12 +215,63 @@ __device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int ct
     __syncthreads();
 }
 
+__device__ __forceinline__ void tree_begin(const TreeParams& p, int tile, int cta, int ncta, TreeStart* st,
+                                           int64_t* scratch) {
+    TreeReq r;
+    deal_requests(
+        p, cta, ncta, st, scratch,
+        [&](int b, bool tell) {
+            r = tree_request(p, b, tell);
+            return tree_cost(p, r, tile);
+        },
+        [&](int b, int off) {
+            st->b = b;
+            st->r = r;
+            st->off = off;
+        });
+}
+
 // The same over the blocks of a scored call: the block that a CTA's stretch begins in.  Waits for
 // the grid that made the list.  All threads of the CTA; ends with a barrier.
 struct alignas(16) ScoredStart {
     int share, left, pos, off;   // as in TreeStart; `off` within block `block`
     int block;
 };
+
+// Row block `i0 / tokb` of a request whose rows' ends only grow (no ranges of their own).
+__device__ __forceinline__ ScoredBlock scored_block(const ScoredParams& p, int b, const TreeReq& r, int i0, int tile) {
+    ScoredBlock k;
+    k.b = b;
+    k.q_row = r.q_begin + i0;
+    k.rows_tok = min(p.tokb, r.n - i0);
+    k.at = r.len - r.n + i0;
+    k.len = r.len;
+    k.h = 0;
+    const int2 a = scored_range(p, k.q_row, k.at, k.len);
+    const int2 z = scored_range(p, k.q_row + k.rows_tok - 1, k.at + k.rows_tok - 1, k.len);
+    k.lo = a.x;
+    k.hi = z.y;
+    k.full_lo = z.x;
+    k.full_hi = a.y;
+    k.tile0 = k.lo / tile;
+    k.nt = max(1, (k.hi + tile - 1) / tile - k.tile0);
+    return k;
+}
+
+// Without a list (p.blocks null: at most one block a request, and no ranges): a block is its request's.
+__device__ __forceinline__ int64_t scored_cost(const ScoredParams& p, const TreeReq& r, int tile) {
+    return r.n == 0 ? 0 : (int64_t)(scored_block(p, 0, r, 0, tile).nt + p.ucost) * p.H_kv;
+}
+
+__device__ __forceinline__ void scored_begin_here(const ScoredParams& p, int tile, int cta, int ncta, ScoredStart* st,
+                                                  int64_t* scratch) {
+    deal_requests(
+        p, cta, ncta, st, scratch, [&](int b, bool tell) { return scored_cost(p, tree_request(p, b, tell), tile); },
+        [&](int b, int off) {
+            st->block = b;
+            st->off = off;
+        });
+}
 
 __device__ __forceinline__ void scored_begin(const ScoredParams& p, int cta, int ncta, ScoredStart* st) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -328,6 +379,7 @@ struct ScoredPiece {
     ScoredBlock k;
 };
 
+template <bool HERE>   // HERE: there may be no list
 struct ScoredWalk {
     int pos, left, off, block, ready;
     ScoredBlock k;
@@ -337,7 +389,21 @@ struct ScoredWalk {
 
     __device__ __forceinline__ bool next(const ScoredParams& p, int tile, ScoredPiece& it) {
         while (left > 0) {
-            if (!ready) {
+            if (HERE && p.blocks == nullptr && !ready) {
+                // the next request that has rows: 32 looked at a round
+                const int lane = threadIdx.x & 31;
+                for (; block < p.B; block += 32) {
+                    const bool has = block + lane < p.B && tree_request(p, block + lane, false).n > 0;
+                    const unsigned m = __ballot_sync(0xffffffffu, has);
+                    if (m != 0) {
+                        block += __ffs(m) - 1;
+                        break;
+                    }
+                }
+                if (block >= p.B) return false;   // not reached: the stretches end at W
+                k = scored_block(p, block, tree_request(p, block, false), 0, tile);
+                ready = 1;
+            } else if (!ready) {
                 const int4* from = reinterpret_cast<const int4*>(p.blocks + block);
                 const int4 x = __ldcg(from), y = __ldcg(from + 1), z = __ldcg(from + 2);
                 k = ScoredBlock{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y, z.z, 0};

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
     else
         tree_begin(p, kCcTile, cta, gridDim.x, st, reinterpret_cast<int64_t*>(smem + L::scratch));
     int4 rec = make_int4(0, 0, 0, 0);
-    typename std::conditional<V::kScored, ScoredWalk, TreeWalk>::type walk(*st);
+    typename std::conditional<V::kScored, ScoredWalk<false>, TreeWalk>::type walk(*st);
     typename std::conditional<V::kScored, ScoredPiece, TreePiece>::type it;
 #pragma unroll 1
     while (walk.next(p, kCcTile, it)) {

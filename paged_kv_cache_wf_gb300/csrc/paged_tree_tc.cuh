@@ -429,9 +429,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < kRing * 4; ++i) smem[L::wild + i] = 0;
     }
     tc::fence_before_sync();
-    if constexpr (V::kScored)
-        scored_begin(p, cta, gridDim.x, st);
-    else
+    if constexpr (V::kScored) {
+        if (V::kSpread && p.blocks == nullptr)
+            scored_begin_here(p, TN, cta, gridDim.x, st, reinterpret_cast<int64_t*>(smem + L::scratch));
+        else
+            scored_begin(p, cta, gridDim.x, st);
+    } else
         tree_begin(p, TN, cta, gridDim.x, st, reinterpret_cast<int64_t*>(smem + L::scratch));
     tc::fence_after_sync();
     const uint32_t tmem = (uint32_t)misc[0];
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // ============================= walk, query tiles =============================
             // publishes records as far ahead as the ring allows and loads each piece's query
             // tiles once the products that read the tiles before are done
-            typename std::conditional<V::kScored, ScoredWalk, TreeWalk>::type walk(*st);
+            typename std::conditional<V::kScored, ScoredWalk<V::kSpread>, TreeWalk>::type walk(*st);
             typename std::conditional<V::kScored, ScoredPiece, TreePiece>::type it;
             bool more = true;
             int made = 0, asked = 0, second = 0;   // records, pieces whose tiles are asked for, second tiles
@@ -1760,7 +1763,9 @@ cudaError_t launch_bf16(const typename V::Params& p, int ctas, cudaStream_t stre
     const int smem = TtLayout<V, D, QT, false>::total;
     e = allow_dynamic_smem((const void*)kern, smem);
     if (e != cudaSuccess) return e;
-    if constexpr (V::kScored) {
+    bool after = false;                      // the grid that makes a scored call's list
+    if constexpr (V::kScored) after = p.blocks != nullptr;
+    if (after) {
         return launch_after(kern, ctas, smem, stream, tq, tk, tv, p, box_tok, NoScales{});
     } else {
         kern<<<ctas, kTcThreads, smem, stream>>>(tq, tk, tv, p, box_tok, NoScales{});
