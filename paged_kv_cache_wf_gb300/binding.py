@@ -491,7 +491,7 @@ def wf_paged_scored_attention(out, q, k_pool, v_pool, block_tables, seq_lens, cu
     if out.shape != q.shape or out.dtype is not dt or D != k_pool.shape[3] or \
             dt is not (bf16 if pool_dt is u8 else pool_dt) or v_pool.shape != k_pool.shape or v_pool.dtype is not pool_dt:
         raise ValueError("out is like q [T, H_q, D] of the pool's dtype (bf16 for fp8 pools) and head size")
-    if seq_lens.shape[0] != B or cu_q_lens.shape[0] != B + 1 or block_tables.dtype is not i32 or \
+    if seq_lens.numel() != B or cu_q_lens.numel() != B + 1 or block_tables.dtype is not i32 or \
             seq_lens.dtype is not i32 or cu_q_lens.dtype is not i32:
         raise ValueError("block_tables [B, M], seq_lens [B] and cu_q_lens [B + 1] are int32")
     if slopes is not None and (slopes.dtype is not f32 or slopes.numel() != H_q):
@@ -523,8 +523,8 @@ def wf_verify_drafts(accepted, num_accepted, next_tokens, target, draft, tokens,
         raise ValueError("target must be [T, V] float32 or bfloat16 with dense rows")
     if draft is not None and (draft.shape != target.shape or draft.dtype is not dt or (V > 1 and draft.stride(1) != 1)):
         raise ValueError("draft must be like target")
-    if tokens.shape != (T,) or coins.shape != (T,) or (parents is not None and parents.shape != (T,)) or \
-            picks.shape != (B,) or cu_q_lens.shape != (B + 1,) or num_accepted.shape != (B,) or next_tokens.shape != (B,):
+    if tokens.numel() != T or coins.numel() != T or (parents is not None and parents.numel() != T) or \
+            picks.numel() != B or cu_q_lens.numel() != B + 1 or num_accepted.numel() != B or next_tokens.numel() != B:
         raise ValueError("tokens, parents and coins are [T], picks, num_accepted and next_tokens [B], cu_q_lens [B + 1]")
     if coins.dtype is not f32 or picks.dtype is not f32:
         raise ValueError("coins and picks are float32")
@@ -556,10 +556,10 @@ def wf_build_step(block_tables, seq_lens, new_lens, free_blocks, num_free, new_s
         if t is not None and t.dtype is not i32:
             raise ValueError("tables, lengths, lists, offsets and positions are int32")
     B, M = block_tables.shape
-    rows = slot_mapping.shape[0]
-    if slot_mapping.dtype is not i64 or positions.shape != (rows,) or (depths is not None and depths.shape != (rows,)):
+    rows = slot_mapping.numel()
+    if slot_mapping.dtype is not i64 or positions.numel() != rows or (depths is not None and depths.numel() != rows):
         raise ValueError("slot_mapping [max_tokens] is int64, positions and depths are [max_tokens]")
-    if seq_lens.shape != (B,) or new_lens.shape != (B,) or new_seq_lens.shape != (B,) or cu_q_lens.shape != (B + 1,) or \
+    if seq_lens.numel() != B or new_lens.numel() != B or new_seq_lens.numel() != B or cu_q_lens.numel() != B + 1 or \
             num_free.numel() != 1 or new_num_free.numel() != 1 or free_blocks.dim() != 1:
         raise ValueError("seq_lens, new_lens and new_seq_lens are [B], cu_q_lens [B + 1], free_blocks [N], num_free and "
                          "new_num_free [1]")
@@ -583,7 +583,7 @@ def wf_trim_blocks(block_tables, seq_lens, kept_lens, free_blocks, num_free, new
         if t.dtype is not i32:
             raise ValueError("tables, lengths and lists are int32")
     B, M = block_tables.shape
-    if seq_lens.shape != (B,) or kept_lens.shape != (B,) or free_blocks.dim() != 1 or num_free.numel() != 1 or \
+    if seq_lens.numel() != B or kept_lens.numel() != B or free_blocks.dim() != 1 or num_free.numel() != 1 or \
             new_num_free.numel() != 1:
         raise ValueError("seq_lens and kept_lens are [B], free_blocks [N], num_free and new_num_free [1]")
     rc = (_lib or load()).wf_trim_blocks(

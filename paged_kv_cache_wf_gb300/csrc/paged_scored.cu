@@ -253,7 +253,7 @@ cudaError_t launch_list(const ListParams& p, bool d128, cudaStream_t stream) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1;
     return d128 ? cudaLaunchKernelEx(&cfg, scored_list_kernel<128>, p, ctas)
                 : cudaLaunchKernelEx(&cfg, scored_list_kernel<64>, p, ctas);
 }

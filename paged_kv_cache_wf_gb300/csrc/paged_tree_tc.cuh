@@ -67,9 +67,10 @@ constexpr float kLazyMax = 8.f;   // rescale O only when a row's maximum grows b
 // factor 2^-14 and 2^-25, which a long tail of small weights would feel).
 constexpr float kCodesUp = 7.f;
 static_assert(kLazyMax + kCodesUp <= 15.f, "fp16 weights overflow");
-// Scored calls over bf16 pools: bf16 weights and fp32 sums have the range for more, and then hardly any tile
-// after a row's first rescales (with 8 some row of a warp did every few tiles, a sixth of the time).
-constexpr float kLazyFar = 40.f;
+// Scored calls over bf16 pools: bf16 weights and fp32 sums have the range for more (values of V up to 2^90 or so),
+// and then hardly any tile after a row's first rescales (with 8 some row of a warp did every few tiles, a sixth of
+// the time).
+constexpr float kLazyFar = 24.f;
 constexpr int kSoftW = 8, kKW = 8, kVW = 9, kWalkW = 10, kMmaW = 11, kFinW = 13, kFin = 3;
 constexpr int kTcThreads = (kFinW + kFin) * 32;
 constexpr int kSoftRegs = 192, kOtherRegs = 64;

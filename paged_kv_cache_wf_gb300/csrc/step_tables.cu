@@ -274,7 +274,7 @@ cudaError_t launch_step(void (*kern)(const Params), const Params& p, int64_t ent
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -291,8 +291,8 @@ cudaError_t launch_build_step(const BuildArgs& a, uint32_t* dev_status, cudaStre
 cudaError_t launch_trim_blocks(const TrimArgs& a, uint32_t* dev_status, cudaStream_t stream) {
     const TrimParams p{a.block_tables, a.seq_lens, a.kept_lens, a.num_free,   a.free_blocks,
                        a.new_num_free, dev_status, a.max_blocks_per_seq, a.B, a.num_blocks, a.block_size};
-    // what goes back is known on the device only: a few blocks a request, as after drafts
-    return launch_step(trim_blocks_kernel, p, 4 * (int64_t)a.B, (2 * a.B + 1) * (int)sizeof(int32_t), stream);
+    // What goes back is known on the device only: taken as 16 blocks a request (finished ones among them).
+    return launch_step(trim_blocks_kernel, p, 16 * (int64_t)a.B, (2 * a.B + 1) * (int)sizeof(int32_t), stream);
 }
 
 }  // namespace wf

@@ -434,18 +434,28 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_drafts_ke
                 // the slice with the next token: the first with a weight whose running sum passes the threshold
                 Pair run = shfl_up(incl, 1), before{0.f, 0.f};
                 if (lane == 0) run = Pair{0.f, 0.f};
-                int owner = INT32_MAX;
+                int owner = INT32_MAX, some = -1;
+                Pair some_before{0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < kSlices / 32; ++k) {
                     const Pair up = run + part[k];
+                    if (part[k].h > 0.f) {
+                        some = kSlices / 32 * lane + k;
+                        some_before = run;
+                    }
                     if (owner == INT32_MAX && part[k].h > 0.f && threshold < up) {
                         owner = kSlices / 32 * lane + k;
                         before = run;
                     }
                     run = up;
                 }
-                const int first_owner = __reduce_min_sync(0xffffffffu, owner);
-                if (owner == first_owner) {          // of all lanes where there is none: it is not used then
+                int first_owner = __reduce_min_sync(0xffffffffu, owner);
+                if (first_owner == INT32_MAX) {      // a sum so small that the threshold rounds up to it: the last one
+                    first_owner = __reduce_max_sync(0xffffffffu, some);
+                    owner = some;
+                    before = some_before;
+                }
+                if (owner == first_owner) {          // (of all lanes where there is none: it is not used then)
                     s_owner = first_owner;
                     s_before = before;
                 }

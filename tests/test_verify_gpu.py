@@ -187,6 +187,16 @@ def test_values_that_are_no_probabilities():
         assert single([row] * 3, [row] * 3, [0, 1, 1], [-1, 0, 0], [0, 1.0, 1.0], 0.5) == ([0], -1, bad)
 
 
+def test_sums_at_the_end_of_the_range():
+    """Sums so small that a threshold rounds up to them, and so large that they only just stay finite."""
+    tiny = 2.0 ** -149
+    for pick in (0.0, 0.4, 0.6, 1 - 2 ** -24):
+        assert single([[0.0, tiny, 0.0]], None, [0], [-1], [0], pick) == ([0], 1, 0)
+        assert single([[0.0] * 600 + [tiny] + [0.0] * 5000], None, [0], [-1], [0], pick) == ([0], 600, 0)
+    assert single([[0.0, 3e38, 1.0]], None, [0], [-1], [0], 0.9) == ([0], 1, 0)
+    assert single([[0.0, 3e38, 3e38]], None, [0], [-1], [0], 0.9) == ([0], -1, wf.WF_DEV_BAD_PROBS)
+
+
 def test_bad_requests_are_left_out():
     def batch():
         b = Batch([4, 6, 3], 100, True, seed=8)
