@@ -1,7 +1,7 @@
-// paged_tree_tc.cuh -- tree attention on the tensor cores (tcgen05, TMA, TMEM) for bf16
-// and fp8 pools whose block size is a multiple of 16.
+// paged_tree_tc.cuh -- tree attention and scored attention on the tensor cores (tcgen05, TMA,
+// TMEM) for bf16 and fp8 pools whose block size is a multiple of 16.
 //
-// What is computed is paged_tree.cu's: row (draft, query head) sees its request's cached
+// What is computed is paged_tree_cc.cuh's: row (draft, query head) sees its request's cached
 // positions and the drafts of its mask; o = softmax(scale q K^T) V.
 //
 // GB300 design.  A work unit (paged_tree.cuh) is one row block of a request under one
@@ -47,6 +47,19 @@
 // widened) to 135 us, batch of 64.  Widening K too would cost twice the finishing warps'
 // work, and splitting the weights into two e4m3 parts would cost the softmax warps more
 // conversions than they have time for.
+//
+// Scored attention (ScoredView; paged_scored.cu has the formulas).  A unit's tiles are those that some
+// of its rows see, from the last one down, and two things differ in the softmax:
+//   - Half tiles (row blocks of more than 32 rows).  A step takes 64 positions: S of the second half runs
+//     while the first is worked on, and S of the next tile's first half as soon as P V has read its
+//     columns, so a stream waits for its products 300 clocks a half instead of 2000 a tile.  Eight prompts of
+//     128-2048 tokens: 198 us plain, 224 with a bias, 279 capped, 321 capped and biased (96 us of products at
+//     the bf16 rate); a half step then is 2100 clocks, of which the two streams' products are 1300.
+//   - Spread (at most 32 rows).  The rows stand in all four quarters of the query tile and each quarter's
+//     warp takes a quarter of a tile's positions, so eight warps share what one warp a stream had: 231 capped
+//     decodes 266 us (252 at the copy peak; 393 before).  The quarters' sums and outputs are joined at a piece's end.
+// Row blocks of fp8 pools stay at 128 rows or 32.  What is left: packed documents (206 us, 31 of products) spend half
+// of their time on their pieces' ends, 1.8 tiles a piece and stream; one user (10.6 us) is the start, one tile and the join.
 #pragma once
 
 #include <cuda.h>

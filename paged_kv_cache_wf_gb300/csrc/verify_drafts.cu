@@ -17,13 +17,15 @@
 // Numbers are compared with borders that they may lie next to, so sums are exact to about 2^-46, in
 // pairs of fp32 numbers: products and differences with their rounding errors, and sums with theirs.
 // (In fp64, which this GPU has a 64th of its fp32 rate for, the sums over a warp's lanes alone took
-// longer than reading the rows: 64 trees 19 us instead of 12.)
+// longer than reading the rows: 64 trees 19 us instead of 12; now 10.8.)
 //
 // Bound: HBM, one or two rows of the vocabulary a request.  A cluster takes a request; every CTA
 // walks the tree by itself on the gathered p_u(x), q_u(x) of all nodes and reads its part of a row
 // where a sum is needed, which is once for a chain: the sums that a rejection's remainder needs are
 // the running sums of the next token too, up to the slice of the one warp that holds it, which looks
-// at it again.  Slices' sums are written to every CTA of the cluster, so a row takes one barrier.
+// at it again.  231 chains of up to 4 drafts over 128000 fp32 tokens 46.6 us, 172 MB that are 25.4 at the copy peak:
+// a request is 8 us of dependent rounds around its 6-16 us of loads, and a second row for a rejected draft with
+// a sibling comes on top.  Slices' sums are written to every CTA of the cluster, so a row takes one barrier.
 #include <cooperative_groups.h>
 
 #include "wf_internal.h"
