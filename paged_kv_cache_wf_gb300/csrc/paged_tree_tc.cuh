@@ -52,9 +52,9 @@
 // of its rows see, from the last one down, and two things differ in the softmax:
 //   - Half tiles (row blocks of more than 32 rows).  A step takes 64 positions: S of the second half runs
 //     while the first is worked on, and S of the next tile's first half as soon as P V has read its
-//     columns, so a stream waits for its products 300 clocks a half instead of 2000 a tile.  Eight prompts of
+//     columns, so a stream waits for S 300 clocks a half instead of 2000 a tile.  Eight prompts of
 //     128-2048 tokens: 198 us plain, 224 with a bias, 279 capped, 321 capped and biased (96 us of products at
-//     the bf16 rate); a half step then is 2100 clocks, of which the two streams' products are 1300.
+//     the bf16 rate); a capped half step takes 2400 clocks.
 //   - Spread (at most 32 rows).  The rows stand in all four quarters of the query tile and each quarter's
 //     warp takes a quarter of a tile's positions, so eight warps share what one warp a stream had: 231 capped
 //     decodes 266 us (252 at the copy peak; 393 before).  The quarters' sums and outputs are joined at a piece's end.
