@@ -419,8 +419,9 @@ size_t wf_paged_scored_attention_workspace_size(int32_t B, int32_t num_q_heads, 
  *              So a document packed with others starts its rows' ranges at its first position, a
  *              prefix seen in both directions ends them at its last one, and an empty range is a
  *              row of padding.  The window cuts a range too.
- *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b], below 2^31 - 1024.  max_q_len also
- *              decides how the rows of all requests are laid over the GPU.
+ *   max_q_len  >= every n_b; max_seq_len >= every seq_lens[b], below 2^31 - 1024;
+ *              max_q_len <= max_seq_len <= max_blocks_per_seq*P.  max_q_len also decides how the rows
+ *              of all requests are laid over the GPU.
  *   workspace  device scratch of >= wf_paged_scored_attention_workspace_size(B, H_q, T_total,
  *              max_q_len, max_seq_len, pool) bytes, 16-byte aligned; needs no initialisation.
  *              Calls that overlap in time must not share one.
@@ -472,7 +473,7 @@ wf_status wf_paged_scored_attention(void* out, const void* q, const void* k_pool
  * From node u = 0 on, u's children are tried in order: with w_0 = p_u and N_0 = 1, child i of
  * token x is kept if coins[i] q_u(x) N_k < w_k(x), and u = i; else
  * w_{k+1} = max(w_k - N_k q_u, 0) and N_{k+1} = sum w_{k+1}.  Fixed candidates: kept if
- * coins[i] N_k < w_k(x), else w_{k+1} is w_k without token x and N_{k+1} = N_k - p_u(x).  The
+ * coins[i] N_k < w_k(x), else w_{k+1} is w_k without token x and N_{k+1} = N_k - w_k(x).  The
  * path ends where no child is kept, or at max_accepted nodes (whose last has no children
  * tried).  The next token is the first x with w(0) + .. + w(x) > picks[b] sum w (w = p_u where
  * sum w is 0).  So the tokens are distributed as the target's own if the coins and picks are
@@ -483,6 +484,7 @@ wf_status wf_paged_scored_attention(void* out, const void* q, const void* k_pool
  * (WF_DEV_BAD_SEQLEN), parents or tokens (WF_DEV_BAD_NODE), or pick (WF_DEV_BAD_PROBS) are out of
  * range is skipped and its outputs are left unwritten; where p_u has no positive finite sum its
  * next token is -1 (WF_DEV_BAD_PROBS).
+ * Outputs must not overlap inputs or one another.
  * Pointers are aligned to their elements; 16-byte aligned fp32 (8-byte bf16) rows are read
  * faster.  No workspace.
  */

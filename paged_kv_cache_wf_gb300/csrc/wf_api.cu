@@ -255,6 +255,21 @@ wf_status wf_verify_drafts(int32_t* accepted, int32_t max_accepted, int32_t* num
                           (const void*)tokens, (const void*)parents, (const void*)cu_q_lens, (const void*)coins,
                           (const void*)picks})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return WF_ERR_INVALID_ARG;
+    // written while other requests' inputs are read
+    const int64_t reqs = 4 * (int64_t)B, nodes = 4 * (int64_t)total_q;
+    const auto rows = [&](int64_t stride) { return total_q > 0 ? ((int64_t)(total_q - 1) * stride + vocab) * elt : 0; };
+    const struct {
+        const void* p;
+        int64_t bytes;
+    } in[] = {{target, rows(target_stride)}, {draft, draft ? rows(draft_stride) : 0}, {tokens, nodes},
+              {parents, parents ? nodes : 0}, {coins, nodes}, {cu_q_lens, reqs + 4}, {picks, reqs}},
+      out[] = {{accepted, reqs * max_accepted}, {num_accepted, reqs}, {next_tokens, reqs}};
+    for (int o = 0; o < 3; ++o) {
+        for (const auto& i : in)
+            if (i.bytes > 0 && overlap(out[o].p, out[o].bytes, i.p, i.bytes)) return WF_ERR_INVALID_ARG;
+        for (int x = o + 1; x < 3; ++x)
+            if (overlap(out[o].p, out[o].bytes, out[x].p, out[x].bytes)) return WF_ERR_INVALID_ARG;
+    }
     const wf::VerifyArgs a{accepted, num_accepted, next_tokens, max_accepted, target, draft, target_stride, draft_stride,
                            vocab, probs_dtype, tokens, parents, cu_q_lens, coins, picks, B, total_q, max_q_len};
     return from_cuda(wf::launch_verify_drafts(a, dev_status, stream));

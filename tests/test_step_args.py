@@ -39,6 +39,17 @@ def test_verify_refusals(lib):
         assert call(B=2, **bad) == wf.WF_ERR_INVALID_ARG, bad
 
 
+def test_verify_refuses_outputs_over_inputs_or_one_another(lib):
+    at = lambda i: FAKE + i * FAR   # noqa: E731
+    ok = dict(acc=at(0), num=at(1), nxt=at(2), t=at(3), d=at(4), tok=at(5), par=at(6), cu=at(7), coins=at(8), picks=at(9))
+    last = (9 * 120 + 100) * 4 - 4                       # the last element of the last row
+    for bad in (dict(acc=at(3) + last), dict(acc=at(4)), dict(acc=at(5) + 36), dict(acc=at(6) - 28), dict(num=at(1), nxt=at(1) + 4),
+                dict(num=at(7) + 8), dict(nxt=at(8) + 36), dict(nxt=at(9) + 4), dict(num=at(0) + 28), dict(nxt=at(5))):
+        a = dict(ok, **bad)
+        assert lib.wf_verify_drafts(a["acc"], 4, a["num"], a["nxt"], a["t"], 120, a["d"], 120, 100, wf.WF_DTYPE_F32, a["tok"],
+                                    a["par"], a["cu"], a["coins"], a["picks"], 2, 10, 5, None, None) == wf.WF_ERR_INVALID_ARG, bad
+
+
 def test_build_refusals(lib):
     f = lib.wf_build_step
     at = lambda i: FAKE + i * FAR   # noqa: E731
