@@ -53,12 +53,12 @@
 //   - Half tiles (row blocks of more than 32 rows).  A step takes 64 positions: S of the second half runs
 //     while the first is worked on, and S of the next tile's first half as soon as P V has read its
 //     columns, so a stream waits for S 300 clocks a half instead of 2000 a tile.  Eight prompts of
-//     128-2048 tokens: 198 us plain, 224 with a bias, 279 capped, 321 capped and biased (96 us of products at
+//     128-2048 tokens: 194 us plain, 214 with a bias, 277 capped, 321 capped and biased (96 us of products at
 //     the bf16 rate); a capped half step takes 2400 clocks.
 //   - Spread (at most 32 rows).  The rows stand in all four quarters of the query tile and each quarter's
 //     warp takes a quarter of a tile's positions, so eight warps share what one warp a stream had: 231 capped
 //     decodes 266 us (252 at the copy peak; 393 before).  The quarters' sums and outputs are joined at a piece's end.
-// Row blocks of fp8 pools stay at 128 rows or 32.  What is left: packed documents (206 us, 31 of products) spend half
+// Row blocks of fp8 pools stay at 128 rows or 32.  What is left: packed documents (200 us, 31 of products) spend half
 // of their time on their pieces' ends, 1.8 tiles a piece and stream; one user (10.6 us) is the start, one tile and the join.
 #pragma once
 
@@ -973,53 +973,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 } else {
 #pragma unroll 1
-                for (int u = -1; u < nt && ok; ++u) {
-                    // P V of step u ...
-                    if (u >= 0) {
-                        if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
-                        ppar ^= 1;
-                        tc::fence_after_sync();
-                        const uint32_t vd = (uint32_t)vdesc + ((vx * L::VTILE) >> 4);
-                        if (elect_one()) {
+                    for (int u = -1; u < nt && ok; ++u) {
+                        // P V of step u ...
+                        if (u >= 0) {
+                            if (!need(&v_ready[vx], vpar) || !need(p_full(t), ppar)) break;
+                            ppar ^= 1;
+                            tc::fence_after_sync();
+                            const uint32_t vd = (uint32_t)vdesc + ((vx * L::VTILE) >> 4);
+                            if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < TN / 16; ++kk)
-                                mma<1>(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), 0u, vd + ((kk * 2 * L::ATOM) >> 4),
-                                       (uint32_t)(vdesc >> 32), idO, (u > 0 || kk > 0) ? 1u : 0u);
-                            tc::commit(&v_empty[vx]);
-                            tc::commit(pv_done(t));
-                        }
-                        __syncwarp();
-                        advance();
-                    }
-                    // ... then S of step u + 1
-                    if (u + 1 < nt) {
-                        if (!need(&k_full[kx], kpar)) break;
-                        tc::fence_after_sync();
-                        if (elect_one()) {
-                            const uint32_t kd = (uint32_t)kdesc + ((kx * L::KTILE) >> 4), qd = (uint32_t)qdesc;
-                            const uint32_t khi = (uint32_t)(kdesc >> 32), qhi = (uint32_t)(qdesc >> 32);
-                            if constexpr (CODES) {       // the two parts of q, one after the other
-#pragma unroll
-                                for (int x = 0; x < 2 * D / 32; ++x) {
-                                    const int part = x / (D / 32), kk = x % (D / 32);
-                                    mma<2>(dS, qd + ((part * TM * D + kk * 32) >> 4), qhi, kd + ((kk * 32) >> 4), khi, idS,
-                                           x > 0 ? 1u : 0u);
-                                }
-                            } else {
-#pragma unroll
-                                for (int kk = 0; kk < D / 16; ++kk) {
-                                    const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
-                                    const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
-                                    mma<0>(dS, qd + (qoff >> 4), qhi, kd + (koff >> 4), khi, idS, kk > 0 ? 1u : 0u);
-                                }
+                                for (int kk = 0; kk < TN / 16; ++kk)
+                                    mma<1>(dO, dS + kk * 8 + (kk >= 4 ? 32 : 0), 0u, vd + ((kk * 2 * L::ATOM) >> 4),
+                                           (uint32_t)(vdesc >> 32), idO, (u > 0 || kk > 0) ? 1u : 0u);
+                                tc::commit(&v_empty[vx]);
+                                tc::commit(pv_done(t));
                             }
-                            tc::commit(s_full(t));
-                            tc::commit(&k_empty[kx]);
-                            if (u + 2 == nt) tc::commit(&q_empty[tq]);
+                            __syncwarp();
+                            advance();
                         }
-                        __syncwarp();
+                        // ... then S of step u + 1
+                        if (u + 1 < nt) {
+                            if (!need(&k_full[kx], kpar)) break;
+                            tc::fence_after_sync();
+                            if (elect_one()) {
+                                const uint32_t kd = (uint32_t)kdesc + ((kx * L::KTILE) >> 4), qd = (uint32_t)qdesc;
+                                const uint32_t khi = (uint32_t)(kdesc >> 32), qhi = (uint32_t)(qdesc >> 32);
+                                if constexpr (CODES) {       // the two parts of q, one after the other
+#pragma unroll
+                                    for (int x = 0; x < 2 * D / 32; ++x) {
+                                        const int part = x / (D / 32), kk = x % (D / 32);
+                                        mma<2>(dS, qd + ((part * TM * D + kk * 32) >> 4), qhi, kd + ((kk * 32) >> 4), khi, idS,
+                                               x > 0 ? 1u : 0u);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int kk = 0; kk < D / 16; ++kk) {
+                                        const uint32_t qoff = (kk >> 2) * (TM * 128) + (kk & 3) * 32;
+                                        const uint32_t koff = (kk >> 2) * L::HALF_OFF + (kk & 3) * 32;
+                                        mma<0>(dS, qd + (qoff >> 4), qhi, kd + (koff >> 4), khi, idS, kk > 0 ? 1u : 0u);
+                                    }
+                                }
+                                tc::commit(s_full(t));
+                                tc::commit(&k_empty[kx]);
+                                if (u + 2 == nt) tc::commit(&q_empty[tq]);
+                            }
+                            __syncwarp();
+                        }
                     }
-                }
                 }
                 if (QT == 1 && ok && 2 * nt + t < ring_tiles(all)) {   // stream 1's empty tile: hand it back
                     if (need(&k_full[kx], kpar) && lane == 0) mbar_arrive(&k_empty[kx]);
@@ -1172,135 +1172,135 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc::wait_st();
                             tc::fence_before_sync();
                         } else {
-                        // the row's positions in registers
-                        float s[kWords][32];
+                            // the row's positions in registers
+                            float s[kWords][32];
 #pragma unroll
-                        for (int w = 0; w < kWords; ++w) tc::ld_32cols(sbase + word(w) * 32, s[w]);
-                        tc::wait_ld();
-                        const Cap cap(scale, cap_out_of(p));
-                        bool near = false;
-                        float top = -INFINITY, low = INFINITY;
-                        if constexpr (kCap) {
-                            // Only in a tile that all rows see: what is not seen must not choose the way, which changes
-                            // last bits.  (Chosen among what is seen it cost 231 decodes 271 us instead of 264.)
-                            if (!masked) {
+                            for (int w = 0; w < kWords; ++w) tc::ld_32cols(sbase + word(w) * 32, s[w]);
+                            tc::wait_ld();
+                            const Cap cap(scale, cap_out_of(p));
+                            bool near = false;
+                            float top = -INFINITY, low = INFINITY;
+                            if constexpr (kCap) {
+                                // Only in a tile that all rows see: what is not seen must not choose the way, which changes
+                                // last bits.  (Chosen among what is seen it cost 231 decodes 271 us instead of 264.)
+                                if (!masked) {
 #pragma unroll
-                                for (int w = 0; w < kWords; ++w) extremes<true>(s[w], top, low);
-                                near = scale > 0.f &&
-                                       __all_sync(0xffffffffu, !row_valid || fmaxf(top, -low) * scale <= kTanhNear);
+                                    for (int w = 0; w < kWords; ++w) extremes<true>(s[w], top, low);
+                                    near = scale > 0.f &&
+                                           __all_sync(0xffffffffu, !row_valid || fmaxf(top, -low) * scale <= kTanhNear);
+                                }
                             }
-                        }
-                        // Scores that are final before the weights: biased ones, and capped ones of the longer way.
-                        const bool made = kBias || (kCap && !near);
-                        if constexpr (kCap) {
-                            const auto capped = [&](auto f) {
+                            // Scores that are final before the weights: biased ones, and capped ones of the longer way.
+                            const bool made = kBias || (kCap && !near);
+                            if constexpr (kCap) {
+                                const auto capped = [&](auto f) {
+#pragma unroll
+                                    for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                                        for (int e = 0; e < 32; e += 2) {
+                                            const float2 y = f(make_float2(s[w][e], s[w][e + 1]), make_float2(0.f, 0.f));
+                                            s[w][e] = y.x;
+                                            s[w][e + 1] = y.y;
+                                        }
+                                };
+                                if (!near)
+                                    capped([&](float2 x, float2 none) { return cap.far(x, none); });
+                                else if (kBias)
+                                    capped([&](float2 x, float2 none) { return cap.near(x, none); });
+                            }
+                            if constexpr (kBias) {
 #pragma unroll
                                 for (int w = 0; w < kWords; ++w)
-#pragma unroll
-                                    for (int e = 0; e < 32; e += 2) {
-                                        const float2 y = f(make_float2(s[w][e], s[w][e + 1]), make_float2(0.f, 0.f));
-                                        s[w][e] = y.x;
-                                        s[w][e + 1] = y.y;
-                                    }
-                            };
-                            if (!near)
-                                capped([&](float2 x, float2 none) { return cap.far(x, none); });
-                            else if (kBias)
-                                capped([&](float2 x, float2 none) { return cap.near(x, none); });
-                        }
-                        if constexpr (kBias) {
-#pragma unroll
-                            for (int w = 0; w < kWords; ++w)
-                                bias_word(s[w], kCap ? 1.f : scale, slope, step, (float)(k0 + 32 * word(w) - ref), ahead);
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int w = 0; w < kWords; ++w) {
-                                for (int e = 0; e < 32; ++e) s[w][e] = (seen[w] >> e) & 1u ? s[w][e] : fill;
+                                    bias_word(s[w], kCap ? 1.f : scale, slope, step, (float)(k0 + 32 * word(w) - ref), ahead);
                             }
-                        }
-                        if (V::kRule != kRuleCap || made) {
-                            top = -INFINITY;
-                            if (negate) {   // the largest scaled score is the smallest score's
-                                float no = 0.f;
-                                low = INFINITY;
+                            if (masked) {
 #pragma unroll
-                                for (int w = 0; w < kWords; ++w) extremes<true>(s[w], no, low);
-                            } else {
-#pragma unroll
-                                for (int w = 0; w < kWords; ++w) extremes<false>(s[w], top, low);
+                                for (int w = 0; w < kWords; ++w) {
+                                    for (int e = 0; e < 32; ++e) s[w][e] = (seen[w] >> e) & 1u ? s[w][e] : fill;
+                                }
                             }
-                        }
-                        float mt = V::kRule != kRulePlain ? top : negate ? low * scale : top * scale;
-                        if constexpr (V::kRule == kRuleCap) {
-                            // tanh keeps their order
-                            if (near) mt = cap.near(make_float2(top, top), make_float2(0.f, 0.f)).x;
-                        }
-                        float alpha = 1.f;
-                        if (m_ref == -INFINITY) {
-                            m_ref = mt;
-                        } else if (row_valid && mt > m_ref + (CODES ? kLazyMax : kLazyFar)) {
-                            alpha = ex2(m_ref - mt);
-                            m_ref = mt;
-                        }
-                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                            if (!mbar_wait_warp(kHalf ? pv_done_of(t, hf ^ 1) : pv_done(t),
-                                                (kHalf && hf == 1 ? gs + u : gs + u - 1) & 1))
-                                fail();
-                            tc::fence_after_sync();
+                            if (V::kRule != kRuleCap || made) {
+                                top = -INFINITY;
+                                if (negate) {   // the largest scaled score is the smallest score's
+                                    float no = 0.f;
+                                    low = INFINITY;
+#pragma unroll
+                                    for (int w = 0; w < kWords; ++w) extremes<true>(s[w], no, low);
+                                } else {
+#pragma unroll
+                                    for (int w = 0; w < kWords; ++w) extremes<false>(s[w], top, low);
+                                }
+                            }
+                            float mt = V::kRule != kRulePlain ? top : negate ? low * scale : top * scale;
+                            if constexpr (V::kRule == kRuleCap) {
+                                // tanh keeps their order
+                                if (near) mt = cap.near(make_float2(top, top), make_float2(0.f, 0.f)).x;
+                            }
+                            float alpha = 1.f;
+                            if (m_ref == -INFINITY) {
+                                m_ref = mt;
+                            } else if (row_valid && mt > m_ref + (CODES ? kLazyMax : kLazyFar)) {
+                                alpha = ex2(m_ref - mt);
+                                m_ref = mt;
+                            }
+                            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                                if (!mbar_wait_warp(kHalf ? pv_done_of(t, hf ^ 1) : pv_done(t),
+                                                    (kHalf && hf == 1 ? gs + u : gs + u - 1) & 1))
+                                    fail();
+                                tc::fence_after_sync();
     #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                float o[16];
-                                uint32_t w[16];
-                                tc::ld_16cols(obase + c, o);
-                                tc::wait_ld();
+                                for (int c = 0; c < D; c += 16) {
+                                    float o[16];
+                                    uint32_t w[16];
+                                    tc::ld_16cols(obase + c, o);
+                                    tc::wait_ld();
     #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
-                                st_16words(obase + c, w);
+                                    for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * alpha);
+                                    st_16words(obase + c, w);
+                                }
+                                tc::wait_st();
+                            }
+                            l_run *= alpha;
+                            const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+                            const float up = CODES ? kCodesUp - m_use : -m_use;
+                            const float2 nm2 = make_float2(up, up), sc2 = make_float2(scale, scale);
+                            float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                            make_float2(0.f, 0.f)};
+                            // the weights of positions 0-63 take columns 0-31, those of 64-127 columns 64-95
+                            const auto weigh = [&](auto score) {
+#pragma unroll
+                                for (int w = 0; w < kWords; ++w) {
+                                    uint32_t pw[16];
+#pragma unroll
+                                    for (int v = 0; v < 16; ++v) {
+                                        const float2 x = score(make_float2(s[w][2 * v], s[w][2 * v + 1]));
+                                        const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
+                                        ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
+                                        pw[v] = CODES ? pack_f16x2(e2.x, e2.y) : pack_bf16x2(e2.x, e2.y);
+                                    }
+                                    st_16words(sbase + (word(w) >> 1) * 64 + (word(w) & 1) * 16, pw);
+                                }
+                            };
+                            if constexpr (V::kRule == kRulePlain) {
+                                weigh([&](float2 x) { return __ffma2_rn(x, sc2, nm2); });
+                            } else if (V::kRule == kRuleCap && near) {
+                                weigh([&](float2 x) { return cap.near(x, nm2); });
+                            } else {
+                                weigh([&](float2 x) { return __fadd2_rn(x, nm2); });
+                            }
+                            if constexpr (V::kSpread) {          // the other positions are other quarters'
+                                const uint32_t zeros[16] = {};
+#pragma unroll
+                                for (int w = 1; w < 4; ++w) {
+                                    const int x = (quad + w) & 3;
+                                    st_16words(sbase + (x >> 1) * 64 + (x & 1) * 16, zeros);
+                                }
                             }
                             tc::wait_st();
-                        }
-                        l_run *= alpha;
-                        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-                        const float up = CODES ? kCodesUp - m_use : -m_use;
-                        const float2 nm2 = make_float2(up, up), sc2 = make_float2(scale, scale);
-                        float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                        make_float2(0.f, 0.f)};
-                        // the weights of positions 0-63 take columns 0-31, those of 64-127 columns 64-95
-                        const auto weigh = [&](auto score) {
-#pragma unroll
-                            for (int w = 0; w < kWords; ++w) {
-                                uint32_t pw[16];
-#pragma unroll
-                                for (int v = 0; v < 16; ++v) {
-                                    const float2 x = score(make_float2(s[w][2 * v], s[w][2 * v + 1]));
-                                    const float2 e2 = make_float2(ex2(x.x), ex2(x.y));
-                                    ps[v & 3] = __fadd2_rn(ps[v & 3], e2);
-                                    pw[v] = CODES ? pack_f16x2(e2.x, e2.y) : pack_bf16x2(e2.x, e2.y);
-                                }
-                                st_16words(sbase + (word(w) >> 1) * 64 + (word(w) & 1) * 16, pw);
-                            }
-                        };
-                        if constexpr (V::kRule == kRulePlain) {
-                            weigh([&](float2 x) { return __ffma2_rn(x, sc2, nm2); });
-                        } else if (V::kRule == kRuleCap && near) {
-                            weigh([&](float2 x) { return cap.near(x, nm2); });
-                        } else {
-                            weigh([&](float2 x) { return __fadd2_rn(x, nm2); });
-                        }
-                        if constexpr (V::kSpread) {          // the other positions are other quarters'
-                            const uint32_t zeros[16] = {};
-#pragma unroll
-                            for (int w = 1; w < 4; ++w) {
-                                const int x = (quad + w) & 3;
-                                st_16words(sbase + (x >> 1) * 64 + (x & 1) * 16, zeros);
-                            }
-                        }
-                        tc::wait_st();
-                        const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
-                        const float2 pst = __fadd2_rn(ps01, ps23);
-                        l_run += pst.x + pst.y;
-                        tc::fence_before_sync();
+                            const float2 ps01 = __fadd2_rn(ps[0], ps[1]), ps23 = __fadd2_rn(ps[2], ps[3]);
+                            const float2 pst = __fadd2_rn(ps01, ps23);
+                            l_run += pst.x + pst.y;
+                            tc::fence_before_sync();
                         }
                     }
                 } else if (warp_live) {
@@ -1650,9 +1650,9 @@ __device__ __forceinline__ float split_q_row(const uint4& raw, uint2& hi, uint2&
             float x[8];
             widen_chunk<BF16>(raw, x);
             float top = 0.f;
-    #pragma unroll
+#pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-    #pragma unroll
+#pragma unroll
             for (int o = kLanes / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             int ex = 0;
             if (top > 0.f && top < INFINITY) {
@@ -1662,7 +1662,7 @@ __device__ __forceinline__ float split_q_row(const uint4& raw, uint2& hi, uint2&
             }
             const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
             uint32_t h[2] = {}, w[2] = {};
-    #pragma unroll
+#pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float a = x[e] * up, c = x[e + 1] * up;
                 // the format has no infinities: they count as NaN here, as q K^T of one would be
