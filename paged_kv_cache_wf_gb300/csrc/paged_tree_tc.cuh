@@ -53,11 +53,11 @@
 //   - Half tiles (row blocks of more than 32 rows).  A step takes 64 positions: S of the second half runs
 //     while the first is worked on, and S of the next tile's first half as soon as P V has read its
 //     columns, so a stream waits for S 300 clocks a half instead of 2000 a tile.  Eight prompts of
-//     128-2048 tokens: 194 us plain, 214 with a bias, 277 capped, 321 capped and biased (96 us of products at
-//     the bf16 rate); a capped half step takes 2400 clocks.
+//     128-2048 tokens: 194 us plain, 215 with a bias, 266 capped, 311 capped and biased (96 us of products at
+//     the bf16 rate); a capped half step takes about 2300 clocks.
 //   - Spread (at most 32 rows).  The rows stand in all four quarters of the query tile and each quarter's
 //     warp takes a quarter of a tile's positions, so eight warps share what one warp a stream had: 231 capped
-//     decodes 266 us (252 at the copy peak; 393 before).  The quarters' sums and outputs are joined at a piece's end.
+//     decodes 260-266 us (252 at the copy peak; 393 before).  The quarters' sums and outputs are joined at a piece's end.
 // Row blocks of fp8 pools stay at 128 rows or 32.  What is left: packed documents (200 us, 31 of products) spend half
 // of their time on their pieces' ends, 1.8 tiles a piece and stream; one user (10.6 us) is the start, one tile and the join.
 #pragma once
@@ -938,8 +938,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     };
                     if (nt > 0 && need(&k_full[kx], kpar)) {
                         tc::fence_after_sync();
-                        issue_s(0, false);
-                        issue_s(1, nt == 1);
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) issue_s(h, h == 1 && nt == 1);
                         next_k();
                     }
 #pragma unroll 1
@@ -1589,8 +1589,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         continue;
                     }
                     __syncwarp();
+                    // (Rolled, as all that runs once a piece: the warps' loops and this share the instruction cache, and
+                    // capped prompts take 266 us instead of 277 with it and the first products of a piece unrolled.)
                     if (whole) {
-#pragma unroll 2
+#pragma unroll 1
                         for (int k = 0; k < 4; ++k) {           // 8 rows of 64 bytes a store
                             const int rr = k * 8 + (lane >> 2), cc = (lane & 3) * 2;
                             const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
@@ -1605,7 +1607,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     } else {
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < 8; ++k) {           // 4 rows of 128 bytes a store
                             const int rr = k * 4 + (lane >> 3), cc = lane & 7;
                             const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
