@@ -542,6 +542,8 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_drafts_ke
         Pair run = shfl_up(incl, 1);
         if (lane != owner) return;
         run = lane == 0 ? at_warp : at_warp + run;
+        // For the same reason the sum before this lane may pass the threshold already, though no place before it was
+        // found to: then it is the lane's first with a weight.
         int answer = -1;
         for (int k = 0; k < per; k += 4) {
             float2 hi[2], lo[2];
@@ -551,12 +553,13 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_drafts_ke
             for (int e = 0; e < 4; ++e) {
                 const float2 h = hi[e >> 1], l = lo[e >> 1];
                 const Pair w{(e & 1) ? h.y : h.x, (e & 1) ? l.y : l.x};
-                if (w.h > 0.f && !(threshold < run)) {
+                // (w.h is 0, or below it, where the rounded difference is and the rest is not)
+                if (w.h + w.l > 0.f && (answer < 0 || !(threshold < run))) {
                     answer = i + e;
                     run = run + w;
                 }
             }
-            if (threshold < run) break;
+            if (answer >= 0 && threshold < run) break;
         }
         p.next_tokens[b] = answer - r.lo;
         return;

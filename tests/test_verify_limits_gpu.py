@@ -1,0 +1,66 @@
+"""wf_verify_drafts where numbers lie next to their borders."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_wf_gb300 import binding as wf
+from tests.test_verify_gpu import single
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from paged_kv_cache_wf_gb300 import build
+    build.build()
+
+
+U = 2.0 ** -48     # a step of the smaller number in a sum's pair (1, 2^-25)
+
+
+def near(row, pick, x):
+    """Whether x has a weight and the threshold lies in its part of the running sum, up to 2^-44 of the whole."""
+    up = np.cumsum(np.asarray(row, np.longdouble))
+    at = np.longdouble(pick) * up[-1]
+    return row[x] > 0 and up[x] - row[x] <= at + up[-1] * 2.0 ** -44 and up[x] >= at - up[-1] * 2.0 ** -44
+
+
+def sparse(vocab, items):
+    row = np.zeros(vocab)
+    for x, w in items:
+        row[x] = np.float32(w)
+    return row
+
+
+HALF = [(0, 1), (1, 2.0 ** -25)]
+ROWS = {
+    # Weights of parts of a step, each lost where they are added one by one and not where they are added to one another
+    # first, and a tail that makes half of the whole one of the two sums.  Slices of 1024 tokens, four of them a lane:
+    # the second lane's sum is the larger one as the lanes add it up.
+    f"slices {a}": sparse(16384, HALF + [(4096, a * U), (5120, a * U), (6144, a * U), (8192, 1), (8193, 2.0 ** -25)])
+    for a in (0.3, 0.35, 0.4, 0.45)}
+# The same of lanes of four tokens with one that has no weight before the one that is looked in.
+for i, (parts, tail, more) in enumerate([((0.45, 0.3, 0.6, 0.7, 0.74), 28, 1), ((0.74, 0.4, 0.45, 0.45, 0.7, 0.6), 40, 3),
+                                         ((0.45, 0.6, 0.7), 20, 0), ((0.74, 0.4, 0.74, 0.3, 0.6, 0.74), 40, 2),
+                                         ((0.4, 0.3, 0.74, 0.4, 0.74), 36, 2)]):
+    ROWS[f"lanes {i}"] = sparse(200, HALF + [(4 * k + 4, a * U) for k, a in enumerate(parts)] +
+                                [(tail, 1), (tail + 1, 2.0 ** -25), (tail + 2, more * U)])
+
+
+@pytest.mark.parametrize("name", list(ROWS))
+def test_a_threshold_between_two_roundings_of_a_sum(name):
+    row = ROWS[name]
+    path, x, status = single([row.tolist()], None, [0], [-1], [0], 0.5)
+    assert (path, status) == ([0], 0) and 0 <= x < len(row) and near(row, 0.5, x), x
+
+
+@pytest.mark.parametrize("p0, p2, q0, q2", [
+    (0.4157509207725525, 0.8542814254760742, 0.3601817488670349, 0.7555696964263916),
+    (0.36879801750183105, 0.8342269659042358, 0.32532966136932373, 0.7440820932388306),
+    (0.45207345485687256, 0.8837578296661377, 0.3929266035556793, 0.7923756837844849)])
+def test_a_weight_that_is_only_a_rounding_error(p0, p2, q0, q2):
+    """Two rejected children leave p - c q, c = 1 + (p0 - q0) + (p2 - q2): above 0 for token 0 alone, by 2^-27 or so, where p0 is
+    the rounded product."""
+    p, q = [p0, 0.0, p2], [q0, 0.25, q2]
+    assert single([p] * 3, [q] * 3, [0, 1, 1], [-1, 0, 0], [0, 0.5, 0.5], 0.3) == ([0], 0, 0)
