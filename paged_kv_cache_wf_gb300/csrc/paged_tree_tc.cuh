@@ -338,6 +338,69 @@ __device__ __forceinline__ void bias_word(float (&s)[32], float scale, float slo
     }
 }
 
+// What infinities and NaN in 32 columns of V from `v` on (those of the pool's first row) add to a row that sees positions
+// [lo, hi) of a request: a bit a column where it is +infinity, one where it is -infinity, both for NaN.  All lanes of a
+// warp together, a row each; a lane looks at every 32nd position of all of them, and only where some element is not
+// finite do the rows look at the position.  (Each row by itself, an element at a time, took 32 loads a position, and a
+// context of some 10000 of them longer than the other warps' waits last.)  Positions in `skip` are left out.
+// Written to be short: the loops around it share the instruction cache.
+template <bool CODES>
+__device__ __forceinline__ uint2 wild_columns(const unsigned char* v, int64_t row, const int32_t* table, int P, int N, int lo,
+                                              int hi, int2 skip) {
+    constexpr int kWords = CODES ? 8 : 16;               // of 32 columns
+    const int lane = threadIdx.x & 31;
+    const int last = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
+    uint2 got = make_uint2(0u, 0u);
+#pragma unroll 1
+    for (int base = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX); base < last; base += 32) {
+        if (base >= skip.x && base + 32 <= skip.y) {
+            base = skip.y - 32;
+            continue;
+        }
+        uint32_t up = 0, down = 0;
+        const int at = base + lane;
+        const int blk = at < last && !(at >= skip.x && at < skip.y) ? __ldg(table + at / P) : -1;
+        if ((unsigned)blk < (unsigned)N) {
+            const uint32_t* from = reinterpret_cast<const uint32_t*>(v + ((int64_t)blk * P + at % P) * row);
+            uint32_t m = 0;
+#pragma unroll
+            for (int w = 0; w < kWords; w += 4) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + w));
+                if constexpr (CODES) {
+                    m |= nan_codes(x);
+                } else {
+                    const auto full = [](uint32_t y) { return (y & 0x7f807f80u) + 0x00800080u; };
+                    m |= (full(x.x) | full(x.y) | full(x.z) | full(x.w)) & 0x80008000u;
+                }
+            }
+            if (m != 0) {
+#pragma unroll 1
+                for (int e = 0; e < 32; ++e) {
+                    const uint32_t bit = 1u << e;
+                    if constexpr (CODES) {
+                        if ((reinterpret_cast<const unsigned char*>(from)[e] & 0x7f) == 0x7f) up |= bit;
+                    } else {
+                        const float x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(from)[e]);
+                        if (!(x < INFINITY)) up |= bit;
+                        if (!(x > -INFINITY)) down |= bit;
+                    }
+                }
+                if constexpr (CODES) down = up;
+            }
+        }
+#pragma unroll 1
+        for (unsigned m = __ballot_sync(0xffffffffu, (up | down) != 0); m != 0; m &= m - 1) {
+            const int j = __ffs(m) - 1;
+            const uint32_t u = __shfl_sync(0xffffffffu, up, j), d = __shfl_sync(0xffffffffu, down, j);
+            if (base + j >= lo && base + j < hi) {
+                got.x |= u;
+                got.y |= d;
+            }
+        }
+    }
+    return got;
+}
+
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -1504,30 +1567,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int e4 = 0; e4 < 8; ++e4)
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((e4 ^ (lane & 7)) << 4)) =
                             make_float4(o[e4 * 4], o[e4 * 4 + 1], o[e4 * 4 + 2], o[e4 * 4 + 3]);
-                    if (wild && row_valid && (!V::kSpread || quad == 0)) {
-                        // drafts whose V row is not finite: what was zeroed for P V, added to the
-                        // rows that see them
-                        int pos0, pos1;
-                        if constexpr (V::kScored) {
-                            pos0 = max(sees.x, at0 + j0 * TN);
-                            pos1 = min(sees.y, at0 + it.j1 * TN);
-                        } else {
-                            pos0 = max(c, j0 * TN);
-                            pos1 = min(c + n, it.j1 * TN);
+                    // drafts (scored: positions) whose V row is not finite: what was zeroed for P V, added to the rows
+                    // that see them
+                    if constexpr (V::kScored) {
+                        if (wild && (!V::kSpread || quad == 0)) {
+                            const int pos0 = row_valid ? max(sees.x, at0 + j0 * TN) : 0;
+                            const int pos1 = row_valid ? min(sees.y, at0 + it.j1 * TN) : 0;
+                            // (those that all rows see were not touched)
+                            constexpr int kElt = CODES ? 1 : 2;
+                            const uint2 got = wild_columns<CODES>(
+                                static_cast<const unsigned char*>(p.v_pool) + (h_of(it) * D + col) * kElt,
+                                (int64_t)p.H_kv * D * kElt, trow, p.P, p.N, pos0, pos1, full_of(it));
+#pragma unroll 1
+                            for (uint32_t m = got.x | got.y; m != 0; m &= m - 1) {
+                                const int e = __ffs(m) - 1;
+                                float* y = reinterpret_cast<float*>(stage + lane * 128 +
+                                                                    (((e >> 2) ^ (lane & 7)) << 4)) + (e & 3);
+                                *y += !((got.y >> e) & 1u) ? INFINITY : !((got.x >> e) & 1u) ? -INFINITY : NAN;
+                            }
                         }
+                    } else if (wild && row_valid) {
+                        const int pos0 = max(c, j0 * TN), pos1 = min(c + n, it.j1 * TN);
 #pragma unroll 1
                         for (int pos = pos0; pos < pos1; ++pos) {
-                            if constexpr (V::kScored) {
-                                if (pos >= full_of(it).x && pos < full_of(it).y) {   // these were not touched
-                                    pos = full_of(it).y - 1;
-                                    continue;
-                                }
-                            }
                             const int blk = __ldg(trow + pos / p.P);
                             if ((unsigned)blk >= (unsigned)p.N) continue;
-                            if constexpr (!V::kScored) {
-                                if (!tree_bit(p, q_row, pos - c)) continue;
-                            }
+                            if (!tree_bit(p, q_row, pos - c)) continue;
                             const int64_t slot = (int64_t)blk * p.P + pos % p.P;
                             const int64_t at = (slot * p.H_kv + h_of(it)) * D + col;
 #pragma unroll 1
