@@ -428,7 +428,9 @@ size_t wf_paged_scored_attention_workspace_size(int32_t B, int32_t num_q_heads, 
  * A row that sees nothing gives zeros.  Positions that a row does not see have no effect on it,
  * whatever their K and V rows hold (NaN and infinities included), and table entries of blocks before
  * the first position and behind the last one that any row of a request sees are not read: a window's
- * past may be given back.  Requests
+ * past may be given back.  An infinity in V that a row sees makes that column of it infinite, two of
+ * opposite signs or a NaN make it NaN; so may an infinity whose weight is below 2^-126 of the row's
+ * largest.  Requests
  * with n_b = 0 are no-ops.  A request whose n_b or length is out of range (WF_DEV_BAD_SEQLEN) is
  * skipped and its rows are left unwritten; positions of a block id out of range
  * (WF_DEV_BAD_BLOCK) are left out of the softmax.

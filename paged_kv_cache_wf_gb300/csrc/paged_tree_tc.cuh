@@ -346,7 +346,7 @@ __device__ __forceinline__ void bias_word(float (&s)[32], float scale, float slo
 // Written to be short: the loops around it share the instruction cache.
 template <bool CODES>
 __device__ __forceinline__ uint2 wild_columns(const unsigned char* v, int64_t row, const int32_t* table, int P, int N, int lo,
-                                              int hi, int2 skip) {
+                                              int hi, int2 skip = make_int2(0, 0)) {
     constexpr int kWords = CODES ? 8 : 16;               // of 32 columns
     const int lane = threadIdx.x & 31;
     const int last = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
@@ -1570,7 +1570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // drafts (scored: positions) whose V row is not finite: what was zeroed for P V, added to the rows
                     // that see them
                     if constexpr (V::kScored) {
-                        if (wild && (!V::kSpread || quad == 0)) {
+                        if (!V::kSpread && wild) {
                             const int pos0 = row_valid ? max(sees.x, at0 + j0 * TN) : 0;
                             const int pos1 = row_valid ? min(sees.y, at0 + it.j1 * TN) : 0;
                             // (those that all rows see were not touched)
@@ -1628,23 +1628,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                             return a;
                         };
-                        if (whole) {
-                            const int row = quad * 8 + (lane >> 2), cc = (lane & 3) * 2;
-                            const float4 a = sum_at(row, cc), b = sum_at(row, cc + 1);
-                            if (row < live_rows) {
+                        const int cc = lane & 7, row0 = quad * 8 + (lane >> 3);   // rows row0 and row0 + 4
+                        float4 a[2] = {sum_at(row0, cc), sum_at(row0 + 4, cc)};
+                        // An infinity (or NaN) in V that all rows see is NaN in the quarters that have a weight of 0 for it, and
+                        // one that not all see is not in the sums: what the row sees decides.
+                        const auto odd = [&](int k) {
+                            return row0 + 4 * k < live_rows &&
+                                   !((a[k].x - a[k].x) + (a[k].y - a[k].y) + (a[k].z - a[k].z) + (a[k].w - a[k].w) == 0.f);
+                        };
+                        if (__any_sync(0xffffffffu, odd(0) || odd(1) || wild)) {
+#pragma unroll 1
+                            for (int k = 0; k < 2; ++k) {
+                                const int row = row0 + 4 * k;
+                                const int pos0 = max(__shfl_sync(0xffffffffu, sees.x, row), at0 + j0 * TN);
+                                const int pos1 = min(__shfl_sync(0xffffffffu, sees.y, row), at0 + it.j1 * TN);
+                                const float l = __shfl_sync(0xffffffffu, l_run, row);
+                                constexpr int kElt = CODES ? 1 : 2;
+                                const uint2 got = wild_columns<CODES>(
+                                    static_cast<const unsigned char*>(p.v_pool) + (h_of(it) * D + col) * kElt,
+                                    (int64_t)p.H_kv * D * kElt, trow, p.P, p.N, pos0, row < live_rows ? pos1 : 0);
+                                const uint32_t up = got.x >> (4 * cc), down = got.y >> (4 * cc);
+                                const auto settle = [&](float y, int e) {
+                                    if (!(((up | down) >> e) & 1u) || l != l) return y;      // (of NaN among the scores all is NaN)
+                                    return !((down >> e) & 1u) ? INFINITY : !((up >> e) & 1u) ? -INFINITY : NAN;
+                                };
+                                float4 y = k == 0 ? a[0] : a[1];
+                                y = make_float4(settle(y.x, 0), settle(y.y, 1), settle(y.z, 2), settle(y.w, 3));
+                                if (k == 0)
+                                    a[0] = y;
+                                else
+                                    a[1] = y;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int row = row0 + 4 * k;
+                            if (row >= live_rows) continue;
+                            if (whole) {
                                 const int dr = (row * g_inv) >> 16;
                                 const int64_t at = (int64_t)(tile_row + dr) * p.H_q + h_of(it) * p.G + row - dr * p.G;
-                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at * D + col + cc * 4) =
-                                    make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
-                                               pack_bf16x2(b.z, b.w));
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int row = quad * 8 + k * 4 + (lane >> 3), cc = lane & 7;
-                                const float4 a = sum_at(row, cc);
-                                if (row < live_rows)
-                                    *reinterpret_cast<float4*>(p.ws_o + (wbase + row) * D + col + cc * 4) = a;
+                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D + col + cc * 4) =
+                                    make_uint2(pack_bf16x2(a[k].x, a[k].y), pack_bf16x2(a[k].z, a[k].w));
+                            } else {
+                                *reinterpret_cast<float4*>(p.ws_o + (wbase + row) * D + col + cc * 4) = a[k];
                             }
                         }
                         if (!meeting()) {

@@ -48,3 +48,40 @@ def test_a_long_context_without_a_position_that_all_rows_see(shape, where):
     got, want = d["out"].double().cpu().numpy(), clean["out"].double().cpu().numpy()
     want[::2, H_q - H_q // H_kv:, 5] = np.nan
     assert np.array_equal(got, want, equal_nan=True)
+
+
+# cached, new, H_q, H_kv, D, P: few rows a request (one to eight), and more
+SEEN = {"decode": ([700, 130, 257], [1, 1, 1], 8, 2, 128, 16), "decode d64": ([700, 130, 257], [1, 1, 1], 4, 4, 64, 16),
+        "decode group of 8": ([4000, 17], [1, 1], 16, 2, 128, 32), "few": ([600, 300], [8, 5], 8, 2, 128, 16),
+        "one tile": ([600, 300], [20, 9], 8, 2, 128, 16), "two tiles": ([600, 300], [70, 40], 8, 2, 64, 16),
+        "blocks of 7": ([300, 100], [1, 4], 8, 2, 128, 7)}
+SEEN_RULES = {"plain": dict(), "cap": dict(cap=5.0), "window": dict(window=200), "documents": dict(view="documents"),
+              "any": dict(view="any", cap=5.0)}
+
+
+@pytest.mark.parametrize("rule", list(SEEN_RULES))
+@pytest.mark.parametrize("shape", list(SEEN))
+def test_an_infinity_that_a_row_sees_makes_it_infinite(shape, rule):
+    """Whatever its weight, and whether all rows of a block see it or some: one of either sign in two columns, both signs
+    in a third, in the middle of the context."""
+    t = Scored(*SEEN[shape], "bf16", seed=7, **SEEN_RULES[rule])
+    clean = t.device()
+    t.run(clean, t.workspace())
+    d = t.device()
+    G = t.H_q // t.H_kv
+    want = clean["out"].double().cpu().numpy()
+    for b in range(t.B):
+        at = int(t.lens[b]) - int(t.drafted[b])
+        for p, col, value in ((at // 2, 3, np.inf), (max(at - 70, 0), 33, -np.inf), (at // 3, 40, np.inf), (at - 1, 40, -np.inf)):
+            if not t.seen(b)[p]:
+                continue
+            d["v"][int(t.table[b, p // t.P]), p % t.P, t.H_kv - 1, col] = float(value)
+            for i in range(int(t.drafted[b])):
+                lo, hi = t.range(b, i)
+                if lo <= p < hi:
+                    with np.errstate(invalid="ignore"):
+                        want[t.cu[b] + i, t.H_q - G:, col] += value
+    t.run(d, t.workspace())
+    assert wf.wf_device_status_fetch(d["status"]) == 0
+    assert np.array_equal(d["out"].double().cpu().numpy(), want, equal_nan=True)
+    assert np.isinf(want).any() or rule == "any"        # (single tokens see nothing in this view)
