@@ -411,7 +411,9 @@ size_t wf_paged_scored_attention_workspace_size(int32_t B, int32_t num_q_heads, 
  *   seq_lens   [B] int32: tokens of request b in the pool INCLUDING its n_b new ones, already
  *              written.  Row i is the token at position t = seq_lens[b] - n_b + i.
  *   scale      softmax scale; scale * log2(e) must be finite in float32
- *   cap        > 0: a score x = scale q.K_p becomes cap tanh(x / cap); 0: it stays
+ *   cap        > 0: a score x = scale q.K_p becomes cap tanh(x / cap); 0: it stays.  At most 2^100, and
+ *              scale / cap 0 or a normal float32.  On the tensor cores a capped score is off by up to
+ *              2^-17 of itself or, for caps up to 256, 2^-20 of the cap
  *   slopes     [H_q] float32 or NULL: then slopes[g] |t - p| is taken off it (any sign)
  *   window     > 0: position p is seen only if p > t - window; 0: no window
  *   row_ranges [T_total, 2] int32, 8-byte aligned, or NULL: row r sees the positions p with

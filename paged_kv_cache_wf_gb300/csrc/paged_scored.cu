@@ -311,7 +311,7 @@ cudaError_t launch_paged_scored(const ScoredArgs& a, const wf_pool_desc& pool, u
     p.window = a.window;
     p.cap_in = p.cap_out = 0.f;
     if (a.cap > 0.f) {
-        p.cap_in = tree_factor((float)((double)a.scale / (double)a.cap));
+        p.cap_in = (float)((double)a.scale / (double)a.cap);   // (may be 0: scores are masked behind the cap)
         p.cap_out = a.cap * kLog2e;
     }
     const bool tc = tree_tc_supported(pool, a.num_q_heads), codes = tc && pool.dtype == WF_DTYPE_FP8_E4M3;
@@ -340,10 +340,14 @@ cudaError_t launch_paged_scored(const ScoredArgs& a, const wf_pool_desc& pool, u
                              : launch_scored_cc<kRuleCap>(p, pool, ctas, stream)
                : bias ? launch_scored_cc<kRuleBias>(p, pool, ctas, stream)
                       : launch_scored_cc<kRulePlain>(p, pool, ctas, stream);
-    e = capped ? bias ? launch_scored_tc<kRuleCapBias>(p, pool, list.parts, ctas, stream)
-                      : launch_scored_tc<kRuleCap>(p, pool, list.parts, ctas, stream)
-        : bias ? launch_scored_tc<kRuleBias>(p, pool, list.parts, ctas, stream)
-               : launch_scored_tc<kRulePlain>(p, pool, list.parts, ctas, stream);
+    if (a.cap > kWideCap)
+        e = bias ? launch_scored_tc<kRuleWideBias>(p, pool, list.parts, ctas, stream)
+                 : launch_scored_tc<kRuleWide>(p, pool, list.parts, ctas, stream);
+    else
+        e = capped ? bias ? launch_scored_tc<kRuleCapBias>(p, pool, list.parts, ctas, stream)
+                          : launch_scored_tc<kRuleCap>(p, pool, list.parts, ctas, stream)
+            : bias ? launch_scored_tc<kRuleBias>(p, pool, list.parts, ctas, stream)
+                   : launch_scored_tc<kRulePlain>(p, pool, list.parts, ctas, stream);
     if (e != cudaSuccess || ctas == 1) return e;
     return tree_join(p, pool, ctas, stream);
 }

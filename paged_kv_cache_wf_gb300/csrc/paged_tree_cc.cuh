@@ -141,8 +141,7 @@ __global__ void __launch_bounds__(kCcThreads, cc_ctas_per_sm(E::kBytes, D, RPW))
             b = it.b;
         }
         float factor = p.scale_log2;
-        constexpr bool kCap = V::kRule == kRuleCap || V::kRule == kRuleCapBias;
-        constexpr bool kBias = V::kRule == kRuleBias || V::kRule == kRuleCapBias;
+        constexpr bool kCap = V::kCap, kBias = V::kBias;
         if constexpr (kCap) factor = p.cap_in;
         const float qscale = E::kBytes == 1 ? factor * sc.k[min(it.h, kMaxScaleHeads - 1)] : factor;
         const float vscale = E::kBytes == 1 ? sc.v[min(it.h, kMaxScaleHeads - 1)] : 1.f;

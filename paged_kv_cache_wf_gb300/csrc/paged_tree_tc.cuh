@@ -271,7 +271,8 @@ __device__ __forceinline__ float cap_out_of(const P& p) {
 
 // ---- scored calls: the scores of 32 positions of a row ----
 
-// tanh(t) of |t| <= kTanhNear as t times a polynomial of t^2, fitted here for the least largest error, 2^-20.1.
+// tanh(t) of |t| <= kTanhNear as t (1 + c1 t^2 + c2 t^4), fitted here for the least largest error relative to tanh, 2^-17.2, that
+// is below 2^-19.1 in itself.  The leading 1 keeps a score's error a part of the score however large its cap.
 // Most scores lie well inside their cap, and then a tile needs no other special function than its weights'
 // exponentials (eight prompts: 303 us with two more coefficients and a limit of 0.75, 343 with tanh =
 // 1 - 2 / (1 + 2^z) for all scores, and a reciprocal shared by four of them was slower still).
@@ -279,23 +280,26 @@ constexpr float kTanhNear = 0.38f;
 
 // cap_out tanh(k s) + add of two scores.
 struct Cap {
-    float k, z, out, c0, c1, c2;                 // z = 2 log2(e) k
+    float k, z, out, c1, c2;                     // z = 2 log2(e) k
     __device__ __forceinline__ Cap(float k_, float out_)
-        : k(k_), z(2.f * 1.4426950408889634f * k_), out(out_), c0(out_ * 0.99998426f), c1(out_ * -0.33244488f),
-          c2(out_ * 0.12068124f) {}
-    // (of -infinity, for k > 0: -infinity, as the last coefficient is positive)
+        : k(k_), z(2.f * 1.4426950408889634f * k_), out(out_), c1(out_ * -0.33284658f), c2(out_ * 0.12280992f) {}
     __device__ __forceinline__ float2 near(float2 s, float2 add) const {
         const float2 t = __fmul2_rn(s, make_float2(k, k)), w = __fmul2_rn(t, t);
         float2 y = __ffma2_rn(make_float2(c2, c2), w, make_float2(c1, c1));
-        y = __ffma2_rn(y, w, make_float2(c0, c0));
+        y = __ffma2_rn(y, w, make_float2(out, out));
         return __ffma2_rn(t, y, add);
     }
-    // off by 2^-20 of the cap or so: the exponential by 2^-22, the sum by 2^-24, the reciprocal by 2^-23, times 2
-    __device__ __forceinline__ float2 far(float2 s, float2 add) const {
+    // Off by 2^-20 of the cap or so: the exponential by 2^-22, the sum by 2^-24, the reciprocal by 2^-23, times 2.
+    __device__ __forceinline__ float2 far(float2 s) const {
         const float2 e = __fmul2_rn(s, make_float2(z, z));
         const float2 u = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.f, 1.f));
         const float2 v = make_float2(rcp_approx(u.x), rcp_approx(u.y));
-        return __ffma2_rn(v, make_float2(-2.f * out, -2.f * out), __fadd2_rn(add, make_float2(out, out)));
+        return __ffma2_rn(v, make_float2(-2.f * out, -2.f * out), make_float2(out, out));
+    }
+    // Each score in the form that is exact to a part of itself: 2^-20 of the cap is below 2^-18 of a score beyond kTanhNear.
+    __device__ __forceinline__ float2 either(float2 s) const {
+        const float2 a = near(s, make_float2(0.f, 0.f)), b = far(s), t = __fmul2_rn(s, make_float2(k, k));
+        return make_float2(fabsf(t.x) <= kTanhNear ? a.x : b.x, fabsf(t.y) <= kTanhNear ? a.y : b.y);
     }
 };
 
@@ -1121,8 +1125,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             return came;
         };
         const int g_inv = (65536 + p.G - 1) / p.G;       // row / G for rows below 128
-        constexpr bool kCap = V::kRule == kRuleCap || V::kRule == kRuleCapBias;
-        constexpr bool kBias = V::kRule == kRuleBias || V::kRule == kRuleCapBias;
+        constexpr bool kCap = V::kCap, kBias = V::kBias, kWide = V::kWide;
         float scale = kCap ? cap_in_of(p) : p.scale_log2;
         const bool negate = V::kRule == kRulePlain && p.scale_log2 < 0.f;
         int4 rec = make_int4(0, 0, 0, 0);
@@ -1176,8 +1179,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     row = (int64_t)q_row * p.H_q + h_of(it) * p.G + tr % p.G;
                 else
                     row = ((int64_t)it.b * p.max_q_len + it.tok0 + tok) * p.H_q + h_of(it) * p.G + tr % p.G;
-                const float factor = kCap ? cap_in_of(p) : p.scale_log2;
-                scale = tree_factor(factor * sc.k[hs] * (row_valid ? __ldcg(p.q_inv + row) : 1.f));
+                const float inv = row_valid ? __ldcg(p.q_inv + row) : 1.f;
+                scale = kCap ? cap_in_of(p) * sc.k[hs] * inv : tree_factor(p.scale_log2 * sc.k[hs] * inv);
                 v_scale = sc.v[hs];
             }
             float m_ref = -INFINITY, l_run = 0.f;
@@ -1267,7 +1270,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                         }
                                 };
                                 if (!near)
-                                    capped([&](float2 x, float2 none) { return cap.far(x, none); });
+                                    capped([&](float2 x, float2) { return kWide ? cap.either(x) : cap.far(x); });
                                 else if (kBias)
                                     capped([&](float2 x, float2 none) { return cap.near(x, none); });
                             }
@@ -1282,7 +1285,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     for (int e = 0; e < 32; ++e) s[w][e] = (seen[w] >> e) & 1u ? s[w][e] : fill;
                                 }
                             }
-                            if (V::kRule != kRuleCap || made) {
+                            if (!kCap || made) {
                                 top = -INFINITY;
                                 if (negate) {   // the largest scaled score is the smallest score's
                                     float no = 0.f;
@@ -1295,7 +1298,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                 }
                             }
                             float mt = V::kRule != kRulePlain ? top : negate ? low * scale : top * scale;
-                            if constexpr (V::kRule == kRuleCap) {
+                            if constexpr (kCap && !kBias) {
                                 // tanh keeps their order
                                 if (near) mt = cap.near(make_float2(top, top), make_float2(0.f, 0.f)).x;
                             }
@@ -1346,7 +1349,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             };
                             if constexpr (V::kRule == kRulePlain) {
                                 weigh([&](float2 x) { return __ffma2_rn(x, sc2, nm2); });
-                            } else if (V::kRule == kRuleCap && near) {
+                            } else if (kCap && !kBias && near) {
                                 weigh([&](float2 x) { return cap.near(x, nm2); });
                             } else {
                                 weigh([&](float2 x) { return __fadd2_rn(x, nm2); });

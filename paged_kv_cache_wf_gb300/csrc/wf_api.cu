@@ -2,6 +2,7 @@
 // launch), status mapping, and dispatch to the kernels' launchers.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -541,7 +542,12 @@ wf_status wf_paged_scored_attention(void* out, const void* q, const void* k_pool
     // the kernels take scores to powers of two: an infinite factor would make a score of 0 NaN
     constexpr float kLog2e = 1.4426950408889634f;
     if (!std::isfinite(scale * kLog2e) || !(cap >= 0.f) || !std::isfinite(cap * kLog2e)) return WF_ERR_INVALID_ARG;
-    if (cap > 0.f && !std::isfinite((float)(2.0 * kLog2e * (double)scale / (double)cap))) return WF_ERR_INVALID_ARG;
+    if (cap > 0.f) {
+        const double in = std::fabs((double)scale / (double)cap);
+        if (!std::isfinite((float)(2.0 * kLog2e * in))) return WF_ERR_INVALID_ARG;
+        // what is left of a score above this, or of its factor below that, is too little to tell scores apart by
+        if (cap > 0x1p100f || (in > 0.0 && in < (double)FLT_MIN)) return WF_ERR_INVALID_ARG;
+    }
     if (B == 0 || total_q == 0 || max_q_len == 0) return WF_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !cu_q_lens) return WF_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool)) return WF_ERR_INVALID_ARG;
