@@ -1683,10 +1683,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         continue;
                     }
                     __syncwarp();
-                    // (Rolled, as all that runs once a piece: the warps' loops and this share the instruction cache, and
-                    // capped prompts take 266 us instead of 277 with it and the first products of a piece unrolled.)
+                    // Rolled where the warps' loops and this fill the instruction cache (capped prompts 266 us instead of 277,
+                    // with the first products of a piece; drafts over fp8 93.8 instead of 95.0).  Not for trees over bf16,
+                    // where the loads' and stores' latency shows (one request of 8 drafts 10.9 us, rolled 11.4; 32 requests
+                    // 33.8 and 34.0).
+                    constexpr bool kRolled = V::kScored || CODES;
+                    constexpr int kUnrollWhole = kRolled ? 1 : 2, kUnrollPiece = kRolled ? 1 : 8;
                     if (whole) {
-#pragma unroll 1
+#pragma unroll kUnrollWhole
                         for (int k = 0; k < 4; ++k) {           // 8 rows of 64 bytes a store
                             const int rr = k * 8 + (lane >> 2), cc = (lane & 3) * 2;
                             const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
@@ -1701,7 +1705,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     } else {
-#pragma unroll 1
+#pragma unroll kUnrollPiece
                         for (int k = 0; k < 8; ++k) {           // 4 rows of 128 bytes a store
                             const int rr = k * 4 + (lane >> 3), cc = lane & 7;
                             const float4 a = ld_shared_f4(stage + rr * 128 + ((cc ^ (rr & 7)) << 4));
