@@ -481,8 +481,10 @@ wf_status wf_paged_scored_attention(void* out, const void* q, const void* k_pool
  * path ends where no child is kept, or at max_accepted nodes (whose last has no children
  * tried).  The next token is the first x with w(0) + .. + w(x) > picks[b] sum w (w = p_u where
  * sum w is 0).  So the tokens are distributed as the target's own if the coins and picks are
- * independent and uniform, p and q sum to 1, and drawn children come from q.  Sums and
- * comparisons are exact to about 2^-46, so that a seed gives the same tokens anywhere.
+ * independent and uniform, p and q sum to 1, and drawn children come from q.  Sums carry about 46
+ * bits over usual vocabularies (2^-44 of a sum up to 2^18 tokens, 2^-36 at 2^28), so a seed gives the same
+ * tokens anywhere but where a number lies that close to a border: in which order a row is added up
+ * depends on the size of the batch.
  * Negative probabilities and NaN count as 0.
  * A request with n_b = 0 gets num_accepted 0 and next token -1.  One whose rows
  * (WF_DEV_BAD_SEQLEN), parents or tokens (WF_DEV_BAD_NODE), or pick (WF_DEV_BAD_PROBS) are out of

@@ -14,8 +14,11 @@
 // rejected tokens and N_k = 1 - their probabilities.  When no child is kept (or the path is
 // full) the next token is the first x whose running sum of w passes pick_b times the whole sum.
 //
-// Numbers are compared with borders that they may lie next to, so sums are exact to about 2^-46, in
-// pairs of fp32 numbers: products and differences with their rounding errors, and sums with theirs.
+// Numbers are compared with borders that they may lie next to, so sums are kept in pairs of fp32 numbers: products
+// and differences with their rounding errors, and sums with theirs.  Eight additions of a thread
+// lose 2^-42 of its sum at worst, so n of them n 2^-46 (their sum grows meanwhile): 2^-39 for 2^18 tokens in
+// clusters of 4, 2^-27 for 2^28 in one CTA.  The errors have both signs, and what is left is rather the square root
+// of that count: 2^-44 and 2^-38.
 // (In fp64, which this GPU has a 64th of its fp32 rate for, the sums over a warp's lanes alone took
 // longer than reading the rows: 64 trees 19 us instead of 12; now 10.8.)
 //
@@ -126,6 +129,14 @@ struct PairSum {
         const float2 y = __ffma2_rn(b, minus, hi);                           // what hi lost
         s = t;
         e = __fadd2_rn(e, __fadd2_rn(__fadd2_rn(x, y), lo));
+    }
+    // The errors into the sum, so that their own sum stays small beside it: left alone it grows with the tokens, and with it
+    // its rounding (2^17 equal tokens of one thread: off by 2^-22 of their sum).
+    __device__ __forceinline__ void fold() {
+        const float2 minus = make_float2(-1.f, -1.f);
+        const float2 t = __fadd2_rn(s, e);
+        e = __ffma2_rn(__ffma2_rn(s, minus, t), minus, e);
+        s = t;
     }
     __device__ __forceinline__ Pair value() const {
         return any_sum(s.x, s.y) + any_sum(e.x, e.y);
@@ -238,6 +249,7 @@ __device__ __forceinline__ Pair slice_sum(const Row& r, int first, int last, flo
                 weight<DRAWN>(make_float2(a[u][e], a[u][e + 1]), b2, ch, cl, hi, lo);
                 sum.add(hi, lo);
             }
+        sum.fold();
     }
     return sum.value();
 }
@@ -511,6 +523,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyPerSm) verify_drafts_ke
             weights(start + lane * per + k, hi, lo);
             part.add(hi[0], lo[0]);
             part.add(hi[1], lo[1]);
+            part.fold();
         }
         const Pair sum = part.value(), incl = lane_sums(sum);
         if (lane == 31) s_part[warp] = incl;

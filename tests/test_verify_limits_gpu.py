@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from paged_kv_cache_wf_gb300 import binding as wf
+from tests import _step as S
 from tests.test_verify_gpu import single
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +65,23 @@ def test_a_weight_that_is_only_a_rounding_error(p0, p2, q0, q2):
     the rounded product."""
     p, q = [p0, 0.0, p2], [q0, 0.25, q2]
     assert single([p] * 3, [q] * 3, [0, 1, 1], [-1, 0, 0], [0, 0.5, 0.5], 0.3) == ([0], 0, 0)
+
+
+@pytest.mark.parametrize("drawn", [False, True])
+@pytest.mark.parametrize("vocab, weight", [((1 << 26) - 5, 0.1), ((1 << 25) + 3, 0.7234567), ((1 << 26) - 64, 1 / 3)])
+def test_sums_of_many_equal_tokens(vocab, weight, drawn):
+    """One row of a long vocabulary in a batch that leaves it a single CTA: 2^17 and more tokens a thread, whose additions round
+    alike.  With equal weights the next token is floor(pick vocab); sums off by 2^-40 move that by 2^-14 of a token."""
+    B = 700
+    target = torch.full((1, vocab), weight, dtype=torch.float32, device="cuda")
+    draft = torch.zeros_like(target) if drawn else None
+    accepted, count, following = torch.full((B, 1), -5, dtype=torch.int32, device="cuda"), S.i32([-5] * B), S.i32([-5] * B)
+    for pick in (0.3, 0.41, 0.77, 0.93):
+        pick = float(np.float32(pick))
+        at = np.longdouble(pick) * vocab
+        assert 0.01 < at - np.floor(at) < 0.99
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        wf.wf_verify_drafts(accepted, count, following, target, draft, S.i32([0]), None, S.i32([0] * 70 + [1] * (B - 69)), 1,
+                            torch.zeros(1, device="cuda"), torch.full((B,), pick, device="cuda"), dev_status=st)
+        assert int(st.item()) == 0 and int(following[69].item()) == int(np.floor(at)), (pick, int(following[69].item()) - int(np.floor(at)))
+        assert following.sum().item() == int(np.floor(at)) - (B - 1) and count.sum().item() == 1
