@@ -85,3 +85,64 @@ def test_sums_of_many_equal_tokens(vocab, weight, drawn):
                             torch.zeros(1, device="cuda"), torch.full((B,), pick, device="cuda"), dev_status=st)
         assert int(st.item()) == 0 and int(following[69].item()) == int(np.floor(at)), (pick, int(following[69].item()) - int(np.floor(at)))
         assert following.sum().item() == int(np.floor(at)) - (B - 1) and count.sum().item() == 1
+
+
+class Rows:
+    """Trees over a long vocabulary, made on the GPU; `some` of the requests are looked at in float64."""
+
+    def __init__(self, B, vocab, drawn, probs, seed, some=10):
+        r = np.random.default_rng(seed)
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.B, self.drawn = B, drawn
+        self.nodes = r.integers(0, 4, B)
+        self.nodes[:some] = r.integers(3, 8, some)
+        self.cu = np.concatenate([[0], np.cumsum(self.nodes)])
+        T, kind = int(self.cu[-1]), torch.float32 if probs == "f32" else torch.bfloat16
+        self.target, self.draft = (torch.empty((T, vocab), dtype=kind, device="cuda") for _ in range(2))
+        for at in range(0, T, 64):
+            x = 2.5 * torch.randn((min(64, T - at), vocab), generator=gen, device="cuda")
+            self.target[at:at + 64] = torch.softmax(x, -1)
+            self.draft[at:at + 64] = torch.softmax(x + 1.2 * torch.randn(x.shape, generator=gen, device="cuda"), -1)
+        self.parents = np.array([-1 if i == 0 else r.integers(max(0, i - 3), i) for n in self.nodes for i in range(n)])
+        up = torch.from_numpy(np.repeat(self.cu[:-1], self.nodes) + np.maximum(self.parents, 0)).cuda()
+        rows = self.draft[up] if drawn else self.target[up]
+        self.tokens = torch.multinomial(rows.float(), 1, generator=gen)[:, 0].int()
+        self.coins, self.picks = r.random(T).astype(np.float32), r.random(B).astype(np.float32)
+        # (a draw that rounds up to 1 is none)
+        self.coins, self.picks = (np.minimum(x, np.float32(1 - 2.0 ** -24)) for x in (self.coins, self.picks))
+        self.some = np.concatenate([np.arange(some), r.integers(some, B, 4), [B - 1]])
+
+    def check(self):
+        depth = 8
+        accepted = torch.full((self.B, depth), -5, dtype=torch.int32, device="cuda")
+        count, following = S.i32([-5] * self.B), S.i32([-5] * self.B)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        draft = self.draft if self.drawn else None
+        wf.wf_verify_drafts(accepted, count, following, self.target, draft, self.tokens, S.i32(self.parents), S.i32(self.cu),
+                            int(self.nodes.max()), torch.from_numpy(self.coins).cuda(), torch.from_numpy(self.picks).cuda(),
+                            dev_status=st)
+        assert int(st.item()) == 0
+        path, count, following, tokens = (x.cpu().numpy() for x in (accepted, count, following, self.tokens))
+        rejected = 0
+        for b in self.some:
+            lo, hi = self.cu[b], self.cu[b + 1]
+            if lo == hi:
+                assert count[b] == 0 and following[b] == -1
+                continue
+            p, q = (x[lo:hi].double().cpu().numpy() for x in (self.target, self.draft))
+            want, x = S.verify(p, q if self.drawn else None, tokens[lo:hi], self.parents[lo:hi], self.coins[lo:hi].astype(float),
+                               float(self.picks[b]), depth)
+            assert list(path[b][:count[b]]) == want and (path[b][count[b]:] == -1).all() and following[b] == x, b
+            rejected += len(want) < hi - lo
+        assert rejected > 0
+        live = self.nodes > 0
+        assert (following[live] >= 0).all() and (following[live] < self.target.shape[1]).all() and (count[~live] == 0).all()
+
+
+# Clusters of 16, 8, 4, 2 CTAs and single ones, whose slices of a row are 1024 to 16384 tokens.
+@pytest.mark.parametrize("probs", ["f32", "bf16"])
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("B, vocab", [(19, 128000), (70, 100003), (160, 128000), (231, 100003), (300, 128000), (400, 100003),
+                                      (600, 128000), (700, 50257)])
+def test_batches_of_every_cluster_size(B, vocab, drawn, probs):
+    Rows(B, vocab, drawn, probs, seed=B + vocab).check()
