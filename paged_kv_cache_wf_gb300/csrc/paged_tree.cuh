@@ -47,7 +47,7 @@ struct TreeParams {
 
 // Scored attention (wf_paged_scored_attention) runs the same kernels over another list of units.
 // A row block there has the tiles [tile0, tile0 + nt) that some of its rows see, which a small
-// grid before the kernel works out (scored_blocks_kernel): with windows, documents and causal rows
+// grid before the kernel works out (scored_list_kernel): with windows, documents and causal rows
 // they differ from block to block, and with ranges they stand in device memory.
 struct ScoredBlock {
     int b, q_row, rows_tok, at;     // request, first row of q, rows (tokens), position of the first row

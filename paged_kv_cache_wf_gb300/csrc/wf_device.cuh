@@ -70,13 +70,13 @@ __device__ __forceinline__ void widen_chunk<BF16>(const uint4& c, float* f) {
     f[4] = d.x; f[5] = d.y; f[6] = e.x; f[7] = e.y;
 }
 
-// 2^x on the SFU (approximate, flushes denormals); 2^-inf = +0.
 // 1 / x (to the last bit or so; 1 / infinity is 0).
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^x on the SFU (approximate, flushes denormals); 2^-inf = +0.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -24,6 +24,10 @@ SHAPES = {
     "prompts d64": ([0, 40], [400, 90], 4, 4, 64, 16, "bf16"),
     "fp8 decode": ([64, 300, 1, 127], [1, 1, 1, 1], 8, 2, 128, 16, "fp8"),
     "fp8 prompts": ([64, 0], [140, 33], 8, 2, 128, 32, "fp8"),
+    "decode d64": ([1, 130, 127, 260], [1] * 4, 4, 4, 64, 16, "bf16"),
+    "few d64": ([30, 0, 20], [4, 16, 6], 10, 2, 64, 48, "bf16"),
+    "fp8 decode d64": ([64, 300, 1, 127], [1, 1, 1, 1], 8, 2, 64, 16, "fp8"),
+    "fp8 prompts d64": ([64, 0], [140, 33], 6, 2, 64, 16, "fp8"),
     "fp32 prompts": ([64, 0], [70, 101], 4, 2, 64, 16, "f32"),
 }
 
