@@ -346,28 +346,24 @@ __device__ __forceinline__ void bias_word(float (&s)[32], float scale, float slo
 // [lo, hi) of a request: a bit a column where it is +infinity, one where it is -infinity, both for NaN.  All lanes of a
 // warp together, a row each; a lane looks at every 32nd position of all of them, and only where some element is not
 // finite do the rows look at the position.  (Each row by itself, an element at a time, took 32 loads a position, and a
-// context of some 10000 of them longer than the other warps' waits last.)  Positions in `skip` are left out.
+// context of some 10000 of them longer than the other warps' waits last.)
 // Written to be short: the loops around it share the instruction cache.
 template <bool CODES>
 __device__ __forceinline__ uint2 wild_columns(const unsigned char* v, int64_t row, const int32_t* table, int P, int N, int lo,
-                                              int hi, int2 skip = make_int2(0, 0)) {
+                                              int hi) {
     constexpr int kWords = CODES ? 8 : 16;               // of 32 columns
     const int lane = threadIdx.x & 31;
     const int last = __reduce_max_sync(0xffffffffu, lo < hi ? hi : 0);
     uint2 got = make_uint2(0u, 0u);
 #pragma unroll 1
     for (int base = __reduce_min_sync(0xffffffffu, lo < hi ? lo : INT32_MAX); base < last; base += 32) {
-        if (base >= skip.x && base + 32 <= skip.y) {
-            base = skip.y - 32;
-            continue;
-        }
         uint32_t up = 0, down = 0;
         const int at = base + lane;
-        const int blk = at < last && !(at >= skip.x && at < skip.y) ? __ldg(table + at / P) : -1;
+        const int blk = at < last ? __ldg(table + at / P) : -1;
         if ((unsigned)blk < (unsigned)N) {
             const uint32_t* from = reinterpret_cast<const uint32_t*>(v + ((int64_t)blk * P + at % P) * row);
             uint32_t m = 0;
-#pragma unroll
+#pragma unroll 1
             for (int w = 0; w < kWords; w += 4) {
                 const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + w));
                 if constexpr (CODES) {
@@ -1535,6 +1531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             w0 *= f;
             w1 *= f;
             constexpr int kParts = QT == 1 ? D / 64 : D / 32;      // 32-column groups of this warp
+            bool odd = false;                                      // spread: a sum that is not finite
             if (nt > 0 || QT == 1) {
 #pragma unroll 1
                 for (int part = 0; part < kParts; ++part) {
@@ -1570,44 +1567,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int e4 = 0; e4 < 8; ++e4)
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((e4 ^ (lane & 7)) << 4)) =
                             make_float4(o[e4 * 4], o[e4 * 4 + 1], o[e4 * 4 + 2], o[e4 * 4 + 3]);
-                    // drafts (scored: positions) whose V row is not finite: what was zeroed for P V, added to the rows
-                    // that see them
-                    if constexpr (V::kScored) {
-                        if (!V::kSpread && wild) {
-                            const int pos0 = row_valid ? max(sees.x, at0 + j0 * TN) : 0;
-                            const int pos1 = row_valid ? min(sees.y, at0 + it.j1 * TN) : 0;
-                            // (those that all rows see were not touched)
-                            constexpr int kElt = CODES ? 1 : 2;
-                            const uint2 got = wild_columns<CODES>(
-                                static_cast<const unsigned char*>(p.v_pool) + (h_of(it) * D + col) * kElt,
-                                (int64_t)p.H_kv * D * kElt, trow, p.P, p.N, pos0, pos1, full_of(it));
+                    // drafts whose V row is not finite: what was zeroed for P V, added to the rows that see them
+                    if constexpr (!V::kScored) {
+                        if (wild && row_valid) {
+                            const int pos0 = max(c, j0 * TN), pos1 = min(c + n, it.j1 * TN);
 #pragma unroll 1
-                            for (uint32_t m = got.x | got.y; m != 0; m &= m - 1) {
-                                const int e = __ffs(m) - 1;
-                                float* y = reinterpret_cast<float*>(stage + lane * 128 +
-                                                                    (((e >> 2) ^ (lane & 7)) << 4)) + (e & 3);
-                                *y += !((got.y >> e) & 1u) ? INFINITY : !((got.x >> e) & 1u) ? -INFINITY : NAN;
-                            }
-                        }
-                    } else if (wild && row_valid) {
-                        const int pos0 = max(c, j0 * TN), pos1 = min(c + n, it.j1 * TN);
+                            for (int pos = pos0; pos < pos1; ++pos) {
+                                const int blk = __ldg(trow + pos / p.P);
+                                if ((unsigned)blk >= (unsigned)p.N) continue;
+                                if (!tree_bit(p, q_row, pos - c)) continue;
+                                const int64_t slot = (int64_t)blk * p.P + pos % p.P;
+                                const int64_t at = (slot * p.H_kv + h_of(it)) * D + col;
 #pragma unroll 1
-                        for (int pos = pos0; pos < pos1; ++pos) {
-                            const int blk = __ldg(trow + pos / p.P);
-                            if ((unsigned)blk >= (unsigned)p.N) continue;
-                            if (!tree_bit(p, q_row, pos - c)) continue;
-                            const int64_t slot = (int64_t)blk * p.P + pos % p.P;
-                            const int64_t at = (slot * p.H_kv + h_of(it)) * D + col;
-#pragma unroll 1
-                            for (int e = 0; e < 32; ++e) {
-                                float x;
-                                if constexpr (CODES)
-                                    x = (static_cast<const unsigned char*>(p.v_pool)[at + e] & 0x7f) == 0x7f ? NAN : 0.f;
-                                else
-                                    x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pool)[at + e]);
-                                float* y = reinterpret_cast<float*>(stage + lane * 128 +
-                                                                    (((e >> 2) ^ (lane & 7)) << 4)) + (e & 3);
-                                if (!(fabsf(x) < INFINITY)) *y += x;
+                                for (int e = 0; e < 32; ++e) {
+                                    float x;
+                                    if constexpr (CODES)
+                                        x = (static_cast<const unsigned char*>(p.v_pool)[at + e] & 0x7f) == 0x7f ? NAN : 0.f;
+                                    else
+                                        x = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pool)[at + e]);
+                                    float* y = reinterpret_cast<float*>(stage + lane * 128 +
+                                                                        (((e >> 2) ^ (lane & 7)) << 4)) + (e & 3);
+                                    if (!(fabsf(x) < INFINITY)) *y += x;
+                                }
                             }
                         }
                     }
@@ -1631,49 +1612,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                             return a;
                         };
-                        const int cc = lane & 7, row0 = quad * 8 + (lane >> 3);   // rows row0 and row0 + 4
-                        float4 a[2] = {sum_at(row0, cc), sum_at(row0 + 4, cc)};
-                        // An infinity (or NaN) in V that all rows see is NaN in the quarters that have a weight of 0 for it, and
-                        // one that not all see is not in the sums: what the row sees decides.
-                        const auto odd = [&](int k) {
-                            return row0 + 4 * k < live_rows &&
-                                   !((a[k].x - a[k].x) + (a[k].y - a[k].y) + (a[k].z - a[k].z) + (a[k].w - a[k].w) == 0.f);
+                        const auto finite = [](const float4& y) {
+                            return (y.x - y.x) + (y.y - y.y) + (y.z - y.z) + (y.w - y.w) == 0.f;
                         };
-                        if (__any_sync(0xffffffffu, odd(0) || odd(1) || wild)) {
-#pragma unroll 1
-                            for (int k = 0; k < 2; ++k) {
-                                const int row = row0 + 4 * k;
-                                const int pos0 = max(__shfl_sync(0xffffffffu, sees.x, row), at0 + j0 * TN);
-                                const int pos1 = min(__shfl_sync(0xffffffffu, sees.y, row), at0 + it.j1 * TN);
-                                const float l = __shfl_sync(0xffffffffu, l_run, row);
-                                constexpr int kElt = CODES ? 1 : 2;
-                                const uint2 got = wild_columns<CODES>(
-                                    static_cast<const unsigned char*>(p.v_pool) + (h_of(it) * D + col) * kElt,
-                                    (int64_t)p.H_kv * D * kElt, trow, p.P, p.N, pos0, row < live_rows ? pos1 : 0);
-                                const uint32_t up = got.x >> (4 * cc), down = got.y >> (4 * cc);
-                                const auto settle = [&](float y, int e) {
-                                    if (!(((up | down) >> e) & 1u) || l != l) return y;      // (of NaN among the scores all is NaN)
-                                    return !((down >> e) & 1u) ? INFINITY : !((up >> e) & 1u) ? -INFINITY : NAN;
-                                };
-                                float4 y = k == 0 ? a[0] : a[1];
-                                y = make_float4(settle(y.x, 0), settle(y.y, 1), settle(y.z, 2), settle(y.w, 3));
-                                if (k == 0)
-                                    a[0] = y;
-                                else
-                                    a[1] = y;
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int row = row0 + 4 * k;
-                            if (row >= live_rows) continue;
-                            if (whole) {
+                        if (whole) {
+                            const int row = quad * 8 + (lane >> 2), cc = (lane & 3) * 2;
+                            const float4 a = sum_at(row, cc), b = sum_at(row, cc + 1);
+                            if (row < live_rows) {
+                                odd |= !finite(a) || !finite(b);
                                 const int dr = (row * g_inv) >> 16;
                                 const int64_t at = (int64_t)(tile_row + dr) * p.H_q + h_of(it) * p.G + row - dr * p.G;
-                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D + col + cc * 4) =
-                                    make_uint2(pack_bf16x2(a[k].x, a[k].y), pack_bf16x2(a[k].z, a[k].w));
-                            } else {
-                                *reinterpret_cast<float4*>(p.ws_o + (wbase + row) * D + col + cc * 4) = a[k];
+                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at * D + col + cc * 4) =
+                                    make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                                               pack_bf16x2(b.z, b.w));
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int row = quad * 8 + k * 4 + (lane >> 3), cc = lane & 7;
+                                const float4 a = sum_at(row, cc);
+                                if (row < live_rows) {
+                                    odd |= !finite(a);
+                                    *reinterpret_cast<float4*>(p.ws_o + (wbase + row) * D + col + cc * 4) = a;
+                                }
                             }
                         }
                         if (!meeting()) {
@@ -1718,6 +1679,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (!ok) break;
+            if constexpr (V::kScored) {
+                // Elements of V that are not finite: what a row sees of them decides its columns, over what is stored.  (They
+                // were zeroed for P V unless all rows see them, and then an infinity is NaN in the quarters that have a weight
+                // of 0 for it; fp8 codes have no infinities.)  Spread: lane k < 8 has row quad * 8 + k.
+                if (__any_sync(0xffffffffu, wild || (!CODES && odd)) && warp_live) {
+                    const int row = V::kSpread ? quad * 8 + (lane & 7) : r;
+                    int2 at = sees;
+                    float l = l_run;
+                    if constexpr (V::kSpread) {
+                        at = make_int2(__shfl_sync(0xffffffffu, sees.x, row), __shfl_sync(0xffffffffu, sees.y, row));
+                        l = __shfl_sync(0xffffffffu, l_run, row);
+                    }
+                    at.x = max(at.x, at0 + j0 * TN);
+                    at.y = row < live_rows ? min(at.y, at0 + it.j1 * TN) : 0;
+                    const int dr = (row * g_inv) >> 16;
+                    const int64_t out_row = (int64_t)(tile_row + dr) * p.H_q + h_of(it) * p.G + row - dr * p.G;
+                    __syncwarp();                                  // other lanes stored this row
+#pragma unroll 1
+                    for (int part = 0; part < kParts; ++part) {
+                        const int col = (QT == 1 ? t * (D / 2) : 0) + part * 32;
+                        constexpr int kElt = CODES ? 1 : 2;
+                        const uint2 got = wild_columns<CODES>(
+                            static_cast<const unsigned char*>(p.v_pool) + (h_of(it) * D + col) * kElt,
+                            (int64_t)p.H_kv * D * kElt, trow, p.P, p.N, at.x, at.y);
+                        if (!(l == l) || (V::kSpread && lane >= 8)) continue;      // (of NaN among the scores all is NaN)
+#pragma unroll 1
+                        for (uint32_t m = got.x | got.y; m != 0; m &= m - 1) {
+                            const int e = __ffs(m) - 1;
+                            const float y = !((got.y >> e) & 1u) ? INFINITY : !((got.x >> e) & 1u) ? -INFINITY : NAN;
+                            if (whole)
+                                static_cast<__nv_bfloat16*>(p.out)[out_row * D + col + e] = __float2bfloat16(y);
+                            else
+                                p.ws_o[(wbase + row) * D + col + e] = y;
+                        }
+                    }
+                }
+            }
             // O (and the streams' sums) are read: the next piece may overwrite them
             tc::fence_before_sync();
             if constexpr (QT == 1) {
