@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from paged_kv_cache_wf_gb300 import binding as wf
+from tests import _draft as R
 from tests._scored import Scored
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +86,17 @@ def test_an_infinity_that_a_row_sees_makes_it_infinite(shape, rule):
     assert wf.wf_device_status_fetch(d["status"]) == 0
     assert np.array_equal(d["out"].double().cpu().numpy(), want, equal_nan=True)
     assert np.isinf(want).any() or rule == "any"        # (single tokens see nothing in this view)
+
+
+@pytest.mark.parametrize("rule", ["plain", "cap", "window"])
+@pytest.mark.parametrize("shape", ["decode", "decode d64", "few", "one tile", "two tiles", "blocks of 7"])
+def test_values_at_the_end_of_their_range(shape, rule):
+    """Normal values times 2^90 and scores far apart: sums over 700 positions stay below 2^104."""
+    t = Scored(*SEEN[shape], "bf16", seed=8, q_size=8.0, **SEEN_RULES[rule])
+    t.v *= 2.0 ** 90
+    t.v[torch.isnan(t.v)] = 0                            # (rows that nobody sees)
+    assert float(t.v.abs().max()) < 2.0 ** 94
+    d = t.device()
+    t.run(d, t.workspace())
+    R.check(t, d["out"])
+    assert wf.wf_device_status_fetch(d["status"]) == 0
