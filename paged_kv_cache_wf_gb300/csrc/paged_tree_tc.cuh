@@ -1645,11 +1645,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     __syncwarp();
                     // Rolled where the warps' loops and this fill the instruction cache (capped prompts 266 us instead of 277,
-                    // with the first products of a piece; drafts over fp8 93.8 instead of 95.0).  Not for trees over bf16,
-                    // where the loads' and stores' latency shows (one request of 8 drafts 10.9 us, rolled 11.4; 32 requests
-                    // 33.8 and 34.0).
-                    constexpr bool kRolled = V::kScored || CODES;
-                    constexpr int kUnrollWhole = kRolled ? 1 : 2, kUnrollPiece = kRolled ? 1 : 8;
+                    // with the first products of a piece).  Trees show the loads' and stores' latency: one request of 8 drafts
+                    // 10.9 us, rolled 11.4 (over fp8 12.3 unrolled, 12.4 by fours, 12.8 rolled; 64 requests there 95.0, 94.0, 93.7).
+                    constexpr int kUnrollWhole = V::kScored || CODES ? 1 : 2, kUnrollPiece = V::kScored ? 1 : CODES ? 4 : 8;
                     if (whole) {
 #pragma unroll kUnrollWhole
                         for (int k = 0; k < 4; ++k) {           // 8 rows of 64 bytes a store
