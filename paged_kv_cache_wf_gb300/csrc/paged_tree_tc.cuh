@@ -17,10 +17,10 @@
 //   QT = 2  (up to 256 rows a unit): one 128-row query tile each, on the same tiles, so
 //           a loaded tile serves 256 rows.
 // Device time of a call in a graph of many (issued one by one a call takes 1-2 us more, the widest
-// 10-15), and of its bytes at the copy peak: 32 requests of 1-16 drafts 34.2
-// and 18.1 us, 118 of 33-61 drafts (QT = 2) 272-280 and 190 us, 64 of 3-13 drafts of 64-wide heads
-// 40.4 and 15.5 us, 64 of 8-24 drafts over fp8 96.3 and 37.0 us (64-wide 73 and 18.5 us), 118 of
-// 33-61 drafts over fp8 409 and 118 us (64-wide 291 and 59 us); one request of 8 drafts 11.0 us.
+// 8-15), and of its bytes at the copy peak: 32 requests of 1-16 drafts 33.9
+// and 18.1 us, 118 of 33-61 drafts (QT = 2) 273-280 and 190 us, 64 of 3-13 drafts of 64-wide heads
+// 40.3 and 15.5 us, 64 of 8-24 drafts over fp8 94.0 and 37.0 us (64-wide 72 and 18.5 us), 118 of
+// 33-61 drafts over fp8 405 and 118 us (64-wide 290 and 59 us); one request of 8 drafts 11.0 us.
 // What is left: 5 us from launch to the first product (division of the work, first block ids,
 // first tiles, cold code); 2-5 us around every piece's end, where its streams wait for one
 // another and O is joined; 2-10 us of the join; and with long pieces the chain S -> softmax ->
@@ -32,7 +32,8 @@
 // The finish of a V tile: a weight of 0 hides a position only from finite values (0 *
 // NaN is NaN in P V).  Rows past the request's end or of a bad block are zeroed; an
 // element of a draft's row that is not finite is zeroed too, and the epilogue adds it
-// to the rows that see the draft.  Only tiles that reach the drafts are looked at.
+// to the rows that see the draft.  Only tiles that reach the drafts are looked at (scored: tiles that
+// some row does not see whole).
 //
 // fp8 pools (CODES; QT = 1, see tree_tc_shape).  S takes the K codes as they are (e4m3 x e4m3 ->
 // fp32): a small grid before this one splits every q row, scaled by a power of two so
@@ -53,13 +54,13 @@
 //   - Half tiles (row blocks of more than 32 rows).  A step takes 64 positions: S of the second half runs
 //     while the first is worked on, and S of the next tile's first half as soon as P V has read its
 //     columns, so a stream waits for S 300 clocks a half instead of 2000 a tile.  Eight prompts of
-//     128-2048 tokens: 194 us plain, 215 with a bias, 266 capped, 311 capped and biased (96 us of products at
+//     128-2048 tokens: 194 us plain, 215 with a bias, 261 capped, 311 capped and biased (96 us of products at
 //     the bf16 rate); a capped half step takes about 2300 clocks.
 //   - Spread (at most 32 rows).  The rows stand in all four quarters of the query tile and each quarter's
 //     warp takes a quarter of a tile's positions, so eight warps share what one warp a stream had: 231 capped
-//     decodes 260-266 us (252 at the copy peak; 393 before).  The quarters' sums and outputs are joined at a piece's end.
+//     decodes 260-267 us (252 at the copy peak; 393 before).  The quarters' sums and outputs are joined at a piece's end.
 // Row blocks of fp8 pools stay at 128 rows or 32.  What is left: packed documents (200 us, 31 of products) spend half
-// of their time on their pieces' ends, 1.8 tiles a piece and stream; one user (10.6 us) is the start, one tile and the join.
+// of their time on their pieces' ends, 1.8 tiles a piece and stream; one user (10.9 us) is the start, one tile and the join.
 #pragma once
 
 #include <cuda.h>

@@ -12,8 +12,8 @@
 //
 // Bound: latency.  The bytes are 12 a token and a few a request; what the call takes is a launch
 // and three dependent rounds of loads (lengths; tail block or free list; the same again for a
-// token): a step of 231 decodes 4.0 us, one of 8 prompts and 120 others (8300 rows) 6.5, a trim of one
-// request 2.6, of 231 (14 of them whole) 4.5.  One cluster does all of it: every CTA sums over all requests by itself (that takes
+// token): a step of 231 decodes 4.4 us, one of 8 prompts and 120 others (8300 rows) 6.7, a trim of one
+// request 2.6, of 231 (14 of them whole) 4.6.  One cluster does all of it: every CTA sums over all requests by itself (that takes
 // less than handing the sums on), and a cluster barrier stands between the last read of the
 // lengths and counts and the first write, so that both may be updated in place.
 #include <cooperative_groups.h>

@@ -20,7 +20,7 @@
 // clusters of 4, 2^-27 for 2^28 in one CTA.  The errors have both signs, and what is left is rather the square root
 // of that count: 2^-44 and 2^-38.
 // (In fp64, which this GPU has a 64th of its fp32 rate for, the sums over a warp's lanes alone took
-// longer than reading the rows: 64 trees 19 us instead of 12; now 10.8.)
+// longer than reading the rows: 64 trees 19 us instead of 12; now 10.9.)
 //
 // Bound: HBM, one or two rows of the vocabulary a request.  A cluster takes a request; every CTA
 // walks the tree by itself on the gathered p_u(x), q_u(x) of all nodes and reads its part of a row
